@@ -28,3 +28,9 @@ from ._lib import (  # noqa: F401
     workspace_bytes,
 )
 from .build import build  # noqa: F401
+from .experts import (  # noqa: F401
+    moe_layer,
+    moe_layer_workspace_bytes,
+    muon_update,
+    muon_update_workspace_bytes,
+)

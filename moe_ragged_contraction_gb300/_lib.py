@@ -87,6 +87,21 @@ def load() -> ctypes.CDLL:
         lib.mxfp8_wgrad_tile_config.restype = I
         lib.mxfp8_grouped_gemm_tile_config.argtypes = [I, I, I, L, IP, IP, IP]
         lib.mxfp8_grouped_gemm_tile_config.restype = I
+        F = ctypes.c_float
+        moe = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, P, P]
+        lib.mxfp8_moe_layer.argtypes = moe + [P]
+        lib.mxfp8_moe_layer.restype = I
+        lib.mxfp8_moe_layer_ws.argtypes = moe + [P, Z, P]
+        lib.mxfp8_moe_layer_ws.restype = I
+        lib.mxfp8_moe_layer_workspace_bytes.argtypes = [I] * 6
+        lib.mxfp8_moe_layer_workspace_bytes.restype = Z
+        muon = [P, I, P, I, I, I, F, I, I, F, F, F, F, P]
+        lib.mxfp8_muon_update.argtypes = muon + [P]
+        lib.mxfp8_muon_update.restype = I
+        lib.mxfp8_muon_update_ws.argtypes = muon + [P, Z, P]
+        lib.mxfp8_muon_update_ws.restype = I
+        lib.mxfp8_muon_update_workspace_bytes.argtypes = [I] * 3
+        lib.mxfp8_muon_update_workspace_bytes.restype = Z
         _lib = lib
         return lib
 

@@ -410,6 +410,47 @@ int run(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB
 
 int mxw::set_last_error(int code, const char* msg) { return fail(code, "%s", msg); }
 
+int mxw::host_fail(int code, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return code;
+}
+
+int mxw::host_device(int* dev, int* sms) {
+    DeviceInfo info;
+    const int rc = current_device(dev, &info);
+    if (rc == MXFP8_OK) *sms = info.sms;
+    return rc;
+}
+
+int mxw::host_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
+    return cached_workspace(dev, stream, need, out);
+}
+
+uint64_t mxw::host_wait_limit_ns() { return wait_limit_ns(); }
+
+int mxw::host_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                         const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    const int rc = get_encoder(&enc);
+    if (rc) return rc;
+    cuuint64_t d[5], st[5];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    const CUresult r = enc(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MXFP8_ECUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return MXFP8_OK;
+}
+
 extern "C" {
 
 int mxfp8_wgrad_grouped(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB,

@@ -144,4 +144,19 @@ cudaError_t set_suspend_hint(uint32_t ns);
 // Device status word (MXFP8_DEV_* bits).
 cudaError_t read_device_status(int32_t* status, int clear);
 
+// Device address of the status word on the current device, for kernels of
+// other translation units.
+cudaError_t device_status_address(int** addr);
+
+// Host services of abi.cu shared by the other entry points: sets the message
+// of mxfp8_last_error() and returns `code`; checks the current device (sm_103)
+// and reports its index and SM count; scratch from the per-(device, stream)
+// cache; the limit of the kernels' waits; the tensor-map encoder.
+int host_fail(int code, const char* fmt, ...);
+int host_device(int* dev, int* sms);
+int host_workspace(int dev, cudaStream_t stream, size_t need, void** out);
+uint64_t host_wait_limit_ns();
+int host_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
+
 }  // namespace mxw

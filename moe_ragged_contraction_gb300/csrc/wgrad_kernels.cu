@@ -1911,6 +1911,13 @@ cudaError_t launch_gemm(const GemmArgs& a, const CUtensorMap* maps, const char**
 
 cudaError_t set_suspend_hint(uint32_t ns) { return cudaMemcpyToSymbol(g_suspend_ns, &ns, sizeof(ns)); }
 
+cudaError_t device_status_address(int** addr) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_device_status);
+    *addr = static_cast<int*>(p);
+    return e;
+}
+
 cudaError_t read_device_status(int32_t* status, int clear) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return e;
