@@ -1,25 +1,87 @@
 // A whole mixture-of-experts layer for a few tokens (mxfp8_moe_layer): router,
 // choice of experts, gated MLPs on MXFP8 weights, weighted sum.
+//
+// The layer reads each chosen expert's weights once and does little with them
+// (2 x tokens multiply-adds per weight byte), so it is bound by HBM: the design
+// keeps one stream of weights running through every SM from the routing to the
+// last product. The weights go straight from HBM to the tensor cores: TMA puts
+// E4M3 tiles of 128 rows x 128 columns into shared memory and the block-scaled
+// tcgen05 MMA multiplies them with their E8M0 scales, so no thread touches a
+// weight. The tokens are the N side of the MMA (16 .. 256 columns). The
+// activations keep their precision as two E4M3 pieces per value, each 32-block
+// of a piece with its own power-of-two scale (two columns per token): a bf16
+// value has 8 significant bits and each piece holds 4, so x is represented
+// exactly down to 2^-17 of its block's largest value, and the fp32 inner
+// activations h to about 9 bits.
+//
+// Two kernels per call:
+//   moe_logits  : router logits (partial sums over slices of H), x as pieces,
+//                 counters to zero.
+//   moe_experts : persistent, one CTA per SM (cooperative launch; a programmatic
+//                 dependent of moe_logits). Chooses the experts, then walks two
+//                 phases without a pause in the weight stream: up/gate tiles
+//                 (64 gate and the same 64 up rows, h = silu(g) u on drain) and
+//                 down tiles (128 rows). Each phase's (expert, tile, K-step)
+//                 sequence is cut into equal contiguous shares, one per CTA; a
+//                 tile cut between CTAs is summed from their partial sums in a
+//                 fixed order (no atomics on data: bit-reproducible). The
+//                 weight producer runs ahead across the phase border while the
+//                 activation loader waits for the expert's h. Last, after a grid
+//                 barrier, the weighted sum over each token's experts.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "mxw_experts.h"
 #include "mxw_internal.h"
+#include "mxw_ptx_single.cuh"
 #include "../../include/mxfp8_experts.h"
 
 namespace mxw {
 namespace {
 
+constexpr int PIECES = 2;            // E4M3 pieces per activation
+constexpr int STEP = 128;            // columns of a K-step
+constexpr int TILE = 128;            // weight rows of a tile
+constexpr int A_BYTES = TILE * STEP;
+constexpr int MAX_ST = 12;           // pipeline stages
+constexpr int THREADS = 256;         // weight producer, MMA issuer, 2 loaders, 4 epilogue warps
+constexpr int SMEM_MAX = 232448;
+constexpr int LAG = 3;               // K-steps a loader keeps in flight
+constexpr uint32_t TMEM_ALL = 512;
+constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
+// kind::mxf8f6f4, E4M3 x E4M3, both K-major, E8M0 scales, M = 128
+constexpr uint32_t IDESC = (1u << 23) | (static_cast<uint32_t>(TILE >> 4) << 24);
+
+struct Params {
+    const uint16_t *x, *router;
+    const float* bias;
+    const uint8_t *s13, *s2;
+    int T, experts, first, local, H, I, top_k, score, renormalize;
+    float scale;
+    uint16_t* out;
+    int32_t* user_ids;
+    float* user_weights;
+    // scratch
+    unsigned int* counters;  // [0], [1] grid barriers; [2 ..] h tiles done per chosen expert; then arrivals per up/gate tile
+    float* logits;           // [ksplit][T][experts]
+    int32_t* ids;            // [T][top_k]
+    float* weights;
+    uint8_t *xq, *sx;        // [T][2][Hp], [T][2][Hp / 32]
+    uint8_t *hq, *sh;        // [slots][2][Ip], [slots][2][sh_stride]
+    float* y;                // [slots][Hp]
+    float *part_up, *part_down;  // [CTA][2][T][128]
+    int Hp, Ip, sh_stride, ksplit, slots, n_counters;
+    int up_tiles, down_tiles, up_steps, down_steps;
+    int raw;                 // scale rows not word-aligned (H or I no multiple of 128): scales through a raw buffer
+    uint32_t off_lists, off_epi, off_rows, off_ring;
+    unsigned long long wait_ns;
+    int* status;
+};
+
 __device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-
-__device__ __forceinline__ float e8m0_f(uint8_t s) {
-    return s == 255 ? CUDART_NAN_F : __uint_as_float(s == 0 ? 0x00400000u : static_cast<uint32_t>(s) << 23);
-}
-
-__device__ __forceinline__ float e4m3_f(uint8_t q) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -27,107 +89,899 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One block per token: logits, scores, the top-k (ties to the lower index).
-__global__ void __launch_bounds__(256) route_simple(const MoeArgs a, int32_t* ids, float* wts) {
-    __shared__ float score[MXFP8_MOE_MAX_EXPERTS];
-    __shared__ float key[MXFP8_MOE_MAX_EXPERTS];
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = warp; e < a.experts; e += 8) {
+// E8M0 scale of a block whose largest magnitude has the bits `amax`: the
+// smallest 2^e with amax <= 448 * 2^e (448 = 1.75 * 2^8); 255 for NaN / infinity.
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax) {
+    if (amax >= 0x7F800000u) return 255u;
+    const int s = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return static_cast<uint32_t>(s > 0 ? s : 0);
+}
+
+// One warp, one 32-block: lane l's value v as two E4M3 pieces (returned in the
+// low and second byte) and the pieces' scales s0, s1 (the same in all lanes).
+__device__ __forceinline__ uint32_t split_block(float v, uint32_t& s0, uint32_t& s1) {
+    s0 = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
+    if (s0 == 255u) {
+        s1 = 255u;
+        return 0x7F7Fu;
+    }
+    const float inv0 = __uint_as_float((254u - s0) << 23);
+    const __nv_fp8_storage_t q0 = __nv_cvt_float_to_fp8(v * inv0, __NV_SATFINITE, __NV_E4M3);
+    const float scale0 = __uint_as_float(s0 ? s0 << 23 : 0x400000u);
+    const float r = v - __half2float(__half(__nv_cvt_fp8_to_halfraw(q0, __NV_E4M3))) * scale0;
+    s1 = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(r) & 0x7FFFFFFFu));
+    const float inv1 = __uint_as_float((254u - s1) << 23);
+    const __nv_fp8_storage_t q1 = __nv_cvt_float_to_fp8(r * inv1, __NV_SATFINITE, __NV_E4M3);
+    return static_cast<uint32_t>(q0) | (static_cast<uint32_t>(q1) << 8);
+}
+
+// ============================================================== logits
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Block (expert group, token tile, H slice): 16 MF tokens x 8 NF experts, each
+// of 8 warps a share of the slice, joined in shared memory in warp order. A
+// thread's 16 bytes hold eight consecutive values of a row: the same
+// assignment of columns to the MMA's K on both sides, so the sum is the dot
+// product whatever the order. Then every block splits its share of x and
+// zeroes its share of the counters.
+template <int MF, int NF>
+__global__ void __launch_bounds__(256) moe_logits(const Params p) {
+    __shared__ float red[8][16 * MF][8 * NF];
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
+    const int e0 = blockIdx.x * 8 * NF, t0 = blockIdx.y * 16 * MF;
+    const long long chunks = p.H / 32, nw = 8LL * p.ksplit, wi = blockIdx.z * 8 + warp;
+    const int c0 = static_cast<int>(chunks * wi / nw), c1 = static_cast<int>(chunks * (wi + 1) / nw);
+    float acc[MF][NF][4] = {};
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) {
+        uint4 a[MF][2], b[NF];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t = t0 + 16 * i + 8 * h + g;
+                a[i][h] = t < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + 32 * c + 8 * tg))
+                                  : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int e = e0 + 8 * j + g;
+            b[j] = e < p.experts ? __ldg(reinterpret_cast<const uint4*>(p.router + static_cast<size_t>(e) * p.H + 32 * c + 8 * tg))
+                                 : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) {
+                mma_bf16(acc[i][j], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b[j].x, b[j].y);
+                mma_bf16(acc[i][j], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b[j].z, b[j].w);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[warp][16 * i + g + 8 * (r >> 1)][8 * j + 2 * tg + (r & 1)] = acc[i][j][r];
+    __syncthreads();
+    for (int o = threadIdx.x; o < 16 * MF * 8 * NF; o += 256) {
+        const int t = t0 + o / (8 * NF), e = e0 + o % (8 * NF);
+        if (t < p.T && e < p.experts) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) s += red[w][o / (8 * NF)][o % (8 * NF)];
+            p.logits[(static_cast<size_t>(blockIdx.z) * p.T + t) * p.experts + e] = s;
+        }
+    }
+    const int nblk = gridDim.x * gridDim.y * gridDim.z;
+    const int blk = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int i = blk * 256 + threadIdx.x; i < p.n_counters; i += nblk * 256) p.counters[i] = 0;
+    const int per = p.H / 32;
+    for (int i = blk * 8 + warp; i < p.T * per; i += nblk * 8) {
+        const int t = i / per, b = i - t * per;
+        uint32_t s0, s1;
+        const uint32_t q = split_block(bf16_f(p.x[static_cast<size_t>(t) * p.H + 32 * b + lane]), s0, s1);
+        uint8_t* d = p.xq + static_cast<size_t>(t) * PIECES * p.Hp + 32 * b + lane;
+        d[0] = static_cast<uint8_t>(q);
+        d[p.Hp] = static_cast<uint8_t>(q >> 8);
+        if (lane < PIECES)
+            p.sx[(static_cast<size_t>(t) * PIECES + lane) * (p.Hp / 32) + b] = static_cast<uint8_t>(lane ? s1 : s0);
+    }
+}
+
+// ============================================================== routing
+
+// Order-preserving map of a float to an unsigned integer; NaN below everything, 0 is free for "taken".
+__device__ __forceinline__ uint32_t sort_key(float v) {
+    if (v != v) return 1u;
+    const uint32_t b = __float_as_uint(v + 0.f);  // -0 -> +0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One warp: the choice of token t. Lane l holds experts l, l + 32, ...
+// in the shared arrays (score, key: [experts] each).
+__device__ __forceinline__ void choose(const Params& p, int t, float* score, uint32_t* key, int32_t* ids, float* wts) {
+    const int lane = threadIdx.x & 31;
+    const unsigned full = 0xffffffffu;
+    float m = -CUDART_INF_F;
+    for (int e = lane; e < p.experts; e += 32) {
         float s = 0.f;
-        for (int h = lane; h < a.H; h += 32) s += bf16_f(a.x[t * a.H + h]) * bf16_f(a.router[static_cast<size_t>(e) * a.H + h]);
-        s = warp_sum(s);
-        if (lane == 0) score[e] = s;
+        for (int k = 0; k < p.ksplit; ++k) s += __ldcg(p.logits + (static_cast<size_t>(k) * p.T + t) * p.experts + e);
+        score[e] = s;
+        m = fmaxf(m, s);
+    }
+    if (p.score == MXFP8_SCORE_SOFTMAX) {
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, d));
+        float sum = 0.f;
+        for (int e = lane; e < p.experts; e += 32) sum += (score[e] = expf(score[e] - m));
+        sum = warp_sum(sum);
+        for (int e = lane; e < p.experts; e += 32) score[e] /= sum;
+    } else {
+        for (int e = lane; e < p.experts; e += 32) score[e] = 1.f / (1.f + expf(-score[e]));
+    }
+    uint32_t best = 0;
+    int at = 0x7fffffff;
+    auto scan = [&]() {
+        best = 0;
+        at = 0x7fffffff;
+        for (int e = lane; e < p.experts; e += 32) {
+            const uint32_t v = key[e];
+            if (v > best) { best = v; at = e; }
+        }
+    };
+    for (int e = lane; e < p.experts; e += 32) key[e] = sort_key(score[e] + (p.bias ? p.bias[e] : 0.f));
+    scan();
+    float total = 0.f, mine = 0.f;
+    int my_id = 0;
+    __syncwarp();
+    for (int k = 0; k < p.top_k; ++k) {
+        const uint32_t top = __reduce_max_sync(full, best);
+        const int e = static_cast<int>(__reduce_min_sync(full, best == top ? static_cast<uint32_t>(at) : 0x7fffffffu));
+        const float s = score[e];
+        total += s;
+        if (lane == k) { mine = s; my_id = e; }
+        if ((e & 31) == lane) {
+            key[e] = 0;
+            scan();
+        }
+    }
+    if (lane < p.top_k) {
+        ids[lane] = my_id;
+        wts[lane] = (p.renormalize ? mine / total : mine) * p.scale;
+    }
+    __syncwarp();
+}
+
+// ============================================================== experts
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns,
+                                         int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (mbar_try_wait_suspend(bar, parity, 20000)) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > ns) {
+            *abort_flag = 1;
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigned long long ns, int* status) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > ns) {
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return;
+        }
+}
+
+// Bounded wait until *p >= target (acquire).
+__device__ __forceinline__ bool wait_count(const unsigned int* p, unsigned int target, volatile int* abort_flag,
+                                           unsigned long long ns, int* status) {
+    if (ld_acquire_gpu(p) >= target) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (ld_acquire_gpu(p) >= target) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > ns) {
+            *abort_flag = 1;
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+        __nanosleep(32);
+    }
+}
+
+// Shares of a phase's K-steps: CTA c of the first min(G, total) takes steps
+// [share(c), share(c + 1)), at least one each.
+__device__ __forceinline__ int share(int c, int total, int G) {
+    const int n = min(G, total);
+    return c >= n ? total : static_cast<int>(static_cast<long long>(c) * total / n);
+}
+
+// The CTA that owns step s.
+__device__ __forceinline__ int owner(int s, int total, int G) {
+    G = min(G, total);
+    const unsigned long long v = (static_cast<unsigned long long>(s) + 1) * G - 1;
+    if (v < (1ull << 32)) return static_cast<int>(static_cast<uint32_t>(v) / static_cast<uint32_t>(total));
+    return static_cast<int>(v / static_cast<unsigned long long>(total));
+}
+
+// Per-CTA lists in shared memory.
+struct Lists {
+    float* wts;          // [slots] weight of entry (token, k)
+    uint16_t* eid;       // [slots] local expert of the entry, 0xffff: none
+    uint16_t* slot_of;   // [slots] position of the entry among the local pairs sorted by expert
+    uint16_t* entry_of;  // [slots] entry of a position
+    uint16_t* act_of;    // [local] chosen-expert index of a local expert
+    uint16_t* count;     // [local] tokens; then [chosen] tokens of a chosen expert
+    uint16_t* act;       // [local] local expert of a chosen-expert index
+    uint16_t* off;       // [local] first position of a chosen expert
+    int* info;           // chosen experts, most tokens of one
+};
+
+// A run of K-steps of one tile.
+struct Seg {
+    int phase, tile, a, rt, k0, k1, steps;
+    bool whole;
+};
+
+// The segments of CTA c in order: up/gate tiles, then down tiles.
+struct Walk {
+    int G, c, nact, s, end, phase, total, steps, tiles;
+    const Params& p;
+
+    __device__ __forceinline__ Walk(const Params& p_, int G_, int c_, int nact_) : G(G_), c(c_), nact(nact_), p(p_) { start(0); }
+
+    __device__ __forceinline__ void start(int ph) {
+        phase = ph;
+        steps = ph ? p.down_steps : p.up_steps;
+        tiles = ph ? p.down_tiles : p.up_tiles;
+        total = nact * tiles * steps;
+        s = share(c, total, G);
+        end = share(c + 1, total, G);
+    }
+
+    __device__ __forceinline__ bool next(Seg& g) {
+        if (s >= end) {
+            if (phase) return false;
+            start(1);
+            if (s >= end) return false;
+        }
+        g.phase = phase;
+        g.steps = steps;
+        g.tile = s / steps;
+        g.a = g.tile / tiles;
+        g.rt = g.tile - g.a * tiles;
+        g.k0 = s - g.tile * steps;
+        g.k1 = min(steps, g.k0 + end - s);
+        g.whole = g.k0 == 0 && g.k1 == steps;
+        s += g.k1 - g.k0;
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+    moe_experts(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const Params p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = gridDim.x, cta = blockIdx.x;
+
+    const uint32_t bar_full = sbase, bar_empty = bar_full + 8 * MAX_ST, bar_tfull = bar_empty + 8 * MAX_ST,
+                   bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
+    int* flags = reinterpret_cast<int*>(smem + 8 * (2 * MAX_ST + 5));  // abort, TMEM base, epilogue word x2, chosen, most, barrier ok
+    volatile int* abort_flag = flags;
+    Lists L;
+    L.wts = reinterpret_cast<float*>(smem + p.off_lists);
+    L.eid = reinterpret_cast<uint16_t*>(L.wts + p.slots);
+    L.slot_of = L.eid + p.slots;
+    L.entry_of = L.slot_of + p.slots;
+    L.act_of = L.entry_of + p.slots;
+    L.count = L.act_of + p.local;
+    L.act = L.count + p.local;
+    L.off = L.act + p.local;
+    L.info = flags + 4;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < MAX_ST; ++s) {
+            mbar_init(bar_full + 8 * s, 3);   // weight producer (with its bytes), two loader warps
+            mbar_init(bar_empty + 8 * s, 1);  // the MMAs' commit
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm13);
+        tma_prefetch_desc(&tm2);
+    }
+    if (warp == 1) {
+        tmem_alloc_single(smem_u32(flags + 1), TMEM_ALL);
+        tmem_relinquish_single();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(flags[1]);
+    griddep_wait();  // logits, pieces of x, zeroed counters
+
+    // ---- routing. Up to 8 tokens: every CTA chooses for all of them (one warp
+    // each). More: one warp of CTA t % G for token t, then a grid barrier.
+    {
+        float* score = reinterpret_cast<float*>(smem + p.off_ring) + 2 * static_cast<size_t>(p.experts) * warp;
+        uint32_t* key = reinterpret_cast<uint32_t*>(score + p.experts);
+        bool ok = true;
+        if (p.T <= 8) {
+            int32_t* ids = reinterpret_cast<int32_t*>(smem + p.off_epi) + warp * MXFP8_MOE_MAX_TOPK;
+            if (warp < p.T) {
+                choose(p, warp, score, key, ids, L.wts + warp * p.top_k);
+                if (lane < p.top_k) {
+                    const int e = ids[lane];
+                    L.eid[warp * p.top_k + lane] = e >= p.first && e < p.first + p.local ? static_cast<uint16_t>(e - p.first) : 0xffff;
+                    if (cta == 0) {
+                        if (p.user_ids) p.user_ids[warp * p.top_k + lane] = e;
+                        if (p.user_weights) p.user_weights[warp * p.top_k + lane] = L.wts[warp * p.top_k + lane];
+                    }
+                }
+            }
+            __syncthreads();
+        } else {
+            for (int t = cta + warp * G; t < p.T; t += 8 * G) {
+                int32_t* ids = p.ids + t * p.top_k;
+                float* wts = p.weights + t * p.top_k;
+                choose(p, t, score, key, ids, wts);
+                if (lane < p.top_k) {
+                    if (p.user_ids) p.user_ids[t * p.top_k + lane] = ids[lane];
+                    if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
+                }
+            }
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                red_release_gpu_add(p.counters, 1);
+                flags[6] = wait_count(p.counters, G, abort_flag, p.wait_ns, p.status) ? 1 : 0;
+            }
+            __syncthreads();
+            ok = flags[6] != 0;
+            if (ok)
+                for (int i = threadIdx.x; i < p.slots; i += THREADS) {
+                    const int e = __ldcg(p.ids + i);
+                    L.eid[i] = e >= p.first && e < p.first + p.local ? static_cast<uint16_t>(e - p.first) : 0xffff;
+                    L.wts[i] = __ldcg(p.weights + i);
+                }
+            __syncthreads();
+        }
+        // ---- the (token, expert) pairs sorted by expert, in token order
+        if (warp == 0) {
+            for (int e = lane; e < p.local; e += 32) L.count[e] = 0;
+            __syncwarp();
+            for (int b = 0; ok && b < p.slots; b += 32) {
+                const int i = b + lane;
+                const int e = i < p.slots ? L.eid[i] : 0xffff;
+                const unsigned same = __match_any_sync(0xffffffffu, e != 0xffff ? e : 0x10000 + lane);
+                const int before = __popc(same & ((1u << lane) - 1));
+                const int base = e != 0xffff ? L.count[e] : 0;
+                __syncwarp();
+                if (e != 0xffff) {
+                    L.slot_of[i] = static_cast<uint16_t>(base + before);
+                    if (before == 0) L.count[e] = static_cast<uint16_t>(base + __popc(same));
+                }
+                __syncwarp();
+            }
+            int chosen = 0, first = 0, most = 0;
+            for (int b = 0; b < p.local; b += 32) {
+                const int e = b + lane;
+                const int n = e < p.local ? L.count[e] : 0;
+                const unsigned have = __ballot_sync(0xffffffffu, n > 0);
+                int incl = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, d);
+                    if (lane >= d) incl += v;
+                }
+                __syncwarp();
+                if (n > 0) {
+                    const int a = chosen + __popc(have & ((1u << lane) - 1));
+                    L.act[a] = static_cast<uint16_t>(e);
+                    L.act_of[e] = static_cast<uint16_t>(a);
+                    L.off[a] = static_cast<uint16_t>(first + incl - n);
+                    L.count[a] = static_cast<uint16_t>(n);  // a <= e: the counts still to be read lie behind
+                }
+                __syncwarp();
+                chosen += __popc(have);
+                first += __shfl_sync(0xffffffffu, incl, 31);
+                most = max(most, __reduce_max_sync(0xffffffffu, n));
+            }
+            for (int i = lane; ok && i < p.slots; i += 32)
+                if (L.eid[i] != 0xffff) {
+                    const int s = L.off[L.act_of[L.eid[i]]] + L.slot_of[i];
+                    L.slot_of[i] = static_cast<uint16_t>(s);
+                    L.entry_of[s] = static_cast<uint16_t>(i);
+                }
+            if (lane == 0) {
+                L.info[0] = ok ? chosen : 0;
+                L.info[1] = most;
+            }
+        }
+        fence_proxy_async_shared();  // the ring's space held the scores
+        __syncthreads();
+    }
+    const int nact = L.info[0];
+    // MMA width for the expert with the most tokens; ring of K-step stages
+    const int nmax = max(16, (PIECES * L.info[1] + 15) & ~15);
+    const uint32_t nblk = (nmax + 127) / 128;
+    const uint32_t sf_stage = 512 * (1 + nblk) + (p.raw ? 1024 : 0);
+    const uint32_t ab_stage = A_BYTES + nmax * STEP;
+    const int S = min(MAX_ST, static_cast<int>((SMEM_MAX - 1024 - p.off_ring) / (ab_stage + sf_stage)));
+    const uint32_t ring = sbase + p.off_ring, sf_ring = ring + S * ab_stage;
+    const uint32_t sf_cols = 4 * (1 + nblk);
+    const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;
+    const uint32_t sf_tmem = tmem + nbuf * nmax;
+
+    if (warp == 0) {
+        // ------------------------------------------------ weight producer
+        if (lane == 0) {
+            Walk w(p, G, cta, nact);
+            Seg g;
+            int c = 0;
+            bool ok = true;
+            while (ok && w.next(g)) {
+                const CUtensorMap* map = g.phase ? &tm2 : &tm13;
+                const int e = L.act[g.a];
+                const int r0 = g.phase ? g.rt * TILE : g.rt * (TILE / 2);
+                const int r1 = g.phase ? r0 + TILE / 2 : p.I + r0;
+                for (int k = g.k0; k < g.k1; ++k, ++c) {
+                    const int st = c % S;
+                    if (!wait_bar(bar_empty + 8 * st, ((c / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status)) { ok = false; break; }
+                    const uint32_t dst = ring + st * ab_stage;
+                    mbar_arrive_expect_tx(bar_full + 8 * st, A_BYTES);
+                    tma_load_3d(dst, map, bar_full + 8 * st, k * STEP, r0, e);
+                    tma_load_3d(dst + A_BYTES / 2, map, bar_full + 8 * st, k * STEP, r1, e);
+                }
+            }
+            if (!ok || *abort_flag)
+                for (int d = 1; d <= min(c, S); ++d) {
+                    // every copy in flight lands before the CTA exits: the bytes are
+                    // counted with the loaders' arrivals, so stand in for those
+                    const int st = (c - d) % S;
+                    mbar_arrive(bar_full + 8 * st);
+                    mbar_arrive(bar_full + 8 * st);
+                    drain_bar(bar_full + 8 * st, ((c - d) / S) & 1, 1000000ull, p.status);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        Walk w(p, G, cta, nact);
+        Seg g;
+        int c = 0, tile = 0;
+        bool ok = true;
+        while (ok && w.next(g)) {
+            const int K = g.phase ? p.I : p.H;
+            const int n = max(16, (PIECES * L.count[g.a] + 15) & ~15);
+            const uint32_t idesc = IDESC | (static_cast<uint32_t>(n >> 3) << 17);
+            const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
+            if (lane == 0) ok = wait_bar(bar_tempty + 8 * buf, (use & 1) ^ 1, abort_flag, p.wait_ns, p.status);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            const uint32_t d = tmem + buf * nmax;
+            for (int k = g.k0; k < g.k1; ++k, ++c) {
+                const int st = c % S;
+                if (lane == 0) ok = wait_bar(bar_full + 8 * st, (c / S) & 1, abort_flag, p.wait_ns, p.status);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sf = sf_ring + st * sf_stage, sft = sf_tmem + st * sf_cols;
+                tc_cp_32x128b_warpx4_elect(sft, desc_sf_block(sf));
+                for (uint32_t b = 0; b < nblk; ++b) tc_cp_32x128b_warpx4_elect(sft + 4 + 4 * b, desc_sf_block(sf + 512 + 512 * b));
+                const uint32_t as = ring + st * ab_stage, bs = as + A_BYTES;
+                const int nk = min(4, (K - k * STEP) >> 5);
+                for (int kk = 0; kk < nk; ++kk) {
+                    const uint32_t sel = (static_cast<uint32_t>(kk) << 29) | (static_cast<uint32_t>(kk) << 4);
+                    tc_mma_mxf8_elect(d, desc_kmajor_sw128(as + 32 * kk), desc_kmajor_sw128(bs + 32 * kk), idesc | sel, sft,
+                                      sft + 4, k > g.k0 || kk > 0 ? 1u : 0u);
+                }
+                tc_commit_elect(bar_empty + 8 * st);
+            }
+            if (!ok) break;
+            tc_commit_elect(bar_tfull + 8 * buf);
+            ++tile;
+        }
+        tc_commit_elect(bar_drain);
+        if (lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------ loaders: token columns and scales
+        // Thread l of 64 copies weight-scale rows l and l + 64, and its share of
+        // the token rows' 16-byte pieces and scale words.
+        const int l = (warp - 2) * 32 + lane;
+        uint32_t* rows = reinterpret_cast<uint32_t*>(smem + p.off_rows) + (warp - 2) * 256;  // row offset / 16 of each column
+        Walk w(p, G, cta, nact);
+        Seg g;
+        int c = 0, sent = 0;  // K-steps issued and handed over
+        const int lag = S > LAG ? LAG : 1;  // below S: the stage to be refilled has been handed over
+        bool ok = true;
+        // hand over the stages up to `upto` (their copies have completed)
+        auto hand = [&](int upto) {
+            if (p.raw) {
+                for (int q = sent; q < upto; ++q) {
+                    // two aligned words of each row -> the four scale bytes
+                    const uint32_t sf = sf_ring + (q % S) * sf_stage, rb = sf + 512 * (1 + nblk);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = l + 64 * h;
+                        const uint32_t *src = reinterpret_cast<const uint32_t*>(smem + (rb - sbase) + r * 8);
+                        const uint32_t sh = *reinterpret_cast<const uint8_t*>(smem + p.off_rows + 2048 + (q % S) * 128 + r);
+                        st_shared_b32(sf + (r & 31) * 16 + (r >> 5) * 4, __funnelshift_r(src[0], src[1], sh));
+                    }
+                }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0)
+                for (int q = sent; q < upto; ++q) mbar_arrive(bar_full + 8 * (q % S));
+            sent = upto;
+        };
+        while (ok && w.next(g)) {
+            const int e = L.act[g.a], nt = L.count[g.a], off = L.off[g.a];
+            const int n = PIECES * nt;
+            const uint8_t* plane = g.phase ? p.s2 : p.s13;
+            const int R = g.phase ? p.H : 2 * p.I, K = g.phase ? p.I : p.H;
+            const size_t plane_bytes = static_cast<size_t>(p.local) * R * (K / 32);
+            const uint8_t* act = g.phase ? p.hq : p.xq;
+            const uint8_t* sact = g.phase ? p.sh : p.sx;
+            const int stride = g.phase ? p.Ip : p.Hp, sstride = g.phase ? p.sh_stride : p.Hp / 32;
+            if (g.phase) {
+                // this expert's h: complete what is in flight first, since other
+                // CTAs may be waiting for tiles that need it
+                if (sent < c) {
+                    cp_async_wait<0>();
+                    hand(c);
+                }
+                if (lane == 0) ok = wait_count(p.counters + 2 + g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+            }
+            __syncwarp();
+            for (int r = lane; r < n; r += 32) {
+                const int pc = r >= nt ? 1 : 0, j = r - pc * nt;
+                const int row = g.phase ? off + j : L.entry_of[off + j] / p.top_k;
+                rows[r] = row * PIECES + pc;
+            }
+            __syncwarp();
+            // weight-scale rows of this thread (clamped: rows past the matrix are not stored)
+            size_t srow[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = l + 64 * h;
+                int wr;
+                if (g.phase) wr = min(g.rt * TILE + r, p.H - 1);
+                else wr = h * p.I + min(g.rt * (TILE / 2) + l, p.I - 1);
+                srow[h] = (static_cast<size_t>(e) * R + wr) * (K / 32);
+            }
+            for (int k = g.k0; k < g.k1; ++k, ++c) {
+                const int st = c % S;
+                if (lane == 0) ok = wait_bar(bar_empty + 8 * st, ((c / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                const uint32_t sf = sf_ring + st * sf_stage, bs = ring + st * ab_stage + A_BYTES;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = l + 64 * h;
+                    const size_t at = srow[h] + 4 * k;
+                    if (!p.raw) {
+                        cp_async_4(sf + (r & 31) * 16 + (r >> 5) * 4, plane + at);
+                    } else {
+                        const uint32_t rb = sf + 512 * (1 + nblk) + r * 8;
+                        const size_t w0 = at & ~size_t(3);
+                        cp_async_4(rb, plane + w0);
+                        cp_async_4(rb + 4, plane + (w0 + 8 <= plane_bytes ? w0 + 4 : w0));
+                        smem[p.off_rows + 2048 + st * 128 + r] = static_cast<uint8_t>((at & 3) * 8);
+                    }
+                }
+                for (int r = l; r < n; r += 64)
+                    cp_async_4(sf + 512 + 512 * (r >> 7) + (r & 31) * 16 + ((r >> 5) & 3) * 4,
+                               sact + static_cast<size_t>(rows[r]) * sstride + 4 * k);
+                // thread l takes 16-byte piece l % 8 of rows l / 8, l / 8 + 8, ...
+                // (each warp reads the table that it filled itself)
+                const uint32_t chunk = l & 7;
+                for (int r = l >> 3; r < n; r += 8)
+                    cp_async_16(bs + r * 128 + ((chunk ^ (r & 7)) << 4),
+                                act + static_cast<size_t>(rows[r]) * stride + k * STEP + chunk * 16);
+                cp_async_commit();
+                if (c - sent >= lag) {
+                    if (lag == LAG) cp_async_wait<LAG>();
+                    else cp_async_wait<1>();
+                    hand(c + 1 - lag);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        if (sent < c) hand(c);
+    } else {
+        // ------------------------------------------------ epilogue (4 warps)
+        // Thread = TMEM lane = weight row of the tile. Columns: piece 0 of every
+        // token, then piece 1; their sum is the product.
+        const int q = warp - 4, row = threadIdx.x - 128;
+        float* xch = reinterpret_cast<float*>(smem + p.off_epi);  // [2][8 tokens][128 rows]
+        Walk w(p, G, cta, nact);
+        Seg g;
+        int tile = 0;
+        // h of 32 inner rows of one token: two pieces and their scales
+        auto store_h = [&](int slot, int i0, float gate, float up) {
+            const float h = gate / (1.f + expf(-gate)) * up;
+            uint32_t s0, s1;
+            const uint32_t pc = split_block(h, s0, s1);
+            uint8_t* d = p.hq + static_cast<size_t>(slot) * PIECES * p.Ip + i0 + lane;
+            d[0] = static_cast<uint8_t>(pc);
+            d[p.Ip] = static_cast<uint8_t>(pc >> 8);
+            if (lane < PIECES)
+                p.sh[(static_cast<size_t>(slot) * PIECES + lane) * p.sh_stride + (i0 >> 5)] = static_cast<uint8_t>(lane ? s1 : s0);
+        };
+        while (w.next(g)) {
+            const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
+            const int nt = L.count[g.a], off = L.off[g.a];
+            if (q == 0 && lane == 0)
+                flags[2 + (tile & 1)] = wait_bar(bar_tfull + 8 * buf, use & 1, abort_flag, p.wait_ns, p.status) ? 1 : 0;
+            named_bar_sync(EPI_BAR, 128);
+            if (!flags[2 + (tile & 1)]) break;
+            ++tile;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * nmax + (static_cast<uint32_t>(q * 32) << 16);
+            float* part = (g.phase ? p.part_down : p.part_up) +
+                          (static_cast<size_t>(cta) * 2 + (g.k0 > 0 ? 0 : 1)) * p.T * TILE;
+            for (int j0 = 0; j0 < nt; j0 += 8) {
+                uint32_t v0[8], v1[8];
+                tmem_ld_32x32b_x8(d + j0, v0);
+                tmem_ld_32x32b_x8(d + nt + j0, v1);
+                tmem_wait_ld();
+                reg_fence8(v0);
+                reg_fence8(v1);
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(v0[j]) + __uint_as_float(v1[j]);
+                if (!g.whole) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < nt) part[(j0 + j) * TILE + row] = v[j];
+                } else if (g.phase) {
+                    const int n = g.rt * TILE + row;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < nt && n < p.H)
+                            p.y[static_cast<size_t>(off + j0 + j) * p.Hp + n] = v[j] * L.wts[L.entry_of[off + j0 + j]];
+                } else {
+                    float* x = xch + ((j0 >> 3) & 1) * 8 * TILE;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j * TILE + row] = v[j];
+                    named_bar_sync(EPI_BAR, 128);
+                    // warp q: tokens j0 + 2q, j0 + 2q + 1, both halves of the 64 inner rows
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        const int j = 2 * q + (o >> 1), i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
+                        if (j0 + j < nt && i0 < p.I) store_h(off + j0 + j, i0, x[j * TILE + i], x[j * TILE + TILE / 2 + i]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
+            if (g.phase == 0) {
+                bool finish = g.whole;
+                if (!g.whole) {
+                    // the last CTA to bring its part of the tile sums all of them, in CTA order
+                    const int total = nact * p.up_tiles * p.up_steps;
+                    const int cf = owner(g.tile * p.up_steps, total, G), cl = owner((g.tile + 1) * p.up_steps - 1, total, G);
+                    __threadfence();
+                    named_bar_sync(EPI_BAR, 128);
+                    if (q == 0 && lane == 0)
+                        flags[8] = atom_acq_rel_gpu_add(p.counters + 2 + p.local + g.tile, 1) == static_cast<uint32_t>(cl - cf) ? 1 : 0;
+                    named_bar_sync(EPI_BAR, 128);
+                    finish = flags[8] != 0;
+                    if (finish) {
+                        __threadfence();
+                        for (int o = q; o < 2 * nt; o += 4) {
+                            const int j = o >> 1, i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
+                            if (i0 >= p.I) continue;
+                            float gate = 0.f, up = 0.f;
+                            for (int cc = cf; cc <= cl; ++cc) {
+                                const float* src = p.part_up + (static_cast<size_t>(cc) * 2 + (cc == cf ? 1 : 0)) * p.T * TILE +
+                                                   static_cast<size_t>(j) * TILE;
+                                gate += __ldcg(src + i);
+                                up += __ldcg(src + TILE / 2 + i);
+                            }
+                            store_h(off + j, i0, gate, up);
+                        }
+                    }
+                }
+                if (finish) {
+                    __threadfence();
+                    named_bar_sync(EPI_BAR, 128);
+                    if (q == 0 && lane == 0) red_release_gpu_add(p.counters + 2 + g.a, 1);
+                }
+            }
+        }
+    }
+
+    // ---- every product is in y or a partial: grid barrier, then the weighted sum
+    tc_fence_before();
+    __threadfence();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_single(tmem, TMEM_ALL);
+    if (threadIdx.x == 0) {
+        bool ok = !*abort_flag;
+        if (ok && nact) {
+            red_release_gpu_add(p.counters + 1, 1);
+            ok = wait_count(p.counters + 1, G, abort_flag, p.wait_ns, p.status);
+        }
+        flags[6] = ok ? 1 : 0;
     }
     __syncthreads();
-    if (warp != 0) return;
-    if (a.score == MXFP8_SCORE_SOFTMAX) {
-        float m = -CUDART_INF_F, sum = 0.f;
-        for (int e = lane; e < a.experts; e += 32) m = fmaxf(m, score[e]);
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int e = lane; e < a.experts; e += 32) sum += (score[e] = expf(score[e] - m));
-        sum = warp_sum(sum);
-        for (int e = lane; e < a.experts; e += 32) score[e] /= sum;
-    } else {
-        for (int e = lane; e < a.experts; e += 32) score[e] = 1.f / (1.f + expf(-score[e]));
-    }
-    for (int e = lane; e < a.experts; e += 32) {
-        const float v = score[e] + (a.bias ? a.bias[e] : 0.f);
-        key[e] = v != v ? -CUDART_INF_F : v;
-    }
-    __syncwarp();
-    uint32_t taken[MXFP8_MOE_MAX_EXPERTS / 32 / 32] = {0};
-    float total = 0.f;
-    for (int k = 0; k < a.top_k; ++k) {
-        float best = -CUDART_INF_F;
-        int at = 0x7fffffff;
-        for (int i = 0; i * 32 + lane < a.experts; ++i)
-            if (!((taken[i >> 5] >> (i & 31)) & 1) && (at == 0x7fffffff || key[i * 32 + lane] > best)) {
-                best = key[i * 32 + lane];
-                at = i * 32 + lane;
+    if (!flags[6]) return;
+    const int total = nact * p.down_tiles * p.down_steps, half = p.H / 2;
+    for (int o = cta * THREADS + threadIdx.x; o < p.T * half; o += G * THREADS) {
+        const int t = o / half, n = 2 * (o - t * half), rt = n / TILE, r = n - rt * TILE;
+        float y0 = 0.f, y1 = 0.f;
+        for (int k = 0; k < p.top_k; ++k) {
+            const int i = t * p.top_k + k, e = L.eid[i];
+            if (e == 0xffff) continue;
+            const int a = L.act_of[e], slot = L.slot_of[i], tl = a * p.down_tiles + rt;
+            const int cf = owner(tl * p.down_steps, total, G), cl = owner((tl + 1) * p.down_steps - 1, total, G);
+            if (cf == cl) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(p.y + static_cast<size_t>(slot) * p.Hp + n));
+                y0 += v.x;
+                y1 += v.y;
+            } else {
+                float z0 = 0.f, z1 = 0.f;
+                for (int cc = cf; cc <= cl; ++cc) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(
+                        p.part_down + (static_cast<size_t>(cc) * 2 + (cc == cf ? 1 : 0)) * p.T * TILE +
+                        static_cast<size_t>(slot - L.off[a]) * TILE + r));
+                    z0 += v.x;
+                    z1 += v.y;
+                }
+                y0 += z0 * L.wts[i];
+                y1 += z1 * L.wts[i];
             }
-        for (int d = 16; d > 0; d >>= 1) {
-            const float ob = __shfl_xor_sync(0xffffffffu, best, d);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, d);
-            if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
         }
-        if ((at & 31) == lane) taken[at >> 10] |= 1u << ((at >> 5) & 31);
-        total += score[at];
-        if (lane == 0) { ids[t * a.top_k + k] = at; wts[t * a.top_k + k] = score[at]; }
+        reinterpret_cast<uint32_t*>(p.out)[static_cast<size_t>(t) * half + (n >> 1)] = pack_bf16x2(__float_as_uint(y0), __float_as_uint(y1));
     }
-    __syncwarp();
-    if (lane < a.top_k) wts[t * a.top_k + lane] = a.renormalize ? wts[t * a.top_k + lane] / total * a.scale : wts[t * a.top_k + lane] * a.scale;
 }
 
-__device__ __forceinline__ float row_dot(const uint8_t* q, const uint8_t* s, int n, const float* v32, const uint16_t* v16, int lane) {
-    float acc = 0.f;
-    for (int i = lane; i < n; i += 32) {
-        const float v = v32 ? v32[i] : bf16_f(v16[i]);
-        acc += e4m3_f(q[i]) * e8m0_f(s[i >> 5]) * v;
-    }
-    return warp_sum(acc);
-}
+// ============================================================== host side
 
-// One warp per (token, chosen expert, inner row): h = silu(g) u.
-__global__ void __launch_bounds__(256) up_simple(const MoeArgs a, const int32_t* ids, float* h) {
-    const int slot = blockIdx.y, i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int e = ids[slot] - a.first;
-    if (i >= a.I || e < 0 || e >= a.local) return;
-    const uint16_t* x = a.x + static_cast<size_t>(slot / a.top_k) * a.H;
-    const size_t rg = static_cast<size_t>(e) * 2 * a.I + i, ru = rg + a.I;
-    const float g = row_dot(a.w13 + rg * a.H, a.s13 + rg * (a.H / 32), a.H, nullptr, x, lane);
-    const float u = row_dot(a.w13 + ru * a.H, a.s13 + ru * (a.H / 32), a.H, nullptr, x, lane);
-    if (lane == 0) h[static_cast<size_t>(slot) * a.I + i] = g / (1.f + expf(-g)) * u;
-}
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// One warp per (token, output row): the weighted sum over its experts.
-__global__ void __launch_bounds__(256) down_simple(const MoeArgs a, const int32_t* ids, const float* wts, const float* h) {
-    const int t = blockIdx.y, n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (n >= a.H) return;
-    float y = 0.f;
-    for (int k = 0; k < a.top_k; ++k) {
-        const int slot = t * a.top_k + k, e = ids[slot] - a.first;
-        if (e < 0 || e >= a.local) continue;
-        const size_t r = static_cast<size_t>(e) * a.H + n;
-        y += wts[slot] * row_dot(a.w2 + r * a.I, a.s2 + r * (a.I / 32), a.I, h + static_cast<size_t>(slot) * a.I, nullptr, lane);
-    }
-    if (lane == 0) a.out[static_cast<size_t>(t) * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+struct Layout {
+    int ksplit, Hp, Ip, sh_stride, up_tiles, down_tiles, up_steps, down_steps, slots, local_slots, n_counters, mf, nf;
+    size_t counters, logits, ids, weights, xq, sx, hq, sh, y, part_up, part_down, total;
+};
+
+void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Layout* l) {
+    l->mf = T > 16 ? 2 : 1;
+    l->nf = T > 16 ? 4 : 2;
+    // slices of H so that about 300 blocks share the logits, each of their 8 warps at least one 32-column chunk
+    const int tiles = ((experts + 8 * l->nf - 1) / (8 * l->nf)) * ((T + 16 * l->mf - 1) / (16 * l->mf));
+    int ks = 300 / tiles;
+    if (ks > 8) ks = 8;
+    if (ks > H / 256) ks = H / 256;
+    l->ksplit = ks < 1 ? 1 : ks;
+    l->Hp = (H + STEP - 1) / STEP * STEP;
+    l->Ip = (I + STEP - 1) / STEP * STEP;
+    l->sh_stride = (l->Ip / 32 + 127) & ~127;  // a line of its own for each row: read through L1 while others are written
+    l->up_tiles = (I + TILE / 2 - 1) / (TILE / 2);
+    l->down_tiles = (H + TILE - 1) / TILE;
+    l->up_steps = l->Hp / STEP;
+    l->down_steps = l->Ip / STEP;
+    l->slots = T * top_k;
+    l->local_slots = top_k < local ? T * top_k : T * local;
+    l->n_counters = 2 + local + local * l->up_tiles;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
+    l->counters = take(4 * static_cast<size_t>(l->n_counters));
+    l->logits = take(4 * static_cast<size_t>(l->ksplit) * T * experts);
+    l->ids = take(4 * static_cast<size_t>(l->slots));
+    l->weights = take(4 * static_cast<size_t>(l->slots));
+    l->xq = take(static_cast<size_t>(T) * PIECES * l->Hp);
+    l->sx = take(static_cast<size_t>(T) * PIECES * (l->Hp / 32));
+    l->hq = take(static_cast<size_t>(l->local_slots) * PIECES * l->Ip);
+    l->sh = take(static_cast<size_t>(l->local_slots) * PIECES * l->sh_stride);
+    l->y = take(4 * static_cast<size_t>(l->local_slots) * l->Hp);
+    l->part_up = take(4 * static_cast<size_t>(sms) * 2 * T * TILE);
+    l->part_down = take(4 * static_cast<size_t>(sms) * 2 * T * TILE);
+    l->total = at;
 }
 
 }  // namespace
 
-size_t moe_ws_bytes(int T, int, int, int, int I, int top_k, int) {
-    return static_cast<size_t>(T) * top_k * (8 + static_cast<size_t>(I) * 4) + 256;
+size_t moe_ws_bytes(int T, int experts, int local, int H, int I, int top_k, int sms) {
+    Layout l;
+    layout(T, experts, local, H, I, top_k, sms, &l);
+    return l.total;
 }
 
 int launch_moe(const MoeArgs& a) {
-    const int slots = a.T * a.top_k;
-    float* h = reinterpret_cast<float*>(a.ws);
-    int32_t* ids = a.ids ? a.ids : reinterpret_cast<int32_t*>(h + static_cast<size_t>(slots) * a.I);
-    float* wts = a.weights ? a.weights : h + static_cast<size_t>(slots) * (a.I + 1);
-    route_simple<<<a.T, 256, 0, a.stream>>>(a, ids, wts);
-    up_simple<<<dim3((a.I + 7) / 8, slots), 256, 0, a.stream>>>(a, ids, h);
-    down_simple<<<dim3((a.H + 7) / 8, a.T), 256, 0, a.stream>>>(a, ids, wts, h);
-    const cudaError_t e = cudaGetLastError();
+    Layout l;
+    layout(a.T, a.experts, a.local, a.H, a.I, a.top_k, a.num_sms, &l);
+    if (static_cast<long long>(a.local) * l.up_tiles * l.up_steps > 0x7fffffffLL / 2 ||
+        static_cast<long long>(a.local) * l.down_tiles * l.down_steps > 0x7fffffffLL / 2)
+        return host_fail(MXFP8_EINVAL, "local=%d experts of H=%d, I=%d: too many tiles", a.local, a.H, a.I);
+    Params p{};
+    p.x = a.x; p.router = a.router; p.bias = a.bias; p.s13 = a.s13; p.s2 = a.s2;
+    p.T = a.T; p.experts = a.experts; p.first = a.first; p.local = a.local; p.H = a.H; p.I = a.I; p.top_k = a.top_k;
+    p.score = a.score; p.renormalize = a.renormalize; p.scale = a.scale;
+    p.out = a.out; p.user_ids = a.ids; p.user_weights = a.weights;
+    p.counters = reinterpret_cast<unsigned int*>(a.ws + l.counters);
+    p.logits = reinterpret_cast<float*>(a.ws + l.logits);
+    p.ids = reinterpret_cast<int32_t*>(a.ws + l.ids);
+    p.weights = reinterpret_cast<float*>(a.ws + l.weights);
+    p.xq = a.ws + l.xq; p.sx = a.ws + l.sx; p.hq = a.ws + l.hq; p.sh = a.ws + l.sh;
+    p.y = reinterpret_cast<float*>(a.ws + l.y);
+    p.part_up = reinterpret_cast<float*>(a.ws + l.part_up);
+    p.part_down = reinterpret_cast<float*>(a.ws + l.part_down);
+    p.Hp = l.Hp; p.Ip = l.Ip; p.sh_stride = l.sh_stride; p.ksplit = l.ksplit; p.slots = l.slots; p.n_counters = l.n_counters;
+    p.up_tiles = l.up_tiles; p.down_tiles = l.down_tiles; p.up_steps = l.up_steps; p.down_steps = l.down_steps;
+    p.raw = (a.H % STEP) != 0 || (a.I % STEP) != 0;
+    p.off_lists = 512;
+    p.off_epi = (p.off_lists + l.slots * 10 + a.local * 8 + 127) & ~127u;
+    p.off_rows = p.off_epi + 2 * 8 * TILE * 4;
+    p.off_ring = (p.off_rows + 2048 + (p.raw ? MAX_ST * 128 : 0) + 1023) & ~1023u;
+    p.wait_ns = a.wait_limit_ns;
+    p.status = a.status;
+
+    CUtensorMap m13, m2;
+    const uint32_t box[3] = {STEP, TILE / 2, 1};
+    const uint64_t d13[3] = {static_cast<uint64_t>(a.H), 2 * static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.local)};
+    const uint64_t st13[2] = {static_cast<uint64_t>(a.H), 2 * static_cast<uint64_t>(a.I) * a.H};
+    const uint64_t d2[3] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.local)};
+    const uint64_t st2[2] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.H) * a.I};
+    int rc = host_tensor_map(&m13, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w13, d13, st13, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+    rc = host_tensor_map(&m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w2, d2, st2, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc) return rc;
+
+    static std::atomic<bool> ready[64];
+    cudaError_t e;
+    if (!ready[a.dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(moe_experts, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+        if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s", cudaGetErrorString(e));
+        ready[a.dev].store(true, std::memory_order_relaxed);
+    }
+    const dim3 grid((a.experts + 8 * l.nf - 1) / (8 * l.nf), (a.T + 16 * l.mf - 1) / (16 * l.mf), l.ksplit);
+    if (l.mf == 2) moe_logits<2, 4><<<grid, 256, 0, a.stream>>>(p);
+    else moe_logits<1, 2><<<grid, 256, 0, a.stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "router kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_sms);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_MAX;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // CTAs wait on one another: all of them resident at once
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, moe_experts, m13, m2, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;
 }
