@@ -47,9 +47,10 @@ constexpr int STEP = 128;            // columns of a K-step
 constexpr int TILE = 128;            // weight rows of a tile
 constexpr int A_BYTES = TILE * STEP;
 constexpr int MAX_ST = 12;           // pipeline stages
-constexpr int THREADS = 256;         // weight producer, MMA issuer, 2 loaders, 4 epilogue warps
+constexpr int THREADS = 288;         // warps: 0 weight producer, 1 MMA issuer, 2, 3, 8 loaders, 4 .. 7 epilogue
+constexpr int LOADERS = 3;
+constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (rings of 6 stages or more; else 1)
 constexpr int SMEM_MAX = 232448;
-constexpr int LAG = 3;               // K-steps a loader keeps in flight
 constexpr uint32_t TMEM_ALL = 512;
 constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
 // kind::mxf8f6f4, E4M3 x E4M3, both K-major, E8M0 scales, M = 128
@@ -75,7 +76,6 @@ struct Params {
     float *part_up, *part_down;  // [CTA][2][T][128]
     int Hp, Ip, sh_stride, ksplit, slots, n_counters;
     int up_tiles, down_tiles, up_steps, down_steps;
-    int raw;                 // scale rows not word-aligned (H or I no multiple of 128): scales through a raw buffer
     uint32_t off_lists, off_epi, off_rows, off_ring;
     unsigned long long wait_ns;
     int* status;
@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
 
-    const uint32_t bar_full = sbase, bar_empty = bar_full + 8 * MAX_ST, bar_tfull = bar_empty + 8 * MAX_ST,
-                   bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
-    int* flags = reinterpret_cast<int*>(smem + 8 * (2 * MAX_ST + 5));  // abort, TMEM base, epilogue word x2, chosen, most, barrier ok
+    const uint32_t bar_w = sbase, bar_act = bar_w + 8 * MAX_ST, bar_empty = bar_act + 8 * MAX_ST,
+                   bar_tfull = bar_empty + 8 * MAX_ST, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
+    int* flags = reinterpret_cast<int*>(smem + 8 * (3 * MAX_ST + 5));  // abort, TMEM base, epilogue word x2, chosen, most, barrier ok
     volatile int* abort_flag = flags;
     Lists L;
     L.wts = reinterpret_cast<float*>(smem + p.off_lists);
@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_ST; ++s) {
-            mbar_init(bar_full + 8 * s, 3);   // weight producer (with its bytes), two loader warps
+            mbar_init(bar_w + 8 * s, 1);      // weight producer (with its bytes)
+            mbar_init(bar_act + 8 * s, 1);    // the K-step's loader
             mbar_init(bar_empty + 8 * s, 1);  // the MMAs' commit
         }
         for (int b = 0; b < 2; ++b) {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncthreads();
         } else {
-            for (int t = cta + warp * G; t < p.T; t += 8 * G) {
+            for (int t = warp < 8 ? cta + warp * G : p.T; t < p.T; t += 8 * G) {
                 int32_t* ids = p.ids + t * p.top_k;
                 float* wts = p.weights + t * p.top_k;
                 choose(p, t, score, key, ids, wts);
@@ -525,12 +526,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // MMA width for the expert with the most tokens; ring of K-step stages
     const int nmax = max(16, (PIECES * L.info[1] + 15) & ~15);
     const uint32_t nblk = (nmax + 127) / 128;
-    const uint32_t sf_stage = 512 * (1 + nblk) + (p.raw ? 1024 : 0);
+    const uint32_t sf_stage = 512 * (1 + nblk);
     const uint32_t ab_stage = A_BYTES + nmax * STEP;
     const int S = min(MAX_ST, static_cast<int>((SMEM_MAX - 1024 - p.off_ring) / (ab_stage + sf_stage)));
     const uint32_t ring = sbase + p.off_ring, sf_ring = ring + S * ab_stage;
     const uint32_t sf_cols = 4 * (1 + nblk);
-    const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;
+    const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;  // accumulators
     const uint32_t sf_tmem = tmem + nbuf * nmax;
 
     if (warp == 0) {
@@ -538,7 +539,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
             Walk w(p, G, cta, nact);
             Seg g;
-            int c = 0;
+            int c = 0, st = 0;
+            uint32_t ph = 1;
             bool ok = true;
             while (ok && w.next(g)) {
                 const CUtensorMap* map = g.phase ? &tm2 : &tm13;
@@ -546,173 +548,214 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int r0 = g.phase ? g.rt * TILE : g.rt * (TILE / 2);
                 const int r1 = g.phase ? r0 + TILE / 2 : p.I + r0;
                 for (int k = g.k0; k < g.k1; ++k, ++c) {
-                    const int st = c % S;
-                    if (!wait_bar(bar_empty + 8 * st, ((c / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status)) { ok = false; break; }
+                    if (!wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status)) { ok = false; break; }
                     const uint32_t dst = ring + st * ab_stage;
-                    mbar_arrive_expect_tx(bar_full + 8 * st, A_BYTES);
-                    tma_load_3d(dst, map, bar_full + 8 * st, k * STEP, r0, e);
-                    tma_load_3d(dst + A_BYTES / 2, map, bar_full + 8 * st, k * STEP, r1, e);
+                    mbar_arrive_expect_tx(bar_w + 8 * st, A_BYTES);
+                    tma_load_3d(dst, map, bar_w + 8 * st, k * STEP, r0, e);
+                    tma_load_3d(dst + A_BYTES / 2, map, bar_w + 8 * st, k * STEP, r1, e);
+                    if (++st == S) { st = 0; ph ^= 1; }
                 }
             }
-            if (!ok || *abort_flag)
-                for (int d = 1; d <= min(c, S); ++d) {
-                    // every copy in flight lands before the CTA exits: the bytes are
-                    // counted with the loaders' arrivals, so stand in for those
-                    const int st = (c - d) % S;
-                    mbar_arrive(bar_full + 8 * st);
-                    mbar_arrive(bar_full + 8 * st);
-                    drain_bar(bar_full + 8 * st, ((c - d) / S) & 1, 1000000ull, p.status);
-                }
+            if (!ok || *abort_flag)  // every copy in flight lands before the CTA exits
+                for (int d = 1; d <= min(c, S); ++d) drain_bar(bar_w + 8 * ((c - d) % S), ((c - d) / S) & 1, p.wait_ns, p.status);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        Walk w(p, G, cta, nact);
-        Seg g;
-        int c = 0, tile = 0;
-        bool ok = true;
-        while (ok && w.next(g)) {
-            const int K = g.phase ? p.I : p.H;
-            const int n = max(16, (PIECES * L.count[g.a] + 15) & ~15);
-            const uint32_t idesc = IDESC | (static_cast<uint32_t>(n >> 3) << 17);
-            const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
-            if (lane == 0) ok = wait_bar(bar_tempty + 8 * buf, (use & 1) ^ 1, abort_flag, p.wait_ns, p.status);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-            const uint32_t d = tmem + buf * nmax;
-            for (int k = g.k0; k < g.k1; ++k, ++c) {
-                const int st = c % S;
-                if (lane == 0) ok = wait_bar(bar_full + 8 * st, (c / S) & 1, abort_flag, p.wait_ns, p.status);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        // One elected thread runs the whole loop: with a fresh election for each
+        // instruction, and descriptors rebuilt for it, a K-step took 820 cycles to
+        // issue (measured); this form takes 340, below the 700 in which a K-step's
+        // weights arrive.
+        if (elect_one()) {
+            Walk w(p, G, cta, nact);
+            Seg g;
+            int st = 0, tile = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && w.next(g)) {
+                const int K = g.phase ? p.I : p.H;
+                const int n = max(16, (PIECES * L.count[g.a] + 15) & ~15);
+                const uint32_t idesc = IDESC | (static_cast<uint32_t>(n >> 3) << 17);
+                const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
+                ok = wait_bar(bar_tempty + 8 * buf, (use & 1) ^ 1, abort_flag, p.wait_ns, p.status);
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t sf = sf_ring + st * sf_stage, sft = sf_tmem + st * sf_cols;
-                tc_cp_32x128b_warpx4_elect(sft, desc_sf_block(sf));
-                for (uint32_t b = 0; b < nblk; ++b) tc_cp_32x128b_warpx4_elect(sft + 4 + 4 * b, desc_sf_block(sf + 512 + 512 * b));
-                const uint32_t as = ring + st * ab_stage, bs = as + A_BYTES;
-                const int nk = min(4, (K - k * STEP) >> 5);
-                for (int kk = 0; kk < nk; ++kk) {
-                    const uint32_t sel = (static_cast<uint32_t>(kk) << 29) | (static_cast<uint32_t>(kk) << 4);
-                    tc_mma_mxf8_elect(d, desc_kmajor_sw128(as + 32 * kk), desc_kmajor_sw128(bs + 32 * kk), idesc | sel, sft,
-                                      sft + 4, k > g.k0 || kk > 0 ? 1u : 0u);
+                const uint32_t d = tmem + buf * nmax;
+                for (int k = g.k0; k < g.k1; ++k) {
+                    ok = wait_bar(bar_act + 8 * st, ph, abort_flag, p.wait_ns, p.status) &&
+                         wait_bar(bar_w + 8 * st, ph, abort_flag, p.wait_ns, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sf = sf_ring + st * sf_stage, sft = sf_tmem + st * sf_cols;
+                    tc_cp_32x128b_warpx4(sft, desc_sf_block(sf));
+                    tc_cp_32x128b_warpx4(sft + 4, desc_sf_block(sf + 512));
+                    if (n > 128) tc_cp_32x128b_warpx4(sft + 8, desc_sf_block(sf + 1024));
+                    const uint64_t ad = desc_kmajor_sw128(ring + st * ab_stage);
+                    const uint64_t bd = desc_kmajor_sw128(ring + st * ab_stage + A_BYTES);
+                    const int nk = min(4, (K - k * STEP) >> 5);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // (descriptors count in 16 bytes: 32 bytes on per slice)
+                        if (kk < nk)
+                            tc_mma_mxf8(d, ad + 2 * kk, bd + 2 * kk,
+                                        idesc | (static_cast<uint32_t>(kk) << 29) | (static_cast<uint32_t>(kk) << 4), sft,
+                                        sft + 4, k > g.k0 || kk > 0 ? 1u : 0u);
+                    tc_commit(bar_empty + 8 * st);
+                    if (++st == S) { st = 0; ph ^= 1; }
                 }
-                tc_commit_elect(bar_empty + 8 * st);
+                if (!ok) break;
+                tc_commit(bar_tfull + 8 * buf);
+                ++tile;
             }
-            if (!ok) break;
-            tc_commit_elect(bar_tfull + 8 * buf);
-            ++tile;
+            tc_commit(bar_drain);
+            drain_bar(bar_drain, 0, p.wait_ns, p.status);
         }
-        tc_commit_elect(bar_drain);
-        if (lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
         __syncwarp();
-    } else if (warp < 4) {
+    } else if (warp < 4 || warp >= 8) {
         // ------------------------------------------------ loaders: token columns and scales
-        // Thread l of 64 copies weight-scale rows l and l + 64, and its share of
-        // the token rows' 16-byte pieces and scale words.
-        const int l = (warp - 2) * 32 + lane;
-        uint32_t* rows = reinterpret_cast<uint32_t*>(smem + p.off_rows) + (warp - 2) * 256;  // row offset / 16 of each column
-        Walk w(p, G, cta, nact);
-        Seg g;
-        int c = 0, sent = 0;  // K-steps issued and handed over
-        const int lag = S > LAG ? LAG : 1;  // below S: the stage to be refilled has been handed over
-        bool ok = true;
-        // hand over the stages up to `upto` (their copies have completed)
-        auto hand = [&](int upto) {
-            if (p.raw) {
-                for (int q = sent; q < upto; ++q) {
-                    // two aligned words of each row -> the four scale bytes
-                    const uint32_t sf = sf_ring + (q % S) * sf_stage, rb = sf + 512 * (1 + nblk);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = l + 64 * h;
-                        const uint32_t *src = reinterpret_cast<const uint32_t*>(smem + (rb - sbase) + r * 8);
-                        const uint32_t sh = *reinterpret_cast<const uint8_t*>(smem + p.off_rows + 2048 + (q % S) * 128 + r);
-                        st_shared_b32(sf + (r & 31) * 16 + (r >> 5) * 4, __funnelshift_r(src[0], src[1], sh));
-                    }
-                }
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0)
-                for (int q = sent; q < upto; ++q) mbar_arrive(bar_full + 8 * (q % S));
-            sent = upto;
+        // Loader i takes blocks i, i + 3, ... of two K-steps of a tile (an even one
+        // and the next): lane l reads the scale words of weight rows l, l + 32,
+        // l + 64, l + 96 into registers, one of its blocks (6 K-steps) ahead, so
+        // that their HBM latency is hidden; the token rows and their scales come
+        // from L2 by asynchronous copies. Every block is handed over before the
+        // next is begun: a loader that waits for another CTA's h holds nothing
+        // back. A loader's consecutive blocks start at most S K-steps apart (one
+        // K-step a block in rings of fewer than 6), which keeps its waits on the
+        // stages' parity unambiguous: when it asks for K-step c - S, it has seen
+        // c - 2 S done, and c, still to be handed over by itself, cannot be.
+        const int ldr = warp < 4 ? warp - 2 : warp - 6;
+        const int bs = S >= LOADERS * BLOCK ? BLOCK : 1;
+        uint32_t* rows = reinterpret_cast<uint32_t*>(smem + p.off_rows) + ldr * 256;  // source row of each column
+        struct Block {
+            Seg g;
+            int k0, k1, c;  // K-steps of the tile, and the index of the first among the CTA's
         };
-        while (ok && w.next(g)) {
-            const int e = L.act[g.a], nt = L.count[g.a], off = L.off[g.a];
-            const int n = PIECES * nt;
-            const uint8_t* plane = g.phase ? p.s2 : p.s13;
-            const int R = g.phase ? p.H : 2 * p.I, K = g.phase ? p.I : p.H;
-            const size_t plane_bytes = static_cast<size_t>(p.local) * R * (K / 32);
-            const uint8_t* act = g.phase ? p.hq : p.xq;
-            const uint8_t* sact = g.phase ? p.sh : p.sx;
-            const int stride = g.phase ? p.Ip : p.Hp, sstride = g.phase ? p.sh_stride : p.Hp / 32;
-            if (g.phase) {
-                // this expert's h: complete what is in flight first, since other
-                // CTAs may be waiting for tiles that need it
-                if (sent < c) {
-                    cp_async_wait<0>();
-                    hand(c);
+        Walk w(p, G, cta, nact);
+        Seg seg;
+        seg.k0 = seg.k1 = 0;
+        int kpos = 0, cpos = 0, turn = 0;
+        auto next_block = [&](Block& b) {
+            for (;;) {
+                if (kpos >= seg.k1) {
+                    if (!w.next(seg)) return false;
+                    kpos = seg.k0;
                 }
-                if (lane == 0) ok = wait_count(p.counters + 2 + g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
+                b.k0 = kpos;
+                b.k1 = min(seg.k1, (kpos & ~(bs - 1)) + bs);
+                b.c = cpos;
+                kpos = b.k1;
+                cpos += b.k1 - b.k0;
+                const bool mine = turn == ldr;
+                if (++turn == LOADERS) turn = 0;
+                if (mine) {
+                    b.g = seg;
+                    return true;
+                }
+            }
+        };
+        auto fetch = [&](const Block& b, uint32_t (&v)[4][BLOCK]) {
+            const uint8_t* plane = b.g.phase ? p.s2 : p.s13;
+            const int R = b.g.phase ? p.H : 2 * p.I, K32 = (b.g.phase ? p.I : p.H) / 32;
+            const int k = b.k0 & ~(BLOCK - 1), nw = min(BLOCK, b.g.steps - k);  // words (K-steps), fewer at a row's end
+            const size_t base = static_cast<size_t>(L.act[b.g.a]) * R;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                // (rows past the matrix are not stored: any row's scales will do)
+                const int wr = b.g.phase ? min(b.g.rt * TILE + 32 * h + lane, p.H - 1)
+                                         : (h >> 1) * p.I + min(b.g.rt * (TILE / 2) + 32 * (h & 1) + lane, p.I - 1);
+                const size_t at = (base + wr) * K32 + 4 * k;
+                if ((K32 & 7) == 0) {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(plane + at));
+                    v[h][0] = u.x; v[h][1] = u.y;
+                } else if ((K32 & 3) == 0) {
+#pragma unroll
+                    for (int i = 0; i < BLOCK; ++i) v[h][i] = i < nw ? __ldg(reinterpret_cast<const uint32_t*>(plane + at) + i) : 0u;
+                } else {
+                    // rows of any length: aligned words, shifted together (the plane
+                    // is a whole number of words)
+                    const size_t end = static_cast<size_t>(p.local) * R * K32, w0 = at & ~size_t(3);
+                    uint32_t u[BLOCK + 1];
+#pragma unroll
+                    for (int i = 0; i <= BLOCK; ++i)
+                        u[i] = i <= nw && w0 + 4 * i < end ? __ldg(reinterpret_cast<const uint32_t*>(plane + w0) + i) : 0u;
+#pragma unroll
+                    for (int i = 0; i < BLOCK; ++i) v[h][i] = __funnelshift_r(u[i], u[i + 1], static_cast<uint32_t>(at & 3) * 8);
+                }
+            }
+        };
+        bool ok = true;
+        Block b;
+        bool more = next_block(b);
+        uint32_t nxt[4][BLOCK];
+        if (more) fetch(b, nxt);
+        int tab_a = -1, tab_phase = -1;
+        while (more) {
+            const Block cur = b;
+            uint32_t sc[4][BLOCK];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int i = 0; i < BLOCK; ++i) sc[h][i] = nxt[h][i];
+            more = next_block(b);
+            if (more) fetch(b, nxt);
+            const int phase = cur.g.phase, nt = L.count[cur.g.a], n = PIECES * nt;
+            const uint8_t* act = phase ? p.hq : p.xq;
+            const uint8_t* sact = phase ? p.sh : p.sx;
+            const int stride = phase ? p.Ip : p.Hp, sstride = phase ? p.sh_stride : p.Hp / 32;
+            if (tab_a != cur.g.a || tab_phase != phase) {
+                if (phase) {  // this expert's h
+                    if (lane == 0) ok = wait_count(p.counters + 2 + cur.g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                }
+                const int off = L.off[cur.g.a];
+                __syncwarp();
+                for (int r = lane; r < n; r += 32) {
+                    const int pc = r >= nt ? 1 : 0, j = r - pc * nt;
+                    rows[r] = (phase ? off + j : L.entry_of[off + j] / p.top_k) * PIECES + pc;
+                }
+                __syncwarp();
+                tab_a = cur.g.a;
+                tab_phase = phase;
+            }
+            const int nb = cur.k1 - cur.k0;
+            int st = cur.c % S;
+            const int st0 = st;
+            auto hand = [&](int i) {
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_act + 8 * (st0 + i < S ? st0 + i : st0 + i - S));
+            };
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) {
+                if (i >= nb) break;
+                // the stage's last use (K-step c + i - S) has been multiplied
+                if (lane == 0) ok = wait_bar(bar_empty + 8 * st, (((cur.c + i) / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
-            }
-            __syncwarp();
-            for (int r = lane; r < n; r += 32) {
-                const int pc = r >= nt ? 1 : 0, j = r - pc * nt;
-                const int row = g.phase ? off + j : L.entry_of[off + j] / p.top_k;
-                rows[r] = row * PIECES + pc;
-            }
-            __syncwarp();
-            // weight-scale rows of this thread (clamped: rows past the matrix are not stored)
-            size_t srow[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = l + 64 * h;
-                int wr;
-                if (g.phase) wr = min(g.rt * TILE + r, p.H - 1);
-                else wr = h * p.I + min(g.rt * (TILE / 2) + l, p.I - 1);
-                srow[h] = (static_cast<size_t>(e) * R + wr) * (K / 32);
-            }
-            for (int k = g.k0; k < g.k1; ++k, ++c) {
-                const int st = c % S;
-                if (lane == 0) ok = wait_bar(bar_empty + 8 * st, ((c / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                const uint32_t sf = sf_ring + st * sf_stage, bs = ring + st * ab_stage + A_BYTES;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = l + 64 * h;
-                    const size_t at = srow[h] + 4 * k;
-                    if (!p.raw) {
-                        cp_async_4(sf + (r & 31) * 16 + (r >> 5) * 4, plane + at);
-                    } else {
-                        const uint32_t rb = sf + 512 * (1 + nblk) + r * 8;
-                        const size_t w0 = at & ~size_t(3);
-                        cp_async_4(rb, plane + w0);
-                        cp_async_4(rb + 4, plane + (w0 + 8 <= plane_bytes ? w0 + 4 : w0));
-                        smem[p.off_rows + 2048 + st * 128 + r] = static_cast<uint8_t>((at & 3) * 8);
-                    }
-                }
-                for (int r = l; r < n; r += 64)
+                const int k = cur.k0 + i;
+                const bool odd = k & 1;
+                const uint32_t sf = sf_ring + st * sf_stage, bsm = ring + st * ab_stage + A_BYTES;
+                // one 16-byte store: this K-step's scale words of rows l, l + 32, l + 64, l + 96
+                st_shared_v4(sf + lane * 16, odd ? sc[0][1] : sc[0][0], odd ? sc[1][1] : sc[1][0], odd ? sc[2][1] : sc[2][0],
+                             odd ? sc[3][1] : sc[3][0]);
+                for (int r = lane; r < n; r += 32)
                     cp_async_4(sf + 512 + 512 * (r >> 7) + (r & 31) * 16 + ((r >> 5) & 3) * 4,
                                sact + static_cast<size_t>(rows[r]) * sstride + 4 * k);
-                // thread l takes 16-byte piece l % 8 of rows l / 8, l / 8 + 8, ...
-                // (each warp reads the table that it filled itself)
-                const uint32_t chunk = l & 7;
-                for (int r = l >> 3; r < n; r += 8)
-                    cp_async_16(bs + r * 128 + ((chunk ^ (r & 7)) << 4),
+                const uint32_t chunk = lane & 7;  // lane l takes 16-byte piece l % 8 of rows l / 8, l / 8 + 4, ...
+                for (int r = lane >> 3; r < n; r += 4)
+                    cp_async_16(bsm + r * 128 + ((chunk ^ (r & 7)) << 4),
                                 act + static_cast<size_t>(rows[r]) * stride + k * STEP + chunk * 16);
                 cp_async_commit();
-                if (c - sent >= lag) {
-                    if (lag == LAG) cp_async_wait<LAG>();
-                    else cp_async_wait<1>();
-                    hand(c + 1 - lag);
-                }
+                if (++st == S) st = 0;
             }
+            if (!ok) break;
+            if (nb == 2) {
+                cp_async_wait<1>();
+                hand(0);
+            }
+            cp_async_wait<0>();
+            hand(nb - 1);
         }
         cp_async_wait<0>();
-        if (sent < c) hand(c);
     } else {
         // ------------------------------------------------ epilogue (4 warps)
         // Thread = TMEM lane = weight row of the tile. Columns: piece 0 of every
@@ -937,11 +980,10 @@ int launch_moe(const MoeArgs& a) {
     p.part_down = reinterpret_cast<float*>(a.ws + l.part_down);
     p.Hp = l.Hp; p.Ip = l.Ip; p.sh_stride = l.sh_stride; p.ksplit = l.ksplit; p.slots = l.slots; p.n_counters = l.n_counters;
     p.up_tiles = l.up_tiles; p.down_tiles = l.down_tiles; p.up_steps = l.up_steps; p.down_steps = l.down_steps;
-    p.raw = (a.H % STEP) != 0 || (a.I % STEP) != 0;
     p.off_lists = 512;
     p.off_epi = (p.off_lists + l.slots * 10 + a.local * 8 + 127) & ~127u;
     p.off_rows = p.off_epi + 2 * 8 * TILE * 4;
-    p.off_ring = (p.off_rows + 2048 + (p.raw ? MAX_ST * 128 : 0) + 1023) & ~1023u;
+    p.off_ring = (p.off_rows + LOADERS * 1024 + 1023) & ~1023u;
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
 
