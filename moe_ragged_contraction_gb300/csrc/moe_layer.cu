@@ -18,16 +18,18 @@
 //   moe_logits  : router logits (partial sums over slices of H), x as pieces,
 //                 counters to zero.
 //   moe_experts : persistent, one CTA per SM (cooperative launch; a programmatic
-//                 dependent of moe_logits). Chooses the experts, then walks two
-//                 phases without a pause in the weight stream: up/gate tiles
-//                 (64 gate and the same 64 up rows, h = silu(g) u on drain) and
-//                 down tiles (128 rows). Each phase's (expert, tile, K-step)
-//                 sequence is cut into equal contiguous shares, one per CTA; a
-//                 tile cut between CTAs is summed from their partial sums in a
-//                 fixed order (no atomics on data: bit-reproducible). The
-//                 weight producer runs ahead across the phase border while the
-//                 activation loader waits for the expert's h. Last, after a grid
-//                 barrier, the weighted sum over each token's experts.
+//                 dependent of moe_logits). Chooses the experts, then works off
+//                 one queue of tiles: up/gate tiles (64 gate and the same 64 up
+//                 rows, h = silu(g) u on drain), then down tiles (128 rows), by
+//                 expert. A CTA takes the next tile when its weight producer has
+//                 finished with the last one, so that SMs with a slower path to
+//                 memory take fewer; the producer runs ahead of the products (the
+//                 weights of the first down tiles arrive while h is finished).
+//                 Where the tiles are fewer than the SMs, each is cut into parts
+//                 along the contraction, summed in order by the part that ends
+//                 last. No atomics on data: bit-reproducible whoever computes
+//                 what. Last, after a grid barrier, the weighted sum over each
+//                 token's experts.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
@@ -52,6 +54,7 @@ constexpr int LOADERS = 3;
 constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (rings of 6 stages or more; else 1)
 constexpr int SMEM_MAX = 232448;
 constexpr uint32_t TMEM_ALL = 512;
+constexpr int NQ = 4;                // queue entries in flight in a CTA
 constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
 // kind::mxf8f6f4, E4M3 x E4M3, both K-major, E8M0 scales, M = 128
 constexpr uint32_t IDESC = (1u << 23) | (static_cast<uint32_t>(TILE >> 4) << 24);
@@ -66,14 +69,14 @@ struct Params {
     int32_t* user_ids;
     float* user_weights;
     // scratch
-    unsigned int* counters;  // [0], [1] grid barriers; [2 ..] h tiles done per chosen expert; then arrivals per up/gate tile
+    unsigned int* counters;  // [0], [1] grid barriers; [2] queue; [3 ..] h tiles done per chosen expert; then parts done per up/gate tile
     float* logits;           // [ksplit][T][experts]
     int32_t* ids;            // [T][top_k]
     float* weights;
     uint8_t *xq, *sx;        // [T][2][Hp], [T][2][Hp / 32]
     uint8_t *hq, *sh;        // [slots][2][Ip], [slots][2][sh_stride]
     float* y;                // [slots][Hp]
-    float *part_up, *part_down;  // [CTA][2][T][128]
+    float *part_up, *part_down;  // [unit][T][128]
     int Hp, Ip, sh_stride, ksplit, slots, n_counters;
     int up_tiles, down_tiles, up_steps, down_steps;
     uint32_t off_lists, off_epi, off_rows, off_ring;
@@ -125,19 +128,65 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four 32-blocks of a row at a time: lane l holds columns 4 l .. 4 l + 3 of the
+// 128, eight lanes a block; v becomes the pieces' bytes, s0 and s1 their scales.
+__device__ __forceinline__ void split_rows(const Params& p, int first, int stride) {
+    const int lane = threadIdx.x & 31, per = p.Hp / STEP;
+    for (int i = first; i < p.T * per; i += stride) {
+        const int t = i / per, b = i - t * per, h = b * STEP + 4 * lane;
+        uint2 raw = make_uint2(0, 0);
+        if (h < p.H) raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.H + h));
+        float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
+                      __uint_as_float(raw.y & 0xFFFF0000u)};
+        uint32_t s[PIECES];
+#pragma unroll
+        for (int pc = 0; pc < PIECES; ++pc) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+            s[pc] = block_scale(m);
+            if (pc && s[0] == 255u) s[pc] = 255u;
+            const float inv = __uint_as_float((254u - min(s[pc], 254u)) << 23), up = __uint_as_float(s[pc] ? s[pc] << 23 : 0x400000u);
+            uint32_t q = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_fp8_storage_t f = __nv_cvt_float_to_fp8(v[j] * inv, __NV_SATFINITE, __NV_E4M3);
+                q |= static_cast<uint32_t>(f) << (8 * j);
+                v[j] -= __half2float(__half(__nv_cvt_fp8_to_halfraw(f, __NV_E4M3))) * up;
+            }
+            *reinterpret_cast<uint32_t*>(p.xq + (static_cast<size_t>(t) * PIECES + pc) * p.Hp + h) = s[pc] == 255u ? 0x7F7F7F7Fu : q;
+        }
+        if ((lane & 7) == 0) {
+#pragma unroll
+            for (int pc = 0; pc < PIECES; ++pc)
+                p.sx[(static_cast<size_t>(t) * PIECES + pc) * (p.Hp / 32) + 4 * b + (lane >> 3)] = static_cast<uint8_t>(s[pc]);
+        }
+    }
+}
+
 // Block (expert group, token tile, H slice): 16 MF tokens x 8 NF experts, each
 // of 8 warps a share of the slice, joined in shared memory in warp order. A
 // thread's 16 bytes hold eight consecutive values of a row: the same
 // assignment of columns to the MMA's K on both sides, so the sum is the dot
-// product whatever the order. Then every block splits its share of x and
-// zeroes its share of the counters.
+// product whatever the order. The blocks after those split x into pieces and
+// zero the counters.
 template <int MF, int NF>
 __global__ void __launch_bounds__(256) moe_logits(const Params p) {
     __shared__ float red[8][16 * MF][8 * NF];
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
-    const int e0 = blockIdx.x * 8 * NF, t0 = blockIdx.y * 16 * MF;
-    const long long chunks = p.H / 32, nw = 8LL * p.ksplit, wi = blockIdx.z * 8 + warp;
+    const int ge = (p.experts + 8 * NF - 1) / (8 * NF), gt = (p.T + 16 * MF - 1) / (16 * MF);
+    if (static_cast<int>(blockIdx.x) >= ge * gt * p.ksplit) {
+        const int b = blockIdx.x - ge * gt * p.ksplit, nb = gridDim.x - ge * gt * p.ksplit;
+        split_rows(p, b * 8 + warp, nb * 8);
+        for (int i = b * 256 + threadIdx.x; i < p.n_counters; i += nb * 256) p.counters[i] = 0;
+        return;
+    }
+    const int bz = blockIdx.x / (ge * gt), by = (blockIdx.x - bz * ge * gt) / ge, bx = blockIdx.x - (bz * gt + by) * ge;
+    const int e0 = bx * 8 * NF, t0 = by * 16 * MF;
+    const long long chunks = p.H / 32, nw = 8LL * p.ksplit, wi = bz * 8 + warp;
     const int c0 = static_cast<int>(chunks * wi / nw), c1 = static_cast<int>(chunks * (wi + 1) / nw);
     float acc[MF][NF][4] = {};
 #pragma unroll 4
@@ -178,22 +227,8 @@ __global__ void __launch_bounds__(256) moe_logits(const Params p) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) s += red[w][o / (8 * NF)][o % (8 * NF)];
-            p.logits[(static_cast<size_t>(blockIdx.z) * p.T + t) * p.experts + e] = s;
+            p.logits[(static_cast<size_t>(bz) * p.T + t) * p.experts + e] = s;
         }
-    }
-    const int nblk = gridDim.x * gridDim.y * gridDim.z;
-    const int blk = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-    for (int i = blk * 256 + threadIdx.x; i < p.n_counters; i += nblk * 256) p.counters[i] = 0;
-    const int per = p.H / 32;
-    for (int i = blk * 8 + warp; i < p.T * per; i += nblk * 8) {
-        const int t = i / per, b = i - t * per;
-        uint32_t s0, s1;
-        const uint32_t q = split_block(bf16_f(p.x[static_cast<size_t>(t) * p.H + 32 * b + lane]), s0, s1);
-        uint8_t* d = p.xq + static_cast<size_t>(t) * PIECES * p.Hp + 32 * b + lane;
-        d[0] = static_cast<uint8_t>(q);
-        d[p.Hp] = static_cast<uint8_t>(q >> 8);
-        if (lane < PIECES)
-            p.sx[(static_cast<size_t>(t) * PIECES + lane) * (p.Hp / 32) + b] = static_cast<uint8_t>(lane ? s1 : s0);
     }
 }
 
@@ -303,21 +338,6 @@ __device__ __forceinline__ bool wait_count(const unsigned int* p, unsigned int t
     }
 }
 
-// Shares of a phase's K-steps: CTA c of the first min(G, total) takes steps
-// [share(c), share(c + 1)), at least one each.
-__device__ __forceinline__ int share(int c, int total, int G) {
-    const int n = min(G, total);
-    return c >= n ? total : static_cast<int>(static_cast<long long>(c) * total / n);
-}
-
-// The CTA that owns step s.
-__device__ __forceinline__ int owner(int s, int total, int G) {
-    G = min(G, total);
-    const unsigned long long v = (static_cast<unsigned long long>(s) + 1) * G - 1;
-    if (v < (1ull << 32)) return static_cast<int>(static_cast<uint32_t>(v) / static_cast<uint32_t>(total));
-    return static_cast<int>(v / static_cast<unsigned long long>(total));
-}
-
 // Per-CTA lists in shared memory.
 struct Lists {
     float* wts;          // [slots] weight of entry (token, k)
@@ -331,44 +351,42 @@ struct Lists {
     int* info;           // chosen experts, most tokens of one
 };
 
-// A run of K-steps of one tile.
+// Parts into which a phase's tiles are cut along the contraction: enough to
+// give every CTA one, at least four K-steps each. Handing a partial sum over
+// costs several K-steps' time, so tiles that outnumber half the CTAs stay whole.
+__device__ __forceinline__ int parts_of(int tiles, int steps, int G) {
+    return max(1, min(min(G / max(tiles, 1), steps / 4), 8));
+}
+
+// A unit of the queue: K-steps [k0, k1) of a tile.
 struct Seg {
-    int phase, tile, a, rt, k0, k1, steps;
-    bool whole;
+    int phase, tile, a, rt, part, parts, k0, k1, steps;
 };
 
-// The segments of CTA c in order: up/gate tiles, then down tiles.
-struct Walk {
-    int G, c, nact, s, end, phase, total, steps, tiles;
+struct Queue {
+    int nact, up_parts, down_parts, up_units, units;
     const Params& p;
 
-    __device__ __forceinline__ Walk(const Params& p_, int G_, int c_, int nact_) : G(G_), c(c_), nact(nact_), p(p_) { start(0); }
-
-    __device__ __forceinline__ void start(int ph) {
-        phase = ph;
-        steps = ph ? p.down_steps : p.up_steps;
-        tiles = ph ? p.down_tiles : p.up_tiles;
-        total = nact * tiles * steps;
-        s = share(c, total, G);
-        end = share(c + 1, total, G);
+    __device__ __forceinline__ Queue(const Params& p_, int G, int nact_) : nact(nact_), p(p_) {
+        up_parts = parts_of(nact * p.up_tiles, p.up_steps, G);
+        down_parts = parts_of(nact * p.down_tiles, p.down_steps, G);
+        up_units = nact * p.up_tiles * up_parts;
+        units = up_units + nact * p.down_tiles * down_parts;
     }
 
-    __device__ __forceinline__ bool next(Seg& g) {
-        if (s >= end) {
-            if (phase) return false;
-            start(1);
-            if (s >= end) return false;
-        }
-        g.phase = phase;
-        g.steps = steps;
-        g.tile = s / steps;
+    __device__ __forceinline__ Seg get(int u) const {
+        Seg g;
+        g.phase = u >= up_units;
+        const int v = g.phase ? u - up_units : u, tiles = g.phase ? p.down_tiles : p.up_tiles;
+        g.parts = g.phase ? down_parts : up_parts;
+        g.steps = g.phase ? p.down_steps : p.up_steps;
+        g.tile = v / g.parts;
+        g.part = v - g.tile * g.parts;
         g.a = g.tile / tiles;
         g.rt = g.tile - g.a * tiles;
-        g.k0 = s - g.tile * steps;
-        g.k1 = min(steps, g.k0 + end - s);
-        g.whole = g.k0 == 0 && g.k1 == steps;
-        s += g.k1 - g.k0;
-        return true;
+        g.k0 = g.steps * g.part / g.parts;
+        g.k1 = g.steps * (g.part + 1) / g.parts;
+        return g;
     }
 };
 
@@ -382,7 +400,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     const uint32_t bar_w = sbase, bar_act = bar_w + 8 * MAX_ST, bar_empty = bar_act + 8 * MAX_ST,
                    bar_tfull = bar_empty + 8 * MAX_ST, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
-    int* flags = reinterpret_cast<int*>(smem + 8 * (3 * MAX_ST + 5));  // abort, TMEM base, epilogue word x2, chosen, most, barrier ok
+    const uint32_t bar_qf = bar_drain + 8, bar_qe = bar_qf + 8 * NQ;
+    int* flags = reinterpret_cast<int*>(smem + 8 * (3 * MAX_ST + 5 + 2 * NQ));  // abort, TMEM base, epilogue unit x2, chosen, most, barrier ok, -, last part, queue
     volatile int* abort_flag = flags;
     Lists L;
     L.wts = reinterpret_cast<float*>(smem + p.off_lists);
@@ -406,6 +425,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(bar_tempty + 8 * b, 4);
         }
         mbar_init(bar_drain, 1);
+        for (int i = 0; i < NQ; ++i) {
+            mbar_init(bar_qf + 8 * i, 1);            // weight producer: the entry is written
+            mbar_init(bar_qe + 8 * i, 2 + LOADERS);  // MMA issuer, loaders, epilogue have read it
+        }
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm13);
@@ -451,9 +474,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
                 }
             }
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
+                __threadfence();
                 red_release_gpu_add(p.counters, 1);
                 flags[6] = wait_count(p.counters, G, abort_flag, p.wait_ns, p.status) ? 1 : 0;
             }
@@ -533,28 +556,52 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t sf_cols = 4 * (1 + nblk);
     const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;  // accumulators
     const uint32_t sf_tmem = tmem + nbuf * nmax;
+    const Queue queue(p, G, nact);
+    volatile int* entry = flags + 9;  // [NQ] units; -1: no more
+
+    // Reader's side of the queue: the next entry (-1 at the end), or -2 after an abort.
+    auto read_entry = [&](int i) {
+        if (!wait_bar(bar_qf + 8 * (i % NQ), (i / NQ) & 1, abort_flag, p.wait_ns, p.status)) return -2;
+        const int u = entry[i % NQ];
+        mbar_arrive(bar_qe + 8 * (i % NQ));
+        return u;
+    };
 
     if (warp == 0) {
         // ------------------------------------------------ weight producer
         if (lane == 0) {
-            Walk w(p, G, cta, nact);
-            Seg g;
-            int c = 0, st = 0;
+            int c = 0, st = 0, put = 0;
             uint32_t ph = 1;
             bool ok = true;
-            while (ok && w.next(g)) {
-                const CUtensorMap* map = g.phase ? &tm2 : &tm13;
+            // the first unit is the CTA's own index, the others come from the counter
+            // shared by all; each is published while the unit before is copied
+            auto publish = [&](int u) {
+                if (!wait_bar(bar_qe + 8 * (put % NQ), ((put / NQ) & 1) ^ 1, abort_flag, p.wait_ns, p.status)) return false;
+                entry[put % NQ] = u < queue.units ? u : -1;
+                mbar_arrive(bar_qf + 8 * (put % NQ));
+                ++put;
+                return true;
+            };
+            int u = cta;
+            ok = publish(u);
+            while (ok && u < queue.units) {
+                const int un = static_cast<int>(atomicAdd(p.counters + 2, 1u)) + G;
+                const Seg g = queue.get(u);
                 const int e = L.act[g.a];
-                const int r0 = g.phase ? g.rt * TILE : g.rt * (TILE / 2);
-                const int r1 = g.phase ? r0 + TILE / 2 : p.I + r0;
-                for (int k = g.k0; k < g.k1; ++k, ++c) {
-                    if (!wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status)) { ok = false; break; }
-                    const uint32_t dst = ring + st * ab_stage;
-                    mbar_arrive_expect_tx(bar_w + 8 * st, A_BYTES);
-                    tma_load_3d(dst, map, bar_w + 8 * st, k * STEP, r0, e);
-                    tma_load_3d(dst + A_BYTES / 2, map, bar_w + 8 * st, k * STEP, r1, e);
+                const int kp = min(g.k0 + 3, g.k1 - 1);  // (the counter's answer is back by then)
+                for (int k = g.k0; ok && k < g.k1; ++k) {
+                    if (k == kp) ok = publish(un);
+                    if (!ok) break;
+                    ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
+                    if (!ok) break;
+                    const uint32_t dst = ring + st * ab_stage, bar = bar_w + 8 * st;
+                    mbar_arrive_expect_tx(bar, A_BYTES);
+                    if (g.phase) tma_load_3d(dst, &tm2, bar, k * STEP, g.rt * TILE, e);
+                    else tma_load_4d(dst, &tm13, bar, k * STEP, g.rt * (TILE / 2), 0, e);
+                    ++c;
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
+                u = un;
             }
             if (!ok || *abort_flag)  // every copy in flight lands before the CTA exits
                 for (int d = 1; d <= min(c, S); ++d) drain_bar(bar_w + 8 * ((c - d) % S), ((c - d) / S) & 1, p.wait_ns, p.status);
@@ -567,12 +614,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         // issue (measured); this form takes 340, below the 700 in which a K-step's
         // weights arrive.
         if (elect_one()) {
-            Walk w(p, G, cta, nact);
-            Seg g;
             int st = 0, tile = 0;
             uint32_t ph = 0;
             bool ok = true;
-            while (ok && w.next(g)) {
+            while (ok) {
+                const int u = read_entry(tile);
+                if (u < 0) break;
+                const Seg g = queue.get(u);
                 const int K = g.phase ? p.I : p.H;
                 const int n = max(16, (PIECES * L.count[g.a] + 15) & ~15);
                 const uint32_t idesc = IDESC | (static_cast<uint32_t>(n >> 3) << 17);
@@ -628,14 +676,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             Seg g;
             int k0, k1, c;  // K-steps of the tile, and the index of the first among the CTA's
         };
-        Walk w(p, G, cta, nact);
         Seg seg;
         seg.k0 = seg.k1 = 0;
-        int kpos = 0, cpos = 0, turn = 0;
-        auto next_block = [&](Block& b) {
+        int kpos = 0, cpos = 0, turn = 0, got = 0;
+        // The loader's next block: 1 found, 0 no more, 2 not yet known (the next
+        // unit is not published; only when not told to wait).
+        auto next_block = [&](Block& b, bool wait) {
             for (;;) {
                 if (kpos >= seg.k1) {
-                    if (!w.next(seg)) return false;
+                    int u = -3;
+                    if (lane == 0 && (wait || mbar_try_wait(bar_qf + 8 * (got % NQ), (got / NQ) & 1))) u = read_entry(got);
+                    u = __shfl_sync(0xffffffffu, u, 0);
+                    if (u == -3) return 2;
+                    if (u < 0) return 0;
+                    ++got;
+                    seg = queue.get(u);
                     kpos = seg.k0;
                 }
                 b.k0 = kpos;
@@ -647,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (++turn == LOADERS) turn = 0;
                 if (mine) {
                     b.g = seg;
-                    return true;
+                    return 1;
                 }
             }
         };
@@ -683,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         };
         bool ok = true;
         Block b;
-        bool more = next_block(b);
+        int more = next_block(b, true);
         uint32_t nxt[4][BLOCK];
         if (more) fetch(b, nxt);
         int tab_a = -1, tab_phase = -1;
@@ -694,15 +749,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int h = 0; h < 4; ++h)
 #pragma unroll
                 for (int i = 0; i < BLOCK; ++i) sc[h][i] = nxt[h][i];
-            more = next_block(b);
-            if (more) fetch(b, nxt);
+            more = next_block(b, false);
+            if (more == 1) fetch(b, nxt);
             const int phase = cur.g.phase, nt = L.count[cur.g.a], n = PIECES * nt;
             const uint8_t* act = phase ? p.hq : p.xq;
             const uint8_t* sact = phase ? p.sh : p.sx;
             const int stride = phase ? p.Ip : p.Hp, sstride = phase ? p.sh_stride : p.Hp / 32;
             if (tab_a != cur.g.a || tab_phase != phase) {
                 if (phase) {  // this expert's h
-                    if (lane == 0) ok = wait_count(p.counters + 2 + cur.g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
+                    if (lane == 0) ok = wait_count(p.counters + 3 + cur.g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     if (!ok) break;
                 }
@@ -754,6 +809,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             cp_async_wait<0>();
             hand(nb - 1);
+            if (more == 2) {
+                more = next_block(b, true);
+                if (more) fetch(b, nxt);
+            }
         }
         cp_async_wait<0>();
     } else {
@@ -762,8 +821,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         // token, then piece 1; their sum is the product.
         const int q = warp - 4, row = threadIdx.x - 128;
         float* xch = reinterpret_cast<float*>(smem + p.off_epi);  // [2][8 tokens][128 rows]
-        Walk w(p, G, cta, nact);
-        Seg g;
         int tile = 0;
         // h of 32 inner rows of one token: two pieces and their scales
         auto store_h = [&](int slot, int i0, float gate, float up) {
@@ -776,18 +833,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane < PIECES)
                 p.sh[(static_cast<size_t>(slot) * PIECES + lane) * p.sh_stride + (i0 >> 5)] = static_cast<uint8_t>(lane ? s1 : s0);
         };
-        while (w.next(g)) {
+        for (;;) {
             const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
-            const int nt = L.count[g.a], off = L.off[g.a];
-            if (q == 0 && lane == 0)
-                flags[2 + (tile & 1)] = wait_bar(bar_tfull + 8 * buf, use & 1, abort_flag, p.wait_ns, p.status) ? 1 : 0;
+            if (q == 0 && lane == 0) {
+                int u = read_entry(tile);
+                if (u >= 0 && !wait_bar(bar_tfull + 8 * buf, use & 1, abort_flag, p.wait_ns, p.status)) u = -2;
+                flags[2 + (tile & 1)] = u;
+            }
             named_bar_sync(EPI_BAR, 128);
-            if (!flags[2 + (tile & 1)]) break;
+            const int unit = flags[2 + (tile & 1)];
+            if (unit < 0) break;
+            const Seg g = queue.get(unit);
+            const int nt = L.count[g.a], off = L.off[g.a];
+            const bool whole = g.parts == 1;
             ++tile;
             tc_fence_after();
             const uint32_t d = tmem + buf * nmax + (static_cast<uint32_t>(q * 32) << 16);
-            float* part = (g.phase ? p.part_down : p.part_up) +
-                          (static_cast<size_t>(cta) * 2 + (g.k0 > 0 ? 0 : 1)) * p.T * TILE;
+            float* part = g.phase ? p.part_down + static_cast<size_t>(unit - queue.up_units) * p.T * TILE
+                                  : p.part_up + static_cast<size_t>(unit) * p.T * TILE;
             for (int j0 = 0; j0 < nt; j0 += 8) {
                 uint32_t v0[8], v1[8];
                 tmem_ld_32x32b_x8(d + j0, v0);
@@ -798,7 +861,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float v[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(v0[j]) + __uint_as_float(v1[j]);
-                if (!g.whole) {
+                if (!whole) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (j0 + j < nt) part[(j0 + j) * TILE + row] = v[j];
@@ -825,37 +888,35 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
             if (g.phase == 0) {
-                bool finish = g.whole;
-                if (!g.whole) {
-                    // the last CTA to bring its part of the tile sums all of them, in CTA order
-                    const int total = nact * p.up_tiles * p.up_steps;
-                    const int cf = owner(g.tile * p.up_steps, total, G), cl = owner((g.tile + 1) * p.up_steps - 1, total, G);
-                    __threadfence();
+                bool finish = whole;
+                if (!whole) {
+                    // the part that ends last sums all of them, in order
                     named_bar_sync(EPI_BAR, 128);
-                    if (q == 0 && lane == 0)
-                        flags[8] = atom_acq_rel_gpu_add(p.counters + 2 + p.local + g.tile, 1) == static_cast<uint32_t>(cl - cf) ? 1 : 0;
+                    if (q == 0 && lane == 0) {
+                        __threadfence();
+                        flags[8] = atom_acq_rel_gpu_add(p.counters + 3 + p.local + g.tile, 1) == static_cast<uint32_t>(g.parts - 1) ? 1 : 0;
+                        __threadfence();
+                    }
                     named_bar_sync(EPI_BAR, 128);
                     finish = flags[8] != 0;
-                    if (finish) {
-                        __threadfence();
-                        for (int o = q; o < 2 * nt; o += 4) {
-                            const int j = o >> 1, i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
-                            if (i0 >= p.I) continue;
-                            float gate = 0.f, up = 0.f;
-                            for (int cc = cf; cc <= cl; ++cc) {
-                                const float* src = p.part_up + (static_cast<size_t>(cc) * 2 + (cc == cf ? 1 : 0)) * p.T * TILE +
-                                                   static_cast<size_t>(j) * TILE;
-                                gate += __ldcg(src + i);
-                                up += __ldcg(src + TILE / 2 + i);
-                            }
-                            store_h(off + j, i0, gate, up);
+                    for (int o = q; finish && o < 2 * nt; o += 4) {
+                        const int j = o >> 1, i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
+                        if (i0 >= p.I) continue;
+                        float gate = 0.f, up = 0.f;
+                        const float* src = p.part_up + static_cast<size_t>(g.tile * g.parts) * p.T * TILE + static_cast<size_t>(j) * TILE;
+                        for (int c = 0; c < g.parts; ++c, src += static_cast<size_t>(p.T) * TILE) {
+                            gate += __ldcg(src + i);
+                            up += __ldcg(src + TILE / 2 + i);
                         }
+                        store_h(off + j, i0, gate, up);
                     }
                 }
                 if (finish) {
-                    __threadfence();
                     named_bar_sync(EPI_BAR, 128);
-                    if (q == 0 && lane == 0) red_release_gpu_add(p.counters + 2 + g.a, 1);
+                    if (q == 0 && lane == 0) {
+                        __threadfence();
+                        red_release_gpu_add(p.counters + 3 + g.a, 1);
+                    }
                 }
             }
         }
@@ -863,13 +924,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     // ---- every product is in y or a partial: grid barrier, then the weighted sum
     tc_fence_before();
-    __threadfence();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_single(tmem, TMEM_ALL);
     if (threadIdx.x == 0) {
         bool ok = !*abort_flag;
         if (ok && nact) {
+            __threadfence();
             red_release_gpu_add(p.counters + 1, 1);
             ok = wait_count(p.counters + 1, G, abort_flag, p.wait_ns, p.status);
         }
@@ -877,7 +938,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncthreads();
     if (!flags[6]) return;
-    const int total = nact * p.down_tiles * p.down_steps, half = p.H / 2;
+    const int half = p.H / 2;
     for (int o = cta * THREADS + threadIdx.x; o < p.T * half; o += G * THREADS) {
         const int t = o / half, n = 2 * (o - t * half), rt = n / TILE, r = n - rt * TILE;
         float y0 = 0.f, y1 = 0.f;
@@ -885,16 +946,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int i = t * p.top_k + k, e = L.eid[i];
             if (e == 0xffff) continue;
             const int a = L.act_of[e], slot = L.slot_of[i], tl = a * p.down_tiles + rt;
-            const int cf = owner(tl * p.down_steps, total, G), cl = owner((tl + 1) * p.down_steps - 1, total, G);
-            if (cf == cl) {
+            if (queue.down_parts == 1) {
                 const float2 v = __ldcg(reinterpret_cast<const float2*>(p.y + static_cast<size_t>(slot) * p.Hp + n));
                 y0 += v.x;
                 y1 += v.y;
             } else {
                 float z0 = 0.f, z1 = 0.f;
-                for (int cc = cf; cc <= cl; ++cc) {
+                for (int c = 0; c < queue.down_parts; ++c) {
                     const float2 v = __ldcg(reinterpret_cast<const float2*>(
-                        p.part_down + (static_cast<size_t>(cc) * 2 + (cc == cf ? 1 : 0)) * p.T * TILE +
+                        p.part_down + (static_cast<size_t>(tl) * queue.down_parts + c) * p.T * TILE +
                         static_cast<size_t>(slot - L.off[a]) * TILE + r));
                     z0 += v.x;
                     z1 += v.y;
@@ -934,7 +994,7 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
     l->down_steps = l->Ip / STEP;
     l->slots = T * top_k;
     l->local_slots = top_k < local ? T * top_k : T * local;
-    l->n_counters = 2 + local + local * l->up_tiles;
+    l->n_counters = 3 + local + local * l->up_tiles;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
     l->counters = take(4 * static_cast<size_t>(l->n_counters));
@@ -946,8 +1006,8 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
     l->hq = take(static_cast<size_t>(l->local_slots) * PIECES * l->Ip);
     l->sh = take(static_cast<size_t>(l->local_slots) * PIECES * l->sh_stride);
     l->y = take(4 * static_cast<size_t>(l->local_slots) * l->Hp);
-    l->part_up = take(4 * static_cast<size_t>(sms) * 2 * T * TILE);
-    l->part_down = take(4 * static_cast<size_t>(sms) * 2 * T * TILE);
+    l->part_up = take(4 * static_cast<size_t>(sms) * T * TILE);  // (parts are only made up to one per SM)
+    l->part_down = take(4 * static_cast<size_t>(sms) * T * TILE);
     l->total = at;
 }
 
@@ -988,14 +1048,13 @@ int launch_moe(const MoeArgs& a) {
     p.status = a.status;
 
     CUtensorMap m13, m2;
-    const uint32_t box[3] = {STEP, TILE / 2, 1};
-    const uint64_t d13[3] = {static_cast<uint64_t>(a.H), 2 * static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.local)};
-    const uint64_t st13[2] = {static_cast<uint64_t>(a.H), 2 * static_cast<uint64_t>(a.I) * a.H};
-    const uint64_t d2[3] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.H), static_cast<uint64_t>(a.local)};
-    const uint64_t st2[2] = {static_cast<uint64_t>(a.I), static_cast<uint64_t>(a.H) * a.I};
-    int rc = host_tensor_map(&m13, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w13, d13, st13, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    // w13 as [local][2][I][H]: one box holds 64 gate rows and the same 64 up rows
+    const uint32_t b13[4] = {STEP, TILE / 2, 2, 1}, b2[3] = {STEP, TILE, 1};
+    const uint64_t H = a.H, I = a.I, E = a.local;
+    const uint64_t d13[4] = {H, I, 2, E}, st13[3] = {H, I * H, 2 * I * H}, d2[3] = {I, H, E}, st2[2] = {I, H * I};
+    int rc = host_tensor_map(&m13, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w13, d13, st13, b13, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
-    rc = host_tensor_map(&m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w2, d2, st2, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    rc = host_tensor_map(&m2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w2, d2, st2, b2, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc) return rc;
 
     static std::atomic<bool> ready[64];
@@ -1005,9 +1064,11 @@ int launch_moe(const MoeArgs& a) {
         if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s", cudaGetErrorString(e));
         ready[a.dev].store(true, std::memory_order_relaxed);
     }
-    const dim3 grid((a.experts + 8 * l.nf - 1) / (8 * l.nf), (a.T + 16 * l.mf - 1) / (16 * l.mf), l.ksplit);
-    if (l.mf == 2) moe_logits<2, 4><<<grid, 256, 0, a.stream>>>(p);
-    else moe_logits<1, 2><<<grid, 256, 0, a.stream>>>(p);
+    const int lblocks = ((a.experts + 8 * l.nf - 1) / (8 * l.nf)) * ((a.T + 16 * l.mf - 1) / (16 * l.mf)) * l.ksplit;
+    int sblocks = (a.T * (l.Hp / STEP) + 7) / 8;  // one 128-column piece of a row per warp, up to 304 blocks
+    if (sblocks > 304) sblocks = 304;
+    if (l.mf == 2) moe_logits<2, 4><<<lblocks + sblocks, 256, 0, a.stream>>>(p);
+    else moe_logits<1, 2><<<lblocks + sblocks, 256, 0, a.stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "router kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
