@@ -53,6 +53,7 @@ constexpr int THREADS = 288;         // warps: 0 weight producer, 1 MMA issuer, 
 constexpr int LOADERS = 3;
 constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (rings of 6 stages or more; else 1)
 constexpr int SMEM_MAX = 232448;
+constexpr int SMEM_FEW = 221184;      // leaves room beside a moe_logits<1, 2> block: the next kernel's CTAs start under it
 constexpr uint32_t TMEM_ALL = 512;
 constexpr int NQ = 4;                // queue entries in flight in a CTA
 constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
@@ -79,7 +80,7 @@ struct Params {
     float *part_up, *part_down;  // [unit][T][128]
     int Hp, Ip, sh_stride, ksplit, slots, n_counters;
     int up_tiles, down_tiles, up_steps, down_steps;
-    uint32_t off_lists, off_epi, off_rows, off_ring;
+    uint32_t off_lists, off_epi, off_rows, off_ring, smem;
     unsigned long long wait_ns;
     int* status;
 };
@@ -243,13 +244,18 @@ __device__ __forceinline__ uint32_t sort_key(float v) {
 
 // One warp: the choice of token t. Lane l holds experts l, l + 32, ...
 // in the shared arrays (score, key: [experts] each).
-__device__ __forceinline__ void choose(const Params& p, int t, float* score, uint32_t* key, int32_t* ids, float* wts) {
+__device__ __noinline__ void choose(const Params& p, int t, float* score, uint32_t* key, int32_t* ids, float* wts) {
     const int lane = threadIdx.x & 31;
     const unsigned full = 0xffffffffu;
     float m = -CUDART_INF_F;
+#pragma unroll 2
     for (int e = lane; e < p.experts; e += 32) {
-        float s = 0.f;
-        for (int k = 0; k < p.ksplit; ++k) s += __ldcg(p.logits + (static_cast<size_t>(k) * p.T + t) * p.experts + e);
+        float v[8], s = 0.f;  // (ksplit is at most 8: all loads in flight together)
+        const float* src = p.logits + static_cast<size_t>(t) * p.experts + e;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < p.ksplit ? __ldcg(src + static_cast<size_t>(k) * p.T * p.experts) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
         score[e] = s;
         m = fmaxf(m, s);
     }
@@ -297,9 +303,11 @@ __device__ __forceinline__ void choose(const Params& p, int t, float* score, uin
 
 // ============================================================== experts
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns,
-                                         int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Bounded waits. The polling loops are kept out of line: a CTA's first pass
+// through its code misses the instruction cache all along, so the roles' code
+// is kept short.
+__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns,
+                                           int* status) {
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         if (mbar_try_wait_suspend(bar, parity, 20000)) return true;
@@ -312,7 +320,12 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigned long long ns, int* status) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns,
+                                         int* status) {
+    return mbar_try_wait(bar, parity) || wait_bar_slow(bar, parity, abort_flag, ns, status);
+}
+
+__device__ __noinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigned long long ns, int* status) {
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
         if (global_timer_ns() - t0 > ns) {
@@ -322,9 +335,8 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigne
 }
 
 // Bounded wait until *p >= target (acquire).
-__device__ __forceinline__ bool wait_count(const unsigned int* p, unsigned int target, volatile int* abort_flag,
+__device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int target, volatile int* abort_flag,
                                            unsigned long long ns, int* status) {
-    if (ld_acquire_gpu(p) >= target) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         if (ld_acquire_gpu(p) >= target) return true;
@@ -334,8 +346,21 @@ __device__ __forceinline__ bool wait_count(const unsigned int* p, unsigned int t
             atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
             return false;
         }
-        __nanosleep(32);
+        __nanosleep(20);
     }
+}
+
+// One warp: h = silu(gate) up of 32 inner rows of one token, as two pieces and their scales.
+__device__ __noinline__ void store_h(const Params& p, int slot, int i0, float gate, float up) {
+    const int lane = threadIdx.x & 31;
+    const float h = gate / (1.f + expf(-gate)) * up;
+    uint32_t s0, s1;
+    const uint32_t pc = split_block(h, s0, s1);
+    uint8_t* d = p.hq + static_cast<size_t>(slot) * PIECES * p.Ip + i0 + lane;
+    d[0] = static_cast<uint8_t>(pc);
+    d[p.Ip] = static_cast<uint8_t>(pc >> 8);
+    if (lane < PIECES)
+        p.sh[(static_cast<size_t>(slot) * PIECES + lane) * p.sh_stride + (i0 >> 5)] = static_cast<uint8_t>(lane ? s1 : s0);
 }
 
 // Per-CTA lists in shared memory.
@@ -355,7 +380,7 @@ struct Lists {
 // give every CTA one, at least four K-steps each. Handing a partial sum over
 // costs several K-steps' time, so tiles that outnumber half the CTAs stay whole.
 __device__ __forceinline__ int parts_of(int tiles, int steps, int G) {
-    return max(1, min(min(G / max(tiles, 1), steps / 4), 8));
+    return 2 * tiles > G ? 1 : max(1, min(min(G / max(tiles, 1), steps / 4), 8));
 }
 
 // A unit of the queue: K-steps [k0, k1) of a tile.
@@ -380,12 +405,17 @@ struct Queue {
         const int v = g.phase ? u - up_units : u, tiles = g.phase ? p.down_tiles : p.up_tiles;
         g.parts = g.phase ? down_parts : up_parts;
         g.steps = g.phase ? p.down_steps : p.up_steps;
-        g.tile = v / g.parts;
-        g.part = v - g.tile * g.parts;
-        g.a = g.tile / tiles;
+        g.tile = v;
+        g.part = g.k0 = 0;
+        g.k1 = g.steps;
+        if (g.parts > 1) {
+            g.tile = v / g.parts;
+            g.part = v - g.tile * g.parts;
+            g.k0 = g.steps * g.part / g.parts;
+            g.k1 = g.steps * (g.part + 1) / g.parts;
+        }
+        g.a = static_cast<uint32_t>(g.tile) / static_cast<uint32_t>(tiles);
         g.rt = g.tile - g.a * tiles;
-        g.k0 = g.steps * g.part / g.parts;
-        g.k1 = g.steps * (g.part + 1) / g.parts;
         return g;
     }
 };
@@ -551,7 +581,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t nblk = (nmax + 127) / 128;
     const uint32_t sf_stage = 512 * (1 + nblk);
     const uint32_t ab_stage = A_BYTES + nmax * STEP;
-    const int S = min(MAX_ST, static_cast<int>((SMEM_MAX - 1024 - p.off_ring) / (ab_stage + sf_stage)));
+    const int S = min(MAX_ST, static_cast<int>((p.smem - 1024 - p.off_ring) / (ab_stage + sf_stage)));
     const uint32_t ring = sbase + p.off_ring, sf_ring = ring + S * ab_stage;
     const uint32_t sf_cols = 4 * (1 + nblk);
     const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;  // accumulators
@@ -570,6 +600,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------ weight producer
         if (lane == 0) {
+            const uint64_t once = l2_evict_first();  // weights leave L2 first: it keeps the code, x, h and partial sums
             int c = 0, st = 0, put = 0;
             uint32_t ph = 1;
             bool ok = true;
@@ -596,8 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!ok) break;
                     const uint32_t dst = ring + st * ab_stage, bar = bar_w + 8 * st;
                     mbar_arrive_expect_tx(bar, A_BYTES);
-                    if (g.phase) tma_load_3d(dst, &tm2, bar, k * STEP, g.rt * TILE, e);
-                    else tma_load_4d(dst, &tm13, bar, k * STEP, g.rt * (TILE / 2), 0, e);
+                    if (g.phase) tma_load_3d(dst, &tm2, bar, k * STEP, g.rt * TILE, e, once);
+                    else tma_load_4d(dst, &tm13, bar, k * STEP, g.rt * (TILE / 2), 0, e, once);
                     ++c;
                     if (++st == S) { st = 0; ph ^= 1; }
                 }
@@ -674,11 +705,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t* rows = reinterpret_cast<uint32_t*>(smem + p.off_rows) + ldr * 256;  // source row of each column
         struct Block {
             Seg g;
-            int k0, k1, c;  // K-steps of the tile, and the index of the first among the CTA's
+            int k0, k1, st;  // K-steps of the tile, and the first one's stage
+            uint32_t ph;     // parity of the stage's last use
         };
         Seg seg;
         seg.k0 = seg.k1 = 0;
-        int kpos = 0, cpos = 0, turn = 0, got = 0;
+        int kpos = 0, spos = 0, turn = 0, got = 0;
+        uint32_t sph = 1;
         // The loader's next block: 1 found, 0 no more, 2 not yet known (the next
         // unit is not published; only when not told to wait).
         auto next_block = [&](Block& b, bool wait) {
@@ -695,9 +728,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 b.k0 = kpos;
                 b.k1 = min(seg.k1, (kpos & ~(bs - 1)) + bs);
-                b.c = cpos;
+                b.st = spos;
+                b.ph = sph;
                 kpos = b.k1;
-                cpos += b.k1 - b.k0;
+                spos += b.k1 - b.k0;
+                if (spos >= S) { spos -= S; sph ^= 1; }
                 const bool mine = turn == ldr;
                 if (++turn == LOADERS) turn = 0;
                 if (mine) {
@@ -720,9 +755,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if ((K32 & 7) == 0) {
                     const uint2 u = __ldg(reinterpret_cast<const uint2*>(plane + at));
                     v[h][0] = u.x; v[h][1] = u.y;
-                } else if ((K32 & 3) == 0) {
-#pragma unroll
-                    for (int i = 0; i < BLOCK; ++i) v[h][i] = i < nw ? __ldg(reinterpret_cast<const uint32_t*>(plane + at) + i) : 0u;
                 } else {
                     // rows of any length: aligned words, shifted together (the plane
                     // is a whole number of words)
@@ -737,20 +769,25 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         };
         bool ok = true;
-        Block b;
-        int more = next_block(b, true);
+        Block cur, b;
         uint32_t nxt[4][BLOCK];
-        if (more) fetch(b, nxt);
         int tab_a = -1, tab_phase = -1;
-        while (more) {
-            const Block cur = b;
+        bool have = false;
+        for (;;) {
             uint32_t sc[4][BLOCK];
+            cur = b;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
 #pragma unroll
                 for (int i = 0; i < BLOCK; ++i) sc[h][i] = nxt[h][i];
-            more = next_block(b, false);
+            // waits for the next unit only with no block in hand
+            const int more = next_block(b, !have);
             if (more == 1) fetch(b, nxt);
+            if (!have) {
+                if (more == 0) break;
+                have = true;
+                continue;
+            }
             const int phase = cur.g.phase, nt = L.count[cur.g.a], n = PIECES * nt;
             const uint8_t* act = phase ? p.hq : p.xq;
             const uint8_t* sact = phase ? p.sh : p.sx;
@@ -772,7 +809,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tab_phase = phase;
             }
             const int nb = cur.k1 - cur.k0;
-            int st = cur.c % S;
+            int st = cur.st;
+            uint32_t ph = cur.ph;
             const int st0 = st;
             auto hand = [&](int i) {
                 fence_proxy_async_shared();
@@ -782,8 +820,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < BLOCK; ++i) {
                 if (i >= nb) break;
-                // the stage's last use (K-step c + i - S) has been multiplied
-                if (lane == 0) ok = wait_bar(bar_empty + 8 * st, (((cur.c + i) / S) & 1) ^ 1, abort_flag, p.wait_ns, p.status);
+                // the stage's last use has been multiplied
+                if (lane == 0) ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
                 const int k = cur.k0 + i;
@@ -800,7 +838,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     cp_async_16(bsm + r * 128 + ((chunk ^ (r & 7)) << 4),
                                 act + static_cast<size_t>(rows[r]) * stride + k * STEP + chunk * 16);
                 cp_async_commit();
-                if (++st == S) st = 0;
+                if (++st == S) { st = 0; ph ^= 1; }
             }
             if (!ok) break;
             if (nb == 2) {
@@ -809,10 +847,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             cp_async_wait<0>();
             hand(nb - 1);
-            if (more == 2) {
-                more = next_block(b, true);
-                if (more) fetch(b, nxt);
-            }
+            if (more == 0) break;
+            have = more == 1;
         }
         cp_async_wait<0>();
     } else {
@@ -822,17 +858,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int q = warp - 4, row = threadIdx.x - 128;
         float* xch = reinterpret_cast<float*>(smem + p.off_epi);  // [2][8 tokens][128 rows]
         int tile = 0;
-        // h of 32 inner rows of one token: two pieces and their scales
-        auto store_h = [&](int slot, int i0, float gate, float up) {
-            const float h = gate / (1.f + expf(-gate)) * up;
-            uint32_t s0, s1;
-            const uint32_t pc = split_block(h, s0, s1);
-            uint8_t* d = p.hq + static_cast<size_t>(slot) * PIECES * p.Ip + i0 + lane;
-            d[0] = static_cast<uint8_t>(pc);
-            d[p.Ip] = static_cast<uint8_t>(pc >> 8);
-            if (lane < PIECES)
-                p.sh[(static_cast<size_t>(slot) * PIECES + lane) * p.sh_stride + (i0 >> 5)] = static_cast<uint8_t>(lane ? s1 : s0);
-        };
         for (;;) {
             const int buf = nbuf == 2 ? tile & 1 : 0, use = nbuf == 2 ? tile >> 1 : tile;
             if (q == 0 && lane == 0) {
@@ -877,10 +902,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int j = 0; j < 8; ++j) x[j * TILE + row] = v[j];
                     named_bar_sync(EPI_BAR, 128);
                     // warp q: tokens j0 + 2q, j0 + 2q + 1, both halves of the 64 inner rows
-#pragma unroll
+#pragma unroll 1
                     for (int o = 0; o < 4; ++o) {
                         const int j = 2 * q + (o >> 1), i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
-                        if (j0 + j < nt && i0 < p.I) store_h(off + j0 + j, i0, x[j * TILE + i], x[j * TILE + TILE / 2 + i]);
+                        if (j0 + j < nt && i0 < p.I) store_h(p, off + j0 + j, i0, x[j * TILE + i], x[j * TILE + TILE / 2 + i]);
                     }
                 }
             }
@@ -908,7 +933,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             gate += __ldcg(src + i);
                             up += __ldcg(src + TILE / 2 + i);
                         }
-                        store_h(off + j, i0, gate, up);
+                        store_h(p, off + j, i0, gate, up);
                     }
                 }
                 if (finish) {
@@ -1044,6 +1069,7 @@ int launch_moe(const MoeArgs& a) {
     p.off_epi = (p.off_lists + l.slots * 10 + a.local * 8 + 127) & ~127u;
     p.off_rows = p.off_epi + 2 * 8 * TILE * 4;
     p.off_ring = (p.off_rows + LOADERS * 1024 + 1023) & ~1023u;
+    p.smem = l.mf == 1 ? SMEM_FEW : SMEM_MAX;
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
 
@@ -1074,7 +1100,7 @@ int launch_moe(const MoeArgs& a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.num_sms);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_MAX;
+    cfg.dynamicSmemBytes = p.smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
