@@ -17,8 +17,8 @@
 // Two kernels per call:
 //   moe_logits  : router logits (partial sums over slices of H), x as pieces,
 //                 counters to zero.
-//   moe_experts : persistent, one CTA per SM (cooperative launch; a programmatic
-//                 dependent of moe_logits). Chooses the experts, then works off
+//   moe_experts : persistent, one CTA per SM (a programmatic dependent of
+//                 moe_logits). Chooses the experts, then works off
 //                 one queue of tiles: up/gate tiles (64 gate and the same 64 up
 //                 rows, h = silu(g) u on drain), then down tiles (128 rows), by
 //                 expert. A CTA takes the next tile when its weight producer has
@@ -28,8 +28,8 @@
 //                 Where the tiles are fewer than the SMs, each is cut into parts
 //                 along the contraction, summed in order by the part that ends
 //                 last. No atomics on data: bit-reproducible whoever computes
-//                 what. Last, after a grid barrier, the weighted sum over each
-//                 token's experts.
+//                 what. Last, when all tiles are done, the weighted sum over
+//                 each token's experts.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
@@ -55,6 +55,8 @@ constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (r
 constexpr int SMEM_MAX = 232448;
 constexpr int SMEM_FEW = 221184;      // leaves room beside a moe_logits<1, 2> block: the next kernel's CTAs start under it
 constexpr uint32_t TMEM_ALL = 512;
+// counters: tokens claimed and chosen for, units claimed, down units done
+constexpr int C_CLAIM = 0, C_CHOSEN = 1, C_QUEUE = 2, C_DONE = 3, C_H = 4;
 constexpr int NQ = 4;                // queue entries in flight in a CTA
 constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
 // kind::mxf8f6f4, E4M3 x E4M3, both K-major, E8M0 scales, M = 128
@@ -70,7 +72,7 @@ struct Params {
     int32_t* user_ids;
     float* user_weights;
     // scratch
-    unsigned int* counters;  // [0], [1] grid barriers; [2] queue; [3 ..] h tiles done per chosen expert; then parts done per up/gate tile
+    unsigned int* counters;  // C_* below; then h tiles done per chosen expert; then parts done per up/gate tile
     float* logits;           // [ksplit][T][experts]
     int32_t* ids;            // [T][top_k]
     float* weights;
@@ -177,6 +179,7 @@ template <int MF, int NF>
 __global__ void __launch_bounds__(256) moe_logits(const Params p) {
     __shared__ float red[8][16 * MF][8 * NF];
     griddep_launch_dependents();
+    griddep_wait();  // x may come from the kernel before, and a call before may still use the scratch
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
     const int ge = (p.experts + 8 * NF - 1) / (8 * NF), gt = (p.T + 16 * MF - 1) / (16 * MF);
     if (static_cast<int>(blockIdx.x) >= ge * gt * p.ksplit) {
@@ -242,23 +245,28 @@ __device__ __forceinline__ uint32_t sort_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One warp: the choice of token t. Lane l holds experts l, l + 32, ...
-// in the shared arrays (score, key: [experts] each).
-__device__ __noinline__ void choose(const Params& p, int t, float* score, uint32_t* key, int32_t* ids, float* wts) {
-    const int lane = threadIdx.x & 31;
-    const unsigned full = 0xffffffffu;
-    float m = -CUDART_INF_F;
-#pragma unroll 2
-    for (int e = lane; e < p.experts; e += 32) {
-        float v[8], s = 0.f;  // (ksplit is at most 8: all loads in flight together)
-        const float* src = p.logits + static_cast<size_t>(t) * p.experts + e;
+// The CTA: logits of token t (sums of the slices, in order) into shared memory.
+__device__ __forceinline__ void gather_logits(const Params& p, int t, float* score) {
+    const float* src = p.logits + static_cast<size_t>(t) * p.experts;
+    const size_t slice = static_cast<size_t>(p.T) * p.experts;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < p.experts; e += THREADS) {
+        float v[8], s = 0.f;  // (at most 8 slices: all loads in flight together)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < p.ksplit ? __ldcg(src + static_cast<size_t>(k) * p.T * p.experts) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = k < p.ksplit ? __ldcg(src + k * slice + e) : 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[k];
         score[e] = s;
-        m = fmaxf(m, s);
     }
+}
+
+// One warp: the choice for one token from its logits (score: [experts], shared; key: [experts], shared scratch).
+// Lane l holds experts l, l + 32, ...
+__device__ __noinline__ void choose(const Params& p, float* score, uint32_t* key, int32_t* ids, float* wts) {
+    const int lane = threadIdx.x & 31;
+    const unsigned full = 0xffffffffu;
+    float m = -CUDART_INF_F;
+    for (int e = lane; e < p.experts; e += 32) m = fmaxf(m, score[e]);
     if (p.score == MXFP8_SCORE_SOFTMAX) {
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, d));
         float sum = 0.f;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t bar_w = sbase, bar_act = bar_w + 8 * MAX_ST, bar_empty = bar_act + 8 * MAX_ST,
                    bar_tfull = bar_empty + 8 * MAX_ST, bar_tempty = bar_tfull + 16, bar_drain = bar_tempty + 16;
     const uint32_t bar_qf = bar_drain + 8, bar_qe = bar_qf + 8 * NQ;
-    int* flags = reinterpret_cast<int*>(smem + 8 * (3 * MAX_ST + 5 + 2 * NQ));  // abort, TMEM base, epilogue unit x2, chosen, most, barrier ok, -, last part, queue
+    int* flags = reinterpret_cast<int*>(smem + 8 * (3 * MAX_ST + 5 + 2 * NQ));  // abort, TMEM base, epilogue unit x2, chosen, most, wait ok, token, last part, queue
     volatile int* abort_flag = flags;
     Lists L;
     L.wts = reinterpret_cast<float*>(smem + p.off_lists);
@@ -472,18 +480,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(flags[1]);
-    griddep_wait();  // logits, pieces of x, zeroed counters
+    griddep_launch_dependents();  // (what follows in the stream may get ready; it waits for this grid's end)
+    griddep_wait();               // logits, pieces of x, zeroed counters
 
     // ---- routing. Up to 8 tokens: every CTA chooses for all of them (one warp
-    // each). More: one warp of CTA t % G for token t, then a grid barrier.
+    // each). More: CTAs claim a token each and wait until all are chosen for.
+    // (Waits are only ever for work that a running CTA has claimed, here and
+    // below: the kernel ends however few of its CTAs are resident at a time.)
+    unsigned int first_unit = 0;
+    if (threadIdx.x == 0) first_unit = atomicAdd(p.counters + C_QUEUE, 1u);
     {
-        float* score = reinterpret_cast<float*>(smem + p.off_ring) + 2 * static_cast<size_t>(p.experts) * warp;
-        uint32_t* key = reinterpret_cast<uint32_t*>(score + p.experts);
+        float* scores = reinterpret_cast<float*>(smem + p.off_ring);  // [tokens in hand][experts], then as many keys
         bool ok = true;
         if (p.T <= 8) {
-            int32_t* ids = reinterpret_cast<int32_t*>(smem + p.off_epi) + warp * MXFP8_MOE_MAX_TOPK;
+            for (int t = 0; t < p.T; ++t) gather_logits(p, t, scores + t * p.experts);
+            __syncthreads();
             if (warp < p.T) {
-                choose(p, warp, score, key, ids, L.wts + warp * p.top_k);
+                int32_t* ids = reinterpret_cast<int32_t*>(smem + p.off_epi) + warp * MXFP8_MOE_MAX_TOPK;
+                choose(p, scores + warp * p.experts, reinterpret_cast<uint32_t*>(scores) + (p.T + warp) * p.experts, ids,
+                       L.wts + warp * p.top_k);
                 if (lane < p.top_k) {
                     const int e = ids[lane];
                     L.eid[warp * p.top_k + lane] = e >= p.first && e < p.first + p.local ? static_cast<uint16_t>(e - p.first) : 0xffff;
@@ -495,21 +510,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncthreads();
         } else {
-            for (int t = warp < 8 ? cta + warp * G : p.T; t < p.T; t += 8 * G) {
-                int32_t* ids = p.ids + t * p.top_k;
-                float* wts = p.weights + t * p.top_k;
-                choose(p, t, score, key, ids, wts);
-                if (lane < p.top_k) {
-                    if (p.user_ids) p.user_ids[t * p.top_k + lane] = ids[lane];
-                    if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
+            for (;;) {
+                if (threadIdx.x == 0) flags[7] = static_cast<int>(atomicAdd(p.counters + C_CLAIM, 1u));
+                __syncthreads();
+                const int t = flags[7];
+                if (t >= p.T) break;
+                gather_logits(p, t, scores);
+                __syncthreads();
+                if (warp == 0) {
+                    int32_t* ids = p.ids + t * p.top_k;
+                    float* wts = p.weights + t * p.top_k;
+                    choose(p, scores, reinterpret_cast<uint32_t*>(scores) + p.experts, ids, wts);
+                    if (lane < p.top_k) {
+                        if (p.user_ids) p.user_ids[t * p.top_k + lane] = ids[lane];
+                        if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
+                    }
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) red_release_gpu_add(p.counters + C_CHOSEN, 1);
                 }
             }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                __threadfence();
-                red_release_gpu_add(p.counters, 1);
-                flags[6] = wait_count(p.counters, G, abort_flag, p.wait_ns, p.status) ? 1 : 0;
-            }
+            if (threadIdx.x == 0) flags[6] = wait_count(p.counters + C_CHOSEN, p.T, abort_flag, p.wait_ns, p.status) ? 1 : 0;
             __syncthreads();
             ok = flags[6] != 0;
             if (ok)
@@ -604,8 +625,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             int c = 0, st = 0, put = 0;
             uint32_t ph = 1;
             bool ok = true;
-            // the first unit is the CTA's own index, the others come from the counter
-            // shared by all; each is published while the unit before is copied
+            // units come from the counter shared by all; each is published while the
+            // unit before is copied
             auto publish = [&](int u) {
                 if (!wait_bar(bar_qe + 8 * (put % NQ), ((put / NQ) & 1) ^ 1, abort_flag, p.wait_ns, p.status)) return false;
                 entry[put % NQ] = u < queue.units ? u : -1;
@@ -613,10 +634,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++put;
                 return true;
             };
-            int u = cta;
+            int u = static_cast<int>(first_unit);
             ok = publish(u);
             while (ok && u < queue.units) {
-                const int un = static_cast<int>(atomicAdd(p.counters + 2, 1u)) + G;
+                const int un = static_cast<int>(atomicAdd(p.counters + C_QUEUE, 1u));
                 const Seg g = queue.get(u);
                 const int e = L.act[g.a];
                 const int kp = min(g.k0 + 3, g.k1 - 1);  // (the counter's answer is back by then)
@@ -794,7 +815,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int stride = phase ? p.Ip : p.Hp, sstride = phase ? p.sh_stride : p.Hp / 32;
             if (tab_a != cur.g.a || tab_phase != phase) {
                 if (phase) {  // this expert's h
-                    if (lane == 0) ok = wait_count(p.counters + 3 + cur.g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
+                    if (lane == 0) ok = wait_count(p.counters + C_H + cur.g.a, p.up_tiles, abort_flag, p.wait_ns, p.status);
                     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     if (!ok) break;
                 }
@@ -912,14 +933,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
-            if (g.phase == 0) {
+            if (g.phase) {
+                named_bar_sync(EPI_BAR, 128);
+                if (q == 0 && lane == 0) {
+                    __threadfence();
+                    red_release_gpu_add(p.counters + C_DONE, 1);
+                }
+            } else {
                 bool finish = whole;
                 if (!whole) {
                     // the part that ends last sums all of them, in order
                     named_bar_sync(EPI_BAR, 128);
                     if (q == 0 && lane == 0) {
                         __threadfence();
-                        flags[8] = atom_acq_rel_gpu_add(p.counters + 3 + p.local + g.tile, 1) == static_cast<uint32_t>(g.parts - 1) ? 1 : 0;
+                        flags[8] = atom_acq_rel_gpu_add(p.counters + C_H + p.local + g.tile, 1) == static_cast<uint32_t>(g.parts - 1) ? 1 : 0;
                         __threadfence();
                     }
                     named_bar_sync(EPI_BAR, 128);
@@ -940,25 +967,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                     named_bar_sync(EPI_BAR, 128);
                     if (q == 0 && lane == 0) {
                         __threadfence();
-                        red_release_gpu_add(p.counters + 3 + g.a, 1);
+                        red_release_gpu_add(p.counters + C_H + g.a, 1);
                     }
                 }
             }
         }
     }
 
-    // ---- every product is in y or a partial: grid barrier, then the weighted sum
+    // ---- once every product is in y or a partial: the weighted sum, a share per CTA
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc_single(tmem, TMEM_ALL);
     if (threadIdx.x == 0) {
         bool ok = !*abort_flag;
-        if (ok && nact) {
-            __threadfence();
-            red_release_gpu_add(p.counters + 1, 1);
-            ok = wait_count(p.counters + 1, G, abort_flag, p.wait_ns, p.status);
-        }
+        if (ok) ok = wait_count(p.counters + C_DONE, queue.units - queue.up_units, abort_flag, p.wait_ns, p.status);
         flags[6] = ok ? 1 : 0;
     }
     __syncthreads();
@@ -1019,7 +1042,7 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
     l->down_steps = l->Ip / STEP;
     l->slots = T * top_k;
     l->local_slots = top_k < local ? T * top_k : T * local;
-    l->n_counters = 3 + local + local * l->up_tiles;
+    l->n_counters = C_H + local + local * l->up_tiles;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
     l->counters = take(4 * static_cast<size_t>(l->n_counters));
@@ -1093,23 +1116,20 @@ int launch_moe(const MoeArgs& a) {
     const int lblocks = ((a.experts + 8 * l.nf - 1) / (8 * l.nf)) * ((a.T + 16 * l.mf - 1) / (16 * l.mf)) * l.ksplit;
     int sblocks = (a.T * (l.Hp / STEP) + 7) / 8;  // one 128-column piece of a row per warp, up to 304 blocks
     if (sblocks > 304) sblocks = 304;
-    if (l.mf == 2) moe_logits<2, 4><<<lblocks + sblocks, 256, 0, a.stream>>>(p);
-    else moe_logits<1, 2><<<lblocks + sblocks, 256, 0, a.stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "router kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.stream = a.stream;
+    cfg.gridDim = dim3(lblocks + sblocks);
+    cfg.blockDim = dim3(256);
+    e = l.mf == 2 ? cudaLaunchKernelEx(&cfg, moe_logits<2, 4>, p) : cudaLaunchKernelEx(&cfg, moe_logits<1, 2>, p);
+    if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "router kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     cfg.gridDim = dim3(a.num_sms);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = p.smem;
-    cfg.stream = a.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    // CTAs wait on one another: all of them resident at once
-    attr[1].id = cudaLaunchAttributeCooperative;
-    attr[1].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, moe_experts, m13, m2, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;
