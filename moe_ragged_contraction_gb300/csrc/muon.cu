@@ -1,131 +1,644 @@
 // Orthogonalised update of a stack of gradients (mxfp8_muon_update): momentum,
-// Frobenius norm, Newton-Schulz products.
+// Frobenius norm, Newton-Schulz products on the tensor cores.
+//
+// With X the m x n matrix whose rows are the gradient's shorter side, one step is
+//   A = X X^T;   R = b A + c A A - beta I;   X <- (a + beta) X + R X
+// for any beta (the shift changes nothing but the rounding of R: near the end
+// the eigenvalues of A gather around 1, where b A + c A A is about b + c, so
+// the last step takes beta = 0.875 (b + c) and the one before half of that, and
+// R's largest part, its diagonal, is not rounded).
+//
+// Precision. The products run on fp16 operands (11 significant bits, eight
+// times finer than bf16 at the same rate) scaled by powers of two so that the
+// magnitudes that occur (||X||_2 below 32) neither overflow nor meet fp16's
+// subnormals; the accumulators are fp32. Rounding X itself to 11 bits would cost
+// more: its error is spread over all directions while every step multiplies a
+// small singular value by a = 3.4, so that the error of the first steps grows
+// a hundredfold beside what it is to be compared with. The a X term therefore
+// takes X from two fp16 planes (22 bits); in R X only R's dominant directions
+// see the rounding of X. (Simulated in 64 bits on normal, heavy-tailed,
+// decaying and low-rank spectra: 0.4e-3 .. 1.6e-3 relative error, against
+// 3e-3 .. 27e-3 with one plane and 3e-3 .. 59e-3 in bf16.)
+//
+// Kernels of a call: muon_momentum (momentum, partial sums of u^2), muon_scale
+// (X0 = u / norm into its two planes, transposed for tall matrices), muon_main:
+// persistent CTA pairs over all products of all steps, as one list of 256 x 256
+// tiles ordered by product; a tile waits for the product before it of its own
+// matrix only, so with several matrices the pairs never drain between
+// products. A A^T-type products are symmetric: only tiles on and below the
+// diagonal are computed and each is stored twice.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "mxw_experts.h"
 #include "mxw_internal.h"
+#include "mxw_ptx_single.cuh"
 #include "../../include/mxfp8_experts.h"
 
 namespace mxw {
 namespace {
 
-constexpr int NORM_BLOCKS = 64;
+constexpr int NORM_BLOCKS = 64;      // partial sums per matrix
+constexpr int TILE = 256;            // rows and columns of a pair's tile
+constexpr int HALF = TILE / 2;       // each CTA's rows of either operand
+constexpr int KSTEP = 64;               // contraction columns of a stage (128 bytes)
+constexpr int OP_BYTES = HALF * KSTEP * 2;
+constexpr int STAGES = 6;
+constexpr int EPI0 = 2, EPI_WARPS = 8;
+constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
+constexpr int SMEM = STAGES * 2 * OP_BYTES + 1024 + 512;
+constexpr int EPI_BAR = 1;
+// powers of two that the stored matrices are scaled by
+constexpr float SX = 2048.f;         // X
+constexpr float SLO = 2048.f;        // lower plane of X, on top of SX
+constexpr float SA = 4096.f;         // A and R
+// kind::f16: fp16 x fp16 -> fp32, M = 256 across the pair, N = 256; bit 16: B is MN-major
+constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE >> 3) << 17) | (static_cast<uint32_t>(TILE >> 4) << 24);
 
-// u (fp32) and the momentum; per-block partial sums of u^2.
-__global__ void __launch_bounds__(256) momentum_simple(const MuonArgs a, float* u, float* part) {
-    const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
-    float s = 0.f;
-    for (size_t i = blockIdx.x * 256 + threadIdx.x; i < per; i += NORM_BLOCKS * 256) {
-        const float g = a.grad_f32 ? static_cast<const float*>(a.grad)[base + i]
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[base + i]);
-        float v = g;
-        if (a.momentum) {
-            const float m = a.mu * a.momentum[base + i] + g;
-            a.momentum[base + i] = m;
-            v = a.nesterov ? g + a.mu * m : m;
-        }
-        u[base + i] = v;
-        s += v * v;
-    }
-    __shared__ float red[256];
-    red[threadIdx.x] = s;
-    __syncthreads();
-    for (int d = 128; d > 0; d >>= 1) {
-        if (threadIdx.x < d) red[threadIdx.x] += red[threadIdx.x + d];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) part[blockIdx.y * NORM_BLOCKS + blockIdx.x] = red[0];
-}
-
-__global__ void __launch_bounds__(256) normalise_simple(const MuonArgs a, float* u, const float* part) {
-    const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
-    float s = 0.f;
-    for (int i = 0; i < NORM_BLOCKS; ++i) s += part[blockIdx.y * NORM_BLOCKS + i];
-    const float inv = 1.f / (sqrtf(s) + a.eps);
-    for (size_t i = blockIdx.x * 256 + threadIdx.x; i < per; i += NORM_BLOCKS * 256)
-        u[base + i] = isfinite(s) ? u[base + i] * inv : __int_as_float(0x7fffffff);
-}
-
-// C[i][j] = alpha * sum_k A(i,k) B(j,k) + beta * D[i][j]; element (i,k) of an
-// operand at i * si + k * sk; C, D row-major with ldc. out16: bf16 result.
-struct Gemm {
-    const float *A, *B, *D;
-    float* C;
-    uint16_t* out16;
-    int m, n, k;
-    size_t sai, sak, sbj, sbk, ldc, batch_a, batch_b, batch_c;
-    float alpha, beta;
+struct Params {
+    int E, m, n, ldm, ldn, steps, tall, T, Tn, sym, full;  // tiles along m and n; tiles of a symmetric product and of R X
+    float a, b, c;
+    __half *Xh[2], *Xl[2], *A, *R;
+    uint16_t* out;
+    unsigned int* done;  // [E][3 steps] CTA halves of tiles stored
+    unsigned long long wait_ns;
+    int* status;
 };
 
-__global__ void __launch_bounds__(256) gemm_simple(const Gemm g) {
-    __shared__ float As[16][65], Bs[16][65];
-    const float* A = g.A + blockIdx.z * g.batch_a;
-    const float* B = g.B + blockIdx.z * g.batch_b;
-    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < g.k; k0 += 16) {
-        for (int l = threadIdx.x; l < 1024; l += 256) {
-            const int r = l >> 4, k = l & 15;
-            As[k][r] = i0 + r < g.m && k0 + k < g.k ? A[(i0 + r) * g.sai + (k0 + k) * g.sak] : 0.f;
-            Bs[k][r] = j0 + r < g.n && k0 + k < g.k ? B[(j0 + r) * g.sbj + (k0 + k) * g.sbk] : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += As[k][ty * 4 + i] * Bs[k][tx * 4 + j];
-        __syncthreads();
+struct Maps {
+    CUtensorMap xk[2], xm[2], a, r;  // X by rows and by 64 x 64 boxes (its columns as the MMA's N), A, R
+};
+
+// ============================================================== momentum, norm, X0
+
+__device__ __forceinline__ float2 bf16x2_f(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+// Four values of u at element i (a multiple of 4); FIRST also updates the momentum.
+template <bool FIRST>
+__device__ __forceinline__ float4 load_u(const MuonArgs& a, size_t i) {
+    float4 g;
+    if (a.grad_f32) {
+        g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i));
+    } else {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i));
+        const float2 lo = bf16x2_f(r.x), hi = bf16x2_f(r.y);
+        g = make_float4(lo.x, lo.y, hi.x, hi.y);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = i0 + ty * 4 + i, c = j0 + tx * 4 + j;
-            if (r >= g.m || c >= g.n) continue;
-            const size_t at = blockIdx.z * g.batch_c + r * g.ldc + c;
-            const float v = g.alpha * acc[i][j] + (g.D ? g.beta * g.D[at] : 0.f);
-            if (g.out16) g.out16[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            else g.C[at] = v;
+    if (!a.momentum) return g;
+    float4 m = *reinterpret_cast<const float4*>(a.momentum + i);
+    if (FIRST) {
+        m = make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
+        *reinterpret_cast<float4*>(a.momentum + i) = m;
+    }
+    if (!a.nesterov) return m;
+    return make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
+}
+
+__global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* part, unsigned int* done, int n_done) {
+    const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
+    float s = 0.f;
+    for (size_t i = 4 * (blockIdx.x * 256 + threadIdx.x); i < per; i += 4 * NORM_BLOCKS * 256) {
+        const float4 u = load_u<true>(a, base + i);
+        s += (u.x * u.x + u.y * u.y) + (u.z * u.z + u.w * u.w);
+    }
+    __shared__ float red[8];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.f;
+        for (int w = 0; w < 8; ++w) s += red[w];
+        part[blockIdx.y * NORM_BLOCKS + blockIdx.x] = s;
+    }
+    for (int i = (blockIdx.y * NORM_BLOCKS + blockIdx.x) * 256 + threadIdx.x; i < n_done; i += gridDim.y * NORM_BLOCKS * 256)
+        done[i] = 0;
+}
+
+// X0 in two planes; tall matrices are transposed on the way, 64 x 64 at a time.
+__global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params p, const float* part) {
+    __shared__ float t[64][65];
+    __shared__ float s_inv;
+    const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+    if (threadIdx.x < 32) {
+        float s = part[e * NORM_BLOCKS + threadIdx.x] + part[e * NORM_BLOCKS + 32 + threadIdx.x];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        // NaN where the sum is not finite: the whole matrix comes out as NaN
+        if (threadIdx.x == 0) s_inv = s <= 3.4028235e38f ? SX / (sqrtf(s) + a.eps) : __int_as_float(0x7fffffff);
+    }
+    __syncthreads();
+    const float inv = s_inv;
+    const size_t base = static_cast<size_t>(e) * a.N * a.K;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = r0 + (threadIdx.x >> 4) + 16 * k, c = c0 + 4 * (threadIdx.x & 15);
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < a.N && c < a.K) u = load_u<false>(a, base + static_cast<size_t>(r) * a.K + c);
+        // eps = 0 and a zero matrix: 0 * inf would be NaN
+        const float v[4] = {u.x == 0.f && inv == inv ? 0.f : u.x * inv, u.y == 0.f && inv == inv ? 0.f : u.y * inv,
+                            u.z == 0.f && inv == inv ? 0.f : u.z * inv, u.w == 0.f && inv == inv ? 0.f : u.w * inv};
+        if (p.tall) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[4 * (threadIdx.x & 15) + j][(threadIdx.x >> 4) + 16 * k] = v[j];
+        } else if (r < a.N && c < a.K) {
+            const size_t at = (static_cast<size_t>(e) * p.m + r) * p.ldn + c;
+            __half h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = __float2half_rn(v[j]);
+                l[j] = __float2half_rn((v[j] - __half2float(h[j])) * SLO);
+            }
+            *reinterpret_cast<uint2*>(p.Xh[0] + at) = *reinterpret_cast<const uint2*>(h);
+            *reinterpret_cast<uint2*>(p.Xl[0] + at) = *reinterpret_cast<const uint2*>(l);
         }
+    }
+    if (!p.tall) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // row of X = column of the gradient
+        const int i = (threadIdx.x >> 4) + 16 * k, j0 = 4 * (threadIdx.x & 15);
+        if (c0 + i >= a.K || r0 + j0 >= p.ldn) continue;
+        const size_t at = (static_cast<size_t>(e) * p.m + c0 + i) * p.ldn + r0 + j0;
+        __half h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = t[i][j0 + j];
+            h[j] = __float2half_rn(v);
+            l[j] = __float2half_rn((v - __half2float(h[j])) * SLO);
+        }
+        *reinterpret_cast<uint2*>(p.Xh[0] + at) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(p.Xl[0] + at) = *reinterpret_cast<const uint2*>(l);
+    }
+}
+
+// ============================================================== products
+
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns, int* status) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (mbar_try_wait_suspend(bar, parity, 20000)) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > ns) {
+            *abort_flag = 1;
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned long long ns, int* status) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, ns, status);
+}
+
+__device__ __noinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigned long long ns, int* status) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > ns) {
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return;
+        }
+}
+
+__device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int target, volatile int* abort_flag, unsigned long long ns,
+                                        int* status) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        if (ld_acquire_gpu(p) >= target) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > ns) {
+            *abort_flag = 1;
+            atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
+            return false;
+        }
+        __nanosleep(20);
+    }
+}
+
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(mask)
+        : "memory");
+}
+
+// Descriptor of an operand whose rows are contraction steps (MN-major): 64
+// columns of 128 bytes with the 128-byte swizzle, 8-row groups 1024 bytes
+// apart, the next 64 columns 8 KB on.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// A tile of a product: ph 0: A = X X^T, 1: R = b A + c A A - beta I, 2: X <- (a + beta) X + R X.
+struct Item {
+    int step, ph, e, i, j, ksteps;
+};
+
+__device__ __forceinline__ Item get_item(const Params& p, int q) {
+    Item it;
+    const int sym = p.E * p.sym, per = 2 * sym + p.E * p.full;
+    it.step = q / per;
+    q -= it.step * per;
+    it.ph = q < sym ? 0 : q < 2 * sym ? 1 : 2;
+    q -= it.ph * sym;
+    const int tiles = it.ph == 2 ? p.full : p.sym;
+    it.e = q / tiles;
+    q -= it.e * tiles;
+    if (it.ph == 2) {
+        it.j = q / p.T;
+        it.i = q - it.j * p.T;
+    } else {
+        int i = static_cast<int>((sqrtf(8.f * q + 1.f) - 1.f) * 0.5f);
+        while (i * (i + 1) / 2 > q) --i;
+        while ((i + 1) * (i + 2) / 2 <= q) ++i;
+        it.i = i;
+        it.j = q - i * (i + 1) / 2;
+    }
+    it.ksteps = ((it.ph == 0 ? p.n : p.m) + KSTEP - 1) / KSTEP;
+    return it;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    muon_main(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const uint32_t bars = sbase + STAGES * 2 * OP_BYTES;
+    const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_tfull = bar_empty + 8 * STAGES, bar_tempty = bar_tfull + 16,
+                   bar_drain = bar_tempty + 16;
+    int* flags = reinterpret_cast<int*>(smem + STAGES * 2 * OP_BYTES + 8 * (2 * STAGES + 5));  // abort, TMEM base, epilogue go x2
+    volatile int* abort_flag = flags;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 2 * EPI_WARPS);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(flags + 1), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(flags[1]);
+    griddep_wait();
+    const int G = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int total = p.steps * p.E * (2 * p.sym + p.full);
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads (both CTAs)
+        if (lane == 0) {
+            const uint32_t full_leader = mapa_shared(bar_full, 0);
+            int c = 0, st = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (int q = pair; ok && q < total; q += G) {
+                const Item it = get_item(p, q);
+                const int gp = 3 * it.step + it.ph;
+                if (gp) {  // the matrix's product before this one
+                    ok = wait_count(p.done + it.e * 3 * p.steps + gp - 1, 2 * (it.ph == 0 ? p.full : p.sym), abort_flag, p.wait_ns, p.status);
+                    if (!ok) break;
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                }
+                const int x = it.step & 1;
+                const CUtensorMap* ma = it.ph == 0 ? &maps.xk[x] : it.ph == 1 ? &maps.a : &maps.r;
+                const CUtensorMap* mb = it.ph == 2 ? &maps.xm[x] : ma;
+                const int ra = it.i * TILE + static_cast<int>(rank) * HALF, rb = it.j * TILE + static_cast<int>(rank) * HALF;
+                for (int k = 0; k < it.ksteps; ++k, ++c) {
+                    ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
+                    if (!ok) break;
+                    const uint32_t da = sbase + st * 2 * OP_BYTES, db = da + OP_BYTES, fb = full_leader + 8 * st;
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 4 * OP_BYTES);
+                    tma_load_3d_pair(da, ma, fb, k * KSTEP, ra, it.e);
+                    if (it.ph == 2) {
+                        tma_load_3d_pair(db, mb, fb, rb, k * KSTEP, it.e);
+                        tma_load_3d_pair(db + OP_BYTES / 2, mb, fb, rb + 64, k * KSTEP, it.e);
+                    } else {
+                        tma_load_3d_pair(db, mb, fb, k * KSTEP, rb, it.e);
+                    }
+                    if (++st == STAGES) { st = 0; ph ^= 1; }
+                }
+            }
+            if (leader && (!ok || *abort_flag))
+                for (int d = 1; d <= min(c, STAGES); ++d)
+                    drain_bar(bar_full + 8 * ((c - d) % STAGES), ((c - d) / STAGES) & 1, p.wait_ns, p.status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer (leader)
+        if (leader && elect_one()) {
+            int st = 0, tile = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int q = pair; ok && q < total; q += G, ++tile) {
+                const Item it = get_item(p, q);
+                const int buf = tile & 1;
+                ok = wait_bar(bar_tempty + 8 * buf, ((tile >> 1) & 1) ^ 1, abort_flag, p.wait_ns, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * TILE;
+                const bool mn = it.ph == 2;
+                const uint32_t idesc = IDESC | (mn ? 1u << 16 : 0u);
+                const uint32_t bstep = mn ? 2048 >> 4 : 32 >> 4;  // 16 contraction rows, or 32 bytes along a row
+                for (int k = 0; k < it.ksteps; ++k) {
+                    ok = wait_bar(bar_full + 8 * st, ph, abort_flag, p.wait_ns, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t as = sbase + st * 2 * OP_BYTES;
+                    const uint64_t ad = desc_kmajor_sw128(as);
+                    const uint64_t bd = mn ? desc_mnmajor_sw128(as + OP_BYTES) : desc_kmajor_sw128(as + OP_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < KSTEP / 16; ++kk)
+                        tc_mma_f16_pair(d, ad + 2 * kk, bd + bstep * kk, idesc, k > 0 || kk > 0 ? 1u : 0u);
+                    tc_commit_pair(bar_empty + 8 * st, 0x3);
+                    if (++st == STAGES) { st = 0; ph ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit_pair(bar_tfull + 8 * buf, 0x3);
+            }
+            tc_commit_pair(bar_drain, 0x3);
+        }
+        __syncwarp();
+        if (lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ epilogue (8 warps per CTA)
+        const int q4 = warp & 3, h = (warp - EPI0) >> 2;
+        const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+        const bool odd = lane & 1;
+        int tile = 0;
+        for (int q = pair; q < total; q += G, ++tile) {
+            const Item it = get_item(p, q);
+            const int buf = tile & 1;
+            if (warp == EPI0 && lane == 0)
+                flags[2 + buf] = wait_bar(bar_tfull + 8 * buf, (tile >> 1) & 1, abort_flag, p.wait_ns, p.status) ? 1 : 0;
+            named_bar_sync(EPI_BAR, 32 * EPI_WARPS);
+            if (!flags[2 + buf]) break;
+            tc_fence_after();
+            const int r = it.i * TILE + static_cast<int>(rank) * HALF + q4 * 32 + lane;  // row of the product
+            const int c0 = it.j * TILE + h * HALF;
+            const bool last = it.step + 1 == p.steps;
+            const float shift = last ? 0.875f * (p.b + p.c) : it.step + 2 == p.steps ? 0.4375f * (p.b + p.c) : 0.f;
+            const int rows = p.m, cols = it.ph == 2 ? p.n : p.m;
+            const int x = it.step & 1;
+            const size_t xrow = (static_cast<size_t>(it.e) * p.m + r) * p.ldn, arow = (static_cast<size_t>(it.e) * p.m + r) * p.ldm;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + buf * TILE + h * HALF;
+#pragma unroll 1
+            for (int ch = 0; ch < HALF / 32; ++ch) {
+                const int c = c0 + 32 * ch;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + 32 * ch, v);
+                tmem_wait_ld();
+                reg_fence(v);
+                if (c >= cols) continue;  // the same for the whole CTA half
+                float f[32];
+                const bool row_in = r < rows;
+                if (it.ph == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * (SA / (SX * SX));
+                } else if (it.ph == 1) {
+                    const __half* src = p.A + arow + c;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (row_in && c + i < p.ldm) u = __ldcg(reinterpret_cast<const uint4*>(src + i));
+                        const __half* hv = reinterpret_cast<const __half*>(&u);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            f[i + j] = fmaf(p.c / SA, __uint_as_float(v[i + j]), p.b * __half2float(hv[j]));
+                            if (r == c + i + j) f[i + j] -= shift * SA;
+                        }
+                    }
+                } else {
+                    const float ax = p.a + shift;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint4 u = make_uint4(0, 0, 0, 0), w = u;
+                        if (row_in && c + i < p.ldn) {
+                            u = __ldcg(reinterpret_cast<const uint4*>(p.Xh[x] + xrow + c + i));
+                            if (!last || p.steps == 1) w = __ldcg(reinterpret_cast<const uint4*>(p.Xl[x] + xrow + c + i));
+                        }
+                        const __half *hv = reinterpret_cast<const __half*>(&u), *lv = reinterpret_cast<const __half*>(&w);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            f[i + j] = fmaf(ax, fmaf(1.f / SLO, __half2float(lv[j]), __half2float(hv[j])), __uint_as_float(v[i + j]) * (1.f / SA));
+                    }
+                }
+                if (it.ph < 2 || !last) {
+                    // fp16 rows, and the transposed tile of a symmetric product
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&t);
+                    }
+                    const int ld = it.ph == 2 ? p.ldn : p.ldm;
+                    __half* dst = it.ph == 0 ? p.A + arow + c : it.ph == 1 ? p.R + arow + c : p.Xh[x ^ 1] + xrow + c;
+                    if (row_in) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            if (c + 2 * i < ld) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                    }
+                    if (it.ph < 2 && it.i != it.j) {
+                        // lanes r, r + 1 exchange halves: the even lane stores (r, r + 1)
+                        // of row c + 2 i, the odd lane those of row c + 2 i + 1
+                        __half* tr = (it.ph == 0 ? p.A : p.R) + static_cast<size_t>(it.e) * p.m * p.ldm + (r & ~1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i], 1);
+                            const uint32_t y = odd ? __byte_perm(got, w[i], 0x7632) : __byte_perm(w[i], got, 0x5410);
+                            const int row = c + 2 * i + (odd ? 1 : 0);
+                            if (row < p.m && (r & ~1) < p.ldm) *reinterpret_cast<uint32_t*>(tr + static_cast<size_t>(row) * p.ldm) = y;
+                        }
+                    }
+                    if (it.ph == 2 && it.step + 2 < p.steps && row_in) {
+                        // the lower plane (the last step reads the upper one only)
+                        __half* lo = p.Xl[x ^ 1] + xrow + c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2 + j]));
+                                const __half2 t = __floats2half2_rn((f[i + 2 * j] - hv.x) * SLO, (f[i + 2 * j + 1] - hv.y) * SLO);
+                                y[j] = *reinterpret_cast<const uint32_t*>(&t);
+                            }
+                            if (c + i < p.ldn) *reinterpret_cast<uint4*>(lo + i) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                } else {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = pack_bf16x2(__float_as_uint(f[2 * i] * (1.f / SX)), __float_as_uint(f[2 * i + 1] * (1.f / SX)));
+                    if (!p.tall) {
+                        uint16_t* dst = p.out + (static_cast<size_t>(it.e) * p.m + r) * p.n + c;
+                        if (row_in) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                if (c + 2 * i < p.n) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        }
+                    } else {
+                        uint16_t* tr = p.out + static_cast<size_t>(it.e) * p.n * p.m + (r & ~1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i], 1);
+                            const uint32_t y = odd ? __byte_perm(got, w[i], 0x7632) : __byte_perm(w[i], got, 0x5410);
+                            const int row = c + 2 * i + (odd ? 1 : 0);
+                            if (row < p.n && (r & ~1) < p.m) *reinterpret_cast<uint32_t*>(tr + static_cast<size_t>(row) * p.m) = y;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            asm volatile("fence.proxy.async;" ::: "memory");  // these stores before other SMs' TMA loads of them
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(bar_tempty + 8 * buf);
+                else mbar_arrive_cluster(tempty_leader + 8 * buf);
+            }
+            named_bar_sync(EPI_BAR, 32 * EPI_WARPS);
+            if (warp == EPI0 && lane == 0) {
+                __threadfence();
+                red_release_gpu_add(p.done + it.e * 3 * p.steps + 3 * it.step + it.ph, 1);
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ============================================================== host side
+
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct Layout {
+    int m, n, ldm, ldn;
+    size_t part, done, xh[2], xl[2], a, r, total;
+};
+
+void layout(int E, int N, int K, Layout* l) {
+    l->m = N < K ? N : K;
+    l->n = N < K ? K : N;
+    l->ldm = (l->m + 63) & ~63;
+    l->ldn = (l->n + 63) & ~63;
+    size_t at = 0;
+    auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
+    const size_t e = E;
+    l->part = take(4 * e * NORM_BLOCKS);
+    l->done = take(4 * e * 3 * MXFP8_MUON_MAX_STEPS);
+    for (int i = 0; i < 2; ++i) l->xh[i] = take(2 * e * l->m * l->ldn);
+    for (int i = 0; i < 2; ++i) l->xl[i] = take(2 * e * l->m * l->ldn);
+    l->a = take(2 * e * l->m * l->ldm);
+    l->r = take(2 * e * l->m * l->ldm);
+    l->total = at;
+}
+
+int map2(CUtensorMap* map, const void* base, int cols, int ld, int rows, int E, int box_cols, int box_rows) {
+    const uint64_t d[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(E)};
+    const uint64_t s[2] = {2 * static_cast<uint64_t>(ld), 2 * static_cast<uint64_t>(ld) * rows};
+    const uint32_t b[3] = {static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows), 1};
+    return host_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
 
 size_t muon_ws_bytes(int E, int N, int K) {
-    const size_t m = N < K ? N : K, per = static_cast<size_t>(N) * K;
-    return 4 * static_cast<size_t>(E) * (2 * per + 2 * m * m + NORM_BLOCKS) + 256;
+    Layout l;
+    layout(E, N, K, &l);
+    return l.total;
 }
 
 int launch_muon(const MuonArgs& a) {
-    const size_t per = static_cast<size_t>(a.N) * a.K;
-    const int m = a.N < a.K ? a.N : a.K, n = a.N < a.K ? a.K : a.N;
-    const bool tall = a.N > a.K;
-    const size_t mm = static_cast<size_t>(m) * m;
-    float* X = reinterpret_cast<float*>(a.ws);
-    float* Y = X + a.E * per;
-    float* A = Y + a.E * per;
-    float* B = A + a.E * mm;
-    float* part = B + a.E * mm;
-    momentum_simple<<<dim3(NORM_BLOCKS, a.E), 256, 0, a.stream>>>(a, X, part);
-    normalise_simple<<<dim3(NORM_BLOCKS, a.E), 256, 0, a.stream>>>(a, X, part);
-    const size_t si = tall ? 1 : a.K, sk = tall ? a.K : 1;  // X(i, k): row i of the shorter side, column k of the longer
-    auto run = [&](const Gemm& g) {
-        gemm_simple<<<dim3((g.n + 63) / 64, (g.m + 63) / 64, a.E), 256, 0, a.stream>>>(g);
-    };
-    for (int s = 0; s < a.steps; ++s) {
-        const size_t sm = m;
-        run(Gemm{X, X, nullptr, A, nullptr, m, m, n, si, sk, si, sk, sm, per, per, mm, 1.f, 0.f});
-        run(Gemm{A, A, A, B, nullptr, m, m, m, sm, 1, sm, 1, sm, mm, mm, mm, a.c, a.b});
-        uint16_t* out = s + 1 == a.steps ? a.out : nullptr;
-        if (!tall)
-            run(Gemm{B, X, X, Y, out, m, n, m, sm, 1, sk, si, static_cast<size_t>(a.K), mm, per, per, 1.f, a.a});
-        else
-            run(Gemm{X, B, X, Y, out, n, m, m, sk, si, sm, 1, static_cast<size_t>(a.K), per, mm, per, 1.f, a.a});
-        float* t = X;
-        X = Y;
-        Y = t;
+    Layout l;
+    layout(a.E, a.N, a.K, &l);
+    Params p{};
+    p.E = a.E; p.m = l.m; p.n = l.n; p.ldm = l.ldm; p.ldn = l.ldn; p.steps = a.steps; p.tall = a.N > a.K;
+    p.T = (l.m + TILE - 1) / TILE;
+    p.Tn = (l.n + TILE - 1) / TILE;
+    p.sym = p.T * (p.T + 1) / 2;
+    p.full = p.T * p.Tn;
+    if (static_cast<long long>(a.steps) * a.E * (2LL * p.sym + p.full) > 0x7fffffffLL / 2)
+        return host_fail(MXFP8_EINVAL, "E=%d N=%d K=%d steps=%d: too many tiles", a.E, a.N, a.K, a.steps);
+    p.a = a.a; p.b = a.b; p.c = a.c;
+    for (int i = 0; i < 2; ++i) {
+        p.Xh[i] = reinterpret_cast<__half*>(a.ws + l.xh[i]);
+        p.Xl[i] = reinterpret_cast<__half*>(a.ws + l.xl[i]);
     }
-    const cudaError_t e = cudaGetLastError();
+    p.A = reinterpret_cast<__half*>(a.ws + l.a);
+    p.R = reinterpret_cast<__half*>(a.ws + l.r);
+    p.out = a.out;
+    p.done = reinterpret_cast<unsigned int*>(a.ws + l.done);
+    p.wait_ns = a.wait_limit_ns;
+    p.status = a.status;
+    float* part = reinterpret_cast<float*>(a.ws + l.part);
+    Maps maps;
+    int rc = MXFP8_OK;
+    for (int i = 0; i < 2 && !rc; ++i) {
+        rc = map2(&maps.xk[i], p.Xh[i], l.n, l.ldn, l.m, a.E, KSTEP, HALF);
+        if (!rc) rc = map2(&maps.xm[i], p.Xh[i], l.n, l.ldn, l.m, a.E, 64, KSTEP);
+    }
+    if (!rc) rc = map2(&maps.a, p.A, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
+    if (!rc) rc = map2(&maps.r, p.R, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
+    if (rc) return rc;
+
+    static std::atomic<int> max_pairs[64];
+    int pairs = max_pairs[a.dev].load(std::memory_order_relaxed);
+    cudaError_t e;
+    if (pairs == 0) {
+        e = cudaFuncSetAttribute(muon_main, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s", cudaGetErrorString(e));
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(2 * (a.num_sms / 2));
+        q.blockDim = dim3(THREADS);
+        q.dynamicSmemBytes = SMEM;
+        e = cudaOccupancyMaxActiveClusters(&pairs, muon_main, &q);
+        if (e != cudaSuccess || pairs < 1) return host_fail(MXFP8_ECUDA, "update kernel: %s", cudaGetErrorString(e));
+        max_pairs[a.dev].store(pairs, std::memory_order_relaxed);
+    }
+    muon_momentum<<<dim3(NORM_BLOCKS, a.E), 256, 0, a.stream>>>(a, part, p.done, a.E * 3 * a.steps);
+    muon_scale<<<dim3((a.K + 63) / 64, (a.N + 63) / 64, a.E), 256, 0, a.stream>>>(a, p, part);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
+    const int items = a.E * (p.full > p.sym ? p.full : p.sym);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (items < pairs ? items : pairs));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    // CTAs wait on one another: all of them resident at once
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, muon_main, maps, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;
 }
