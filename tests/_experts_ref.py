@@ -28,16 +28,21 @@ def dequantise(q, s):
     return e4m3_table()[q] * np.repeat(scale, 32, axis=-1)
 
 
-def route(x, router, top_k, bias=None, score="softmax", renormalize=True, scale=1.0):
-    """(ids [T, k], weights [T, k], gap [T]): the choice in 64 bits; gap is the smallest distance between the choice
-    value of one of the first k + 1 experts and the next (how far the choice is from a tie)."""
+def choice_values(x, router, bias=None, score="softmax"):
+    """(score, score + bias) [T, experts] in 64 bits."""
     logits = x.astype(np.float64) @ router.astype(np.float64).T
     if score == "softmax":
         p = np.exp(logits - logits.max(-1, keepdims=True))
         p /= p.sum(-1, keepdims=True)
     else:
         p = 1.0 / (1.0 + np.exp(-logits))
-    choice = p if bias is None else p + bias.astype(np.float64)
+    return p, p if bias is None else p + bias.astype(np.float64)
+
+
+def route(x, router, top_k, bias=None, score="softmax", renormalize=True, scale=1.0):
+    """(ids [T, k], weights [T, k], gap [T]): the choice in 64 bits; gap is the smallest distance between the choice
+    value of one of the first k + 1 experts and the next (how far the choice is from a tie)."""
+    p, choice = choice_values(x, router, bias, score)
     order = np.argsort(-choice, axis=-1, kind="stable")
     ids = order[:, :top_k]
     w = np.take_along_axis(p, ids, -1)
