@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // below: the kernel ends however few of its CTAs are resident at a time.)
     unsigned int first_unit = 0;
     if (threadIdx.x == 0) first_unit = atomicAdd(p.counters + C_QUEUE, 1u);
+    if (warp == 0) first_unit = __shfl_sync(0xffffffffu, first_unit, 0);
     {
         float* scores = reinterpret_cast<float*>(smem + p.off_ring);  // [tokens in hand][experts], then as many keys
         bool ok = true;
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ weight producer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t once = l2_evict_first();  // weights leave L2 first: it keeps the code, x, h and partial sums
             int c = 0, st = 0, put = 0;
             uint32_t ph = 1;

@@ -311,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ loads (both CTAs)
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t full_leader = mapa_shared(bar_full, 0);
             int c = 0, st = 0;
             uint32_t ph = 1;
