@@ -45,11 +45,13 @@ constexpr int TILE = 256;            // rows and columns of a pair's tile
 constexpr int HALF = TILE / 2;       // each CTA's rows of either operand
 constexpr int KSTEP = 64;               // contraction columns of a stage (128 bytes)
 constexpr int OP_BYTES = HALF * KSTEP * 2;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
+constexpr int SLOT = 32 * 128;          // an epilogue warp's 32 rows x 64 columns of fp16; two slots per warp
 constexpr int EPI0 = 2, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
-constexpr int SMEM = STAGES * 2 * OP_BYTES + 1024 + 512;
-constexpr int EPI_BAR = 1;
+constexpr int OFF_EPI = STAGES * 2 * OP_BYTES, OFF_BAR = OFF_EPI + 2 * EPI_WARPS * SLOT;
+constexpr int SMEM = OFF_BAR + 1024 + 512;
+static_assert(SMEM <= 232448, "shared memory of a CTA");
 // powers of two that the stored matrices are scaled by
 constexpr float SX = 2048.f;         // X
 constexpr float SLO = 2048.f;        // lower plane of X, on top of SX
@@ -60,15 +62,16 @@ constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE >> 3) << 17) 
 struct Params {
     int E, m, n, ldm, ldn, steps, tall, T, Tn, sym, full;  // tiles along m and n; tiles of a symmetric product and of R X
     float a, b, c;
-    __half *Xh[2], *Xl[2], *A, *R;
-    uint16_t* out;
-    unsigned int* done;  // [E][3 steps] CTA halves of tiles stored
+    __half *Xh, *Xl;     // X0's planes
+    unsigned int* done;  // [E][3 steps] epilogue warps' shares of tiles stored
     unsigned long long wait_ns;
     int* status;
 };
 
 struct Maps {
-    CUtensorMap xk[2], xm[2], a, r;  // X by rows and by 64 x 64 boxes (its columns as the MMA's N), A, R
+    CUtensorMap xk[2], xm[2], a, r;   // operands: X by rows and by 64 x 64 boxes (its columns as the MMA's N), A, R
+    CUtensorMap exh[2], exl[2], ea, er, eout;  // epilogue: boxes of 32 rows x 64 columns
+    CUtensorMap ta, tr, tout;         // transposed: boxes of 32 rows x 32 columns
 };
 
 // ============================================================== momentum, norm, X0
@@ -153,8 +156,8 @@ __global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params
                 h[j] = __float2half_rn(v[j]);
                 l[j] = __float2half_rn((v[j] - __half2float(h[j])) * SLO);
             }
-            *reinterpret_cast<uint2*>(p.Xh[0] + at) = *reinterpret_cast<const uint2*>(h);
-            *reinterpret_cast<uint2*>(p.Xl[0] + at) = *reinterpret_cast<const uint2*>(l);
+            *reinterpret_cast<uint2*>(p.Xh + at) = *reinterpret_cast<const uint2*>(h);
+            *reinterpret_cast<uint2*>(p.Xl + at) = *reinterpret_cast<const uint2*>(l);
         }
     }
     if (!p.tall) return;
@@ -172,8 +175,8 @@ __global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params
             h[j] = __float2half_rn(v);
             l[j] = __float2half_rn((v - __half2float(h[j])) * SLO);
         }
-        *reinterpret_cast<uint2*>(p.Xh[0] + at) = *reinterpret_cast<const uint2*>(h);
-        *reinterpret_cast<uint2*>(p.Xl[0] + at) = *reinterpret_cast<const uint2*>(l);
+        *reinterpret_cast<uint2*>(p.Xh + at) = *reinterpret_cast<const uint2*>(h);
+        *reinterpret_cast<uint2*>(p.Xl + at) = *reinterpret_cast<const uint2*>(l);
     }
 }
 
@@ -218,6 +221,17 @@ __device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int targ
         }
         __nanosleep(20);
     }
+}
+
+__device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
@@ -279,10 +293,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const uint32_t bars = sbase + STAGES * 2 * OP_BYTES;
+    const uint32_t bars = sbase + OFF_BAR;
     const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_tfull = bar_empty + 8 * STAGES, bar_tempty = bar_tfull + 16,
-                   bar_drain = bar_tempty + 16;
-    int* flags = reinterpret_cast<int*>(smem + STAGES * 2 * OP_BYTES + 8 * (2 * STAGES + 5));  // abort, TMEM base, epilogue go x2
+                   bar_drain = bar_tempty + 16, bar_epi = bar_drain + 8;
+    int* flags = reinterpret_cast<int*>(smem + OFF_BAR + 8 * (2 * STAGES + 5 + EPI_WARPS));  // abort, TMEM base
     volatile int* abort_flag = flags;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -294,6 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mbar_init(bar_tempty + 8 * b, 2 * EPI_WARPS);
         }
         mbar_init(bar_drain, 1);
+        for (int w = 0; w < EPI_WARPS; ++w) mbar_init(bar_epi + 8 * w, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -320,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const Item it = get_item(p, q);
                 const int gp = 3 * it.step + it.ph;
                 if (gp) {  // the matrix's product before this one
-                    ok = wait_count(p.done + it.e * 3 * p.steps + gp - 1, 2 * (it.ph == 0 ? p.full : p.sym), abort_flag, p.wait_ns, p.status);
+                    ok = wait_count(p.done + it.e * 3 * p.steps + gp - 1, 2 * EPI_WARPS * (it.ph == 0 ? p.full : p.sym), abort_flag, p.wait_ns, p.status);
                     if (!ok) break;
                     asm volatile("fence.proxy.async;" ::: "memory");
                 }
@@ -387,146 +402,177 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (8 warps per CTA)
+        // A warp owns 32 rows (its TMEM quarter) x 128 columns of the CTA's half
+        // tile, in chunks of 64 columns. What a chunk adds to (A, or X's planes)
+        // is loaded by TMA into the warp's two slots, replaced there by the
+        // result and stored by TMA: whole lines either way (per-lane accesses to
+        // 32 rows at once took 13 us a tile, twice the products' time).
         const int q4 = warp & 3, h = (warp - EPI0) >> 2;
         const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
+        const uint32_t slot = sbase + OFF_EPI + (warp - EPI0) * 2 * SLOT, slot2 = slot + SLOT, bar_in = bar_epi + 8 * (warp - EPI0);
+        const uint32_t row_at = lane * 128, sw = lane & 7;  // 16-byte piece k of the lane's row: row_at + ((k ^ sw) << 4)
         const bool odd = lane & 1;
         int tile = 0;
-        for (int q = pair; q < total; q += G, ++tile) {
+        uint32_t in_ph = 0;
+        bool ok = true;
+        for (int q = pair; ok && q < total; q += G, ++tile) {
             const Item it = get_item(p, q);
             const int buf = tile & 1;
-            if (warp == EPI0 && lane == 0)
-                flags[2 + buf] = wait_bar(bar_tfull + 8 * buf, (tile >> 1) & 1, abort_flag, p.wait_ns, p.status) ? 1 : 0;
-            named_bar_sync(EPI_BAR, 32 * EPI_WARPS);
-            if (!flags[2 + buf]) break;
+            if (lane == 0) ok = wait_bar(bar_tfull + 8 * buf, (tile >> 1) & 1, abort_flag, p.wait_ns, p.status);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
             tc_fence_after();
-            const int r = it.i * TILE + static_cast<int>(rank) * HALF + q4 * 32 + lane;  // row of the product
-            const int c0 = it.j * TILE + h * HALF;
+            const int r0 = it.i * TILE + static_cast<int>(rank) * HALF + q4 * 32, r = r0 + lane;  // row of the product
             const bool last = it.step + 1 == p.steps;
             const float shift = last ? 0.875f * (p.b + p.c) : it.step + 2 == p.steps ? 0.4375f * (p.b + p.c) : 0.f;
-            const int rows = p.m, cols = it.ph == 2 ? p.n : p.m;
-            const int x = it.step & 1;
-            const size_t xrow = (static_cast<size_t>(it.e) * p.m + r) * p.ldn, arow = (static_cast<size_t>(it.e) * p.m + r) * p.ldm;
+            const int cols = it.ph == 2 ? p.n : p.m, x = it.step & 1;
+            const bool mirror = it.ph < 2 && it.i != it.j;
+            const bool low_in = it.ph == 2 && (!last || p.steps == 1), low_out = it.ph == 2 && it.step + 2 < p.steps;
+            const bool tall_out = it.ph == 2 && last && p.tall;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + buf * TILE + h * HALF;
 #pragma unroll 1
-            for (int ch = 0; ch < HALF / 32; ++ch) {
-                const int c = c0 + 32 * ch;
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + 32 * ch, v);
-                tmem_wait_ld();
-                reg_fence(v);
-                if (c >= cols) continue;  // the same for the whole CTA half
-                float f[32];
-                const bool row_in = r < rows;
-                if (it.ph == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * (SA / (SX * SX));
-                } else if (it.ph == 1) {
-                    const __half* src = p.A + arow + c;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 u = make_uint4(0, 0, 0, 0);
-                        if (row_in && c + i < p.ldm) u = __ldcg(reinterpret_cast<const uint4*>(src + i));
-                        const __half* hv = reinterpret_cast<const __half*>(&u);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            f[i + j] = fmaf(p.c / SA, __uint_as_float(v[i + j]), p.b * __half2float(hv[j]));
-                            if (r == c + i + j) f[i + j] -= shift * SA;
-                        }
-                    }
-                } else {
-                    const float ax = p.a + shift;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint4 u = make_uint4(0, 0, 0, 0), w = u;
-                        if (row_in && c + i < p.ldn) {
-                            u = __ldcg(reinterpret_cast<const uint4*>(p.Xh[x] + xrow + c + i));
-                            if (!last || p.steps == 1) w = __ldcg(reinterpret_cast<const uint4*>(p.Xl[x] + xrow + c + i));
-                        }
-                        const __half *hv = reinterpret_cast<const __half*>(&u), *lv = reinterpret_cast<const __half*>(&w);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            f[i + j] = fmaf(ax, fmaf(1.f / SLO, __half2float(lv[j]), __half2float(hv[j])), __uint_as_float(v[i + j]) * (1.f / SA));
+            for (int ch = 0; ch < 2; ++ch) {
+                const int c = it.j * TILE + h * HALF + 64 * ch;
+                if (c >= cols || r0 >= p.m) break;
+                if (lane == 0) {
+                    bulk_wait_group_read<0>();  // the slots' last stores have been read
+                    if (it.ph) {
+                        mbar_arrive_expect_tx(bar_in, low_in ? 2 * SLOT : SLOT);
+                        tma_load_3d_plain(slot, it.ph == 1 ? &maps.ea : &maps.exh[x], bar_in, c, r0, it.e);
+                        if (low_in) tma_load_3d_plain(slot2, &maps.exl[x], bar_in, c, r0, it.e);
                     }
                 }
-                if (it.ph < 2 || !last) {
-                    // fp16 rows, and the transposed tile of a symmetric product
-                    uint32_t w[16];
+                __syncwarp();
+                if (it.ph) {
+                    if (lane == 0) ok = wait_bar(bar_in, in_ph, abort_flag, p.wait_ns, p.status);
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    (void)mbar_try_wait(bar_in, in_ph);  // complete: makes the loads visible to every lane
+                    in_ph ^= 1;
+                }
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + 64 * ch + 32 * hf, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    float f[32];
+                    const uint32_t at = slot + row_at, at2 = slot2 + row_at;
+                    if (it.ph == 0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                        w[i] = *reinterpret_cast<const uint32_t*>(&t);
-                    }
-                    const int ld = it.ph == 2 ? p.ldn : p.ldm;
-                    __half* dst = it.ph == 0 ? p.A + arow + c : it.ph == 1 ? p.R + arow + c : p.Xh[x ^ 1] + xrow + c;
-                    if (row_in) {
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * (SA / (SX * SX));
+                    } else if (it.ph == 1) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            if (c + 2 * i < ld) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                    }
-                    if (it.ph < 2 && it.i != it.j) {
-                        // lanes r, r + 1 exchange halves: the even lane stores (r, r + 1)
-                        // of row c + 2 i, the odd lane those of row c + 2 i + 1
-                        __half* tr = (it.ph == 0 ? p.A : p.R) + static_cast<size_t>(it.e) * p.m * p.ldm + (r & ~1);
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t u[4];
+                            ld_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i], 1);
-                            const uint32_t y = odd ? __byte_perm(got, w[i], 0x7632) : __byte_perm(w[i], got, 0x5410);
-                            const int row = c + 2 * i + (odd ? 1 : 0);
-                            if (row < p.m && (r & ~1) < p.ldm) *reinterpret_cast<uint32_t*>(tr + static_cast<size_t>(row) * p.ldm) = y;
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+                                const int i = 8 * k + 2 * j;
+                                f[i] = fmaf(p.c / SA, __uint_as_float(v[i]), p.b * t.x);
+                                f[i + 1] = fmaf(p.c / SA, __uint_as_float(v[i + 1]), p.b * t.y);
+                            }
+                        }
+                        if (it.i == it.j) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (r == c + 32 * hf + i) f[i] -= shift * SA;
+                        }
+                    } else {
+                        const float ax = p.a + shift;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t u[4], w[4] = {0, 0, 0, 0};
+                            ld_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u);
+                            if (low_in) ld_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), w);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+                                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                                const int i = 8 * k + 2 * j;
+                                f[i] = fmaf(ax, fmaf(1.f / SLO, l.x, t.x), __uint_as_float(v[i]) * (1.f / SA));
+                                f[i + 1] = fmaf(ax, fmaf(1.f / SLO, l.y, t.y), __uint_as_float(v[i + 1]) * (1.f / SA));
+                            }
                         }
                     }
-                    if (it.ph == 2 && it.step + 2 < p.steps && row_in) {
-                        // the lower plane (the last step reads the upper one only)
-                        __half* lo = p.Xl[x ^ 1] + xrow + c;
+                    uint32_t w[16];
+                    if (it.ph == 2 && last) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16x2(__float_as_uint(f[2 * i] * (1.f / SX)), __float_as_uint(f[2 * i + 1] * (1.f / SX)));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                            w[i] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                    }
+                    if (!tall_out) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(at + (((4 * hf + k) ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
+                    if (low_out) {
+                        // the lower plane (the last step reads the upper one only)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
                             uint32_t y[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2 + j]));
-                                const __half2 t = __floats2half2_rn((f[i + 2 * j] - hv.x) * SLO, (f[i + 2 * j + 1] - hv.y) * SLO);
+                                const int i = 8 * k + 2 * j;
+                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * k + j]));
+                                const __half2 t = __floats2half2_rn((f[i] - hv.x) * SLO, (f[i + 1] - hv.y) * SLO);
                                 y[j] = *reinterpret_cast<const uint32_t*>(&t);
                             }
-                            if (c + i < p.ldn) *reinterpret_cast<uint4*>(lo + i) = make_uint4(y[0], y[1], y[2], y[3]);
+                            st_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), y[0], y[1], y[2], y[3]);
                         }
                     }
-                } else {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack_bf16x2(__float_as_uint(f[2 * i] * (1.f / SX)), __float_as_uint(f[2 * i + 1] * (1.f / SX)));
-                    if (!p.tall) {
-                        uint16_t* dst = p.out + (static_cast<size_t>(it.e) * p.m + r) * p.n + c;
-                        if (row_in) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4)
-                                if (c + 2 * i < p.n) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-                        }
-                    } else {
-                        uint16_t* tr = p.out + static_cast<size_t>(it.e) * p.n * p.m + (r & ~1);
+                    if (mirror || tall_out) {
+                        // transposed, 32 rows (this product's columns) of 64 bytes with
+                        // the 64-byte swizzle; lanes r, r + 1 exchange halves: the even
+                        // lane stores (r, r + 1) of row 2 i, the odd lane of 2 i + 1
+                        const uint32_t base = slot2 + hf * 2048, kb = static_cast<uint32_t>(lane & ~1) * 2;
+                        __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i], 1);
                             const uint32_t y = odd ? __byte_perm(got, w[i], 0x7632) : __byte_perm(w[i], got, 0x5410);
-                            const int row = c + 2 * i + (odd ? 1 : 0);
-                            if (row < p.n && (r & ~1) < p.m) *reinterpret_cast<uint32_t*>(tr + static_cast<size_t>(row) * p.m) = y;
+                            const uint32_t row = 2 * i + (odd ? 1 : 0);
+                            st_shared_b32(base + row * 64 + (((kb >> 4) ^ ((row >> 1) & 3)) << 4) + (kb & 15), y);
                         }
                     }
                 }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (it.ph == 0) tma_store_3d(&maps.ea, slot, c, r0, it.e);
+                    else if (it.ph == 1) tma_store_3d(&maps.er, slot, c, r0, it.e);
+                    else if (!last) tma_store_3d(&maps.exh[x ^ 1], slot, c, r0, it.e);
+                    else if (!p.tall) tma_store_3d(&maps.eout, slot, c, r0, it.e);
+                    if (low_out) tma_store_3d(&maps.exl[x ^ 1], slot2, c, r0, it.e);
+                    if (mirror || tall_out) {
+                        const CUtensorMap* t = it.ph == 0 ? &maps.ta : it.ph == 1 ? &maps.tr : &maps.tout;
+                        tma_store_3d(t, slot2, r0, c, it.e);
+                        if (c + 32 < cols) tma_store_3d(t, slot2 + 2048, r0, c + 32, it.e);
+                    }
+                    bulk_commit_group();
+                }
             }
             tc_fence_before();
-            asm volatile("fence.proxy.async;" ::: "memory");  // these stores before other SMs' TMA loads of them
             __syncwarp();
             if (lane == 0) {
                 if (leader) mbar_arrive(bar_tempty + 8 * buf);
                 else mbar_arrive_cluster(tempty_leader + 8 * buf);
-            }
-            named_bar_sync(EPI_BAR, 32 * EPI_WARPS);
-            if (warp == EPI0 && lane == 0) {
+                // the stores have arrived (asynchronous proxy): others may load them
+                bulk_wait_group_all();
+                asm volatile("fence.proxy.async;" ::: "memory");
                 __threadfence();
                 red_release_gpu_add(p.done + it.e * 3 * p.steps + 3 * it.step + it.ph, 1);
             }
+            __syncwarp();
         }
+        if (lane == 0) bulk_wait_group_all();
     }
     tc_fence_before();
     cluster_sync_all();
@@ -560,11 +606,12 @@ void layout(int E, int N, int K, Layout* l) {
     l->total = at;
 }
 
-int map2(CUtensorMap* map, const void* base, int cols, int ld, int rows, int E, int box_cols, int box_rows) {
+int map2(CUtensorMap* map, const void* base, int cols, int ld, int rows, int E, int box_cols, int box_rows, bool bf16 = false) {
     const uint64_t d[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(E)};
     const uint64_t s[2] = {2 * static_cast<uint64_t>(ld), 2 * static_cast<uint64_t>(ld) * rows};
     const uint32_t b[3] = {static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows), 1};
-    return host_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+    return host_tensor_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, d, s, b,
+                           box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -587,13 +634,8 @@ int launch_muon(const MuonArgs& a) {
     if (static_cast<long long>(a.steps) * a.E * (2LL * p.sym + p.full) > 0x7fffffffLL / 2)
         return host_fail(MXFP8_EINVAL, "E=%d N=%d K=%d steps=%d: too many tiles", a.E, a.N, a.K, a.steps);
     p.a = a.a; p.b = a.b; p.c = a.c;
-    for (int i = 0; i < 2; ++i) {
-        p.Xh[i] = reinterpret_cast<__half*>(a.ws + l.xh[i]);
-        p.Xl[i] = reinterpret_cast<__half*>(a.ws + l.xl[i]);
-    }
-    p.A = reinterpret_cast<__half*>(a.ws + l.a);
-    p.R = reinterpret_cast<__half*>(a.ws + l.r);
-    p.out = a.out;
+    p.Xh = reinterpret_cast<__half*>(a.ws + l.xh[0]);
+    p.Xl = reinterpret_cast<__half*>(a.ws + l.xl[0]);
     p.done = reinterpret_cast<unsigned int*>(a.ws + l.done);
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
@@ -601,11 +643,19 @@ int launch_muon(const MuonArgs& a) {
     Maps maps;
     int rc = MXFP8_OK;
     for (int i = 0; i < 2 && !rc; ++i) {
-        rc = map2(&maps.xk[i], p.Xh[i], l.n, l.ldn, l.m, a.E, KSTEP, HALF);
-        if (!rc) rc = map2(&maps.xm[i], p.Xh[i], l.n, l.ldn, l.m, a.E, 64, KSTEP);
+        rc = map2(&maps.xk[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, KSTEP, HALF);
+        if (!rc) rc = map2(&maps.xm[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, 64, KSTEP);
+        if (!rc) rc = map2(&maps.exh[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, 64, 32);
+        if (!rc) rc = map2(&maps.exl[i], a.ws + l.xl[i], l.n, l.ldn, l.m, a.E, 64, 32);
     }
-    if (!rc) rc = map2(&maps.a, p.A, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
-    if (!rc) rc = map2(&maps.r, p.R, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
+    if (!rc) rc = map2(&maps.a, a.ws + l.a, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
+    if (!rc) rc = map2(&maps.r, a.ws + l.r, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
+    if (!rc) rc = map2(&maps.ea, a.ws + l.a, l.m, l.ldm, l.m, a.E, 64, 32);
+    if (!rc) rc = map2(&maps.er, a.ws + l.r, l.m, l.ldm, l.m, a.E, 64, 32);
+    if (!rc) rc = map2(&maps.ta, a.ws + l.a, l.m, l.ldm, l.m, a.E, 32, 32);
+    if (!rc) rc = map2(&maps.tr, a.ws + l.r, l.m, l.ldm, l.m, a.E, 32, 32);
+    if (!rc) rc = map2(&maps.eout, a.out, a.K, a.K, a.N, a.E, 64, 32, true);
+    if (!rc) rc = map2(&maps.tout, a.out, a.K, a.K, a.N, a.E, 32, 32, true);
     if (rc) return rc;
 
     static std::atomic<int> max_pairs[64];
