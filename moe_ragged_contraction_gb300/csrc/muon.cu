@@ -41,14 +41,16 @@ namespace mxw {
 namespace {
 
 constexpr int NORM_BLOCKS = 64;      // partial sums per matrix
-constexpr int TILE = 256;            // rows and columns of a pair's tile
-constexpr int HALF = TILE / 2;       // each CTA's rows of either operand
-constexpr int KSTEP = 64;               // contraction columns of a stage (128 bytes)
+constexpr int TILE = 256;            // rows of a pair's tile (each CTA: 128); its columns: 256 or 128
+constexpr int HALF = TILE / 2;
+constexpr int KSTEP = 64;            // contraction columns of a stage (128 bytes)
 constexpr int OP_BYTES = HALF * KSTEP * 2;
 constexpr int STAGES = 5;
-constexpr int SLOT = 32 * 128;          // an epilogue warp's 32 rows x 64 columns of fp16; two slots per warp
 constexpr int EPI0 = 2, EPI_WARPS = 8;
-constexpr int THREADS = 32 * (EPI0 + EPI_WARPS);
+constexpr int SCOUT = EPI0 + EPI_WARPS;  // warp that waits for the products that a tile needs
+constexpr int THREADS = 32 * (SCOUT + 1);
+constexpr int AHEAD = 4;             // tiles the scout may be ahead
+constexpr int SLOT = 32 * 128;       // 32 rows x 64 columns of fp16; two slots per epilogue warp
 constexpr int OFF_EPI = STAGES * 2 * OP_BYTES, OFF_BAR = OFF_EPI + 2 * EPI_WARPS * SLOT;
 constexpr int SMEM = OFF_BAR + 1024 + 512;
 static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -56,11 +58,11 @@ static_assert(SMEM <= 232448, "shared memory of a CTA");
 constexpr float SX = 2048.f;         // X
 constexpr float SLO = 2048.f;        // lower plane of X, on top of SX
 constexpr float SA = 4096.f;         // A and R
-// kind::f16: fp16 x fp16 -> fp32, M = 256 across the pair, N = 256; bit 16: B is MN-major
-constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE >> 3) << 17) | (static_cast<uint32_t>(TILE >> 4) << 24);
+// kind::f16: fp16 x fp16 -> fp32, M = 256 across the pair; bits 17-22: N / 8; bit 16: B is MN-major
+constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE >> 4) << 24);
 
 struct Params {
-    int E, m, n, ldm, ldn, steps, tall, T, Tn, sym, full;  // tiles along m and n; tiles of a symmetric product and of R X
+    int E, m, n, ldm, ldn, steps, tall, tn, T, sym, full;  // columns of a tile; tiles along m; tiles of a symmetric product and of R X
     float a, b, c;
     __half *Xh, *Xl;     // X0's planes
     unsigned int* done;  // [E][3 steps] epilogue warps' shares of tiles stored
@@ -69,9 +71,10 @@ struct Params {
 };
 
 struct Maps {
-    CUtensorMap xk[2], xm[2], a, r;   // operands: X by rows and by 64 x 64 boxes (its columns as the MMA's N), A, R
+    // X by rows (as the MMA's M and N sides) and by 64 x 64 boxes (its columns as the N side), A likewise, R
+    CUtensorMap xk[2], xkn[2], xm[2], a, an, r;
     CUtensorMap exh[2], exl[2], ea, er, eout;  // epilogue: boxes of 32 rows x 64 columns
-    CUtensorMap ta, tr, tout;         // transposed: boxes of 32 rows x 32 columns
+    CUtensorMap ta, tr, tout;                  // transposed: boxes of 32 x 32
 };
 
 // ============================================================== momentum, norm, X0
@@ -230,9 +233,19 @@ __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
-__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
+// Wait until all but the latest of this thread's committed bulk groups have completed.
+__device__ __forceinline__ void bulk_wait_group_but_one() { asm volatile("cp.async.bulk.wait_group 1;" ::: "memory"); }
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t* v) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr) : "memory");
 }
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 t = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+__device__ __forceinline__ float2 bits_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
 __device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -274,12 +287,18 @@ __device__ __forceinline__ Item get_item(const Params& p, int q) {
     if (it.ph == 2) {
         it.j = q / p.T;
         it.i = q - it.j * p.T;
-    } else {
+    } else if (p.tn == TILE) {  // row i holds i + 1 tiles on and below the diagonal
         int i = static_cast<int>((sqrtf(8.f * q + 1.f) - 1.f) * 0.5f);
         while (i * (i + 1) / 2 > q) --i;
         while ((i + 1) * (i + 2) / 2 <= q) ++i;
         it.i = i;
         it.j = q - i * (i + 1) / 2;
+    } else {                    // 2 i + 2 tiles of half the width
+        int i = static_cast<int>((sqrtf(4.f * q + 1.f) - 1.f) * 0.5f);
+        while (i * (i + 1) > q) --i;
+        while ((i + 1) * (i + 2) <= q) ++i;
+        it.i = i;
+        it.j = q - i * (i + 1);
     }
     it.ksteps = ((it.ph == 0 ? p.n : p.m) + KSTEP - 1) / KSTEP;
     return it;
@@ -295,8 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const bool leader = rank == 0;
     const uint32_t bars = sbase + OFF_BAR;
     const uint32_t bar_full = bars, bar_empty = bars + 8 * STAGES, bar_tfull = bar_empty + 8 * STAGES, bar_tempty = bar_tfull + 16,
-                   bar_drain = bar_tempty + 16, bar_epi = bar_drain + 8;
-    int* flags = reinterpret_cast<int*>(smem + OFF_BAR + 8 * (2 * STAGES + 5 + EPI_WARPS));  // abort, TMEM base
+                   bar_drain = bar_tempty + 16, bar_epi = bar_drain + 8, bar_dep = bar_epi + 8 * EPI_WARPS, bar_dfree = bar_dep + 8 * AHEAD;
+    int* flags = reinterpret_cast<int*>(smem + OFF_BAR + 8 * (2 * STAGES + 5 + EPI_WARPS + 2 * AHEAD));  // abort, TMEM base
     volatile int* abort_flag = flags;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -309,6 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         mbar_init(bar_drain, 1);
         for (int w = 0; w < EPI_WARPS; ++w) mbar_init(bar_epi + 8 * w, 1);
+        for (int i = 0; i < AHEAD; ++i) {
+            mbar_init(bar_dep + 8 * i, 1);                // scout: the tile's inputs are there
+            mbar_init(bar_dfree + 8 * i, 1 + EPI_WARPS);  // producer and epilogue warps have seen it
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -331,27 +354,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int c = 0, st = 0;
             uint32_t ph = 1;
             bool ok = true;
-            for (int q = pair; ok && q < total; q += G) {
-                const Item it = get_item(p, q);
-                const int gp = 3 * it.step + it.ph;
-                if (gp) {  // the matrix's product before this one
-                    ok = wait_count(p.done + it.e * 3 * p.steps + gp - 1, 2 * EPI_WARPS * (it.ph == 0 ? p.full : p.sym), abort_flag, p.wait_ns, p.status);
-                    if (!ok) break;
-                    asm volatile("fence.proxy.async;" ::: "memory");
-                }
+            int tile = 0;
+            Item next = get_item(p, pair);
+            for (int q = pair; ok && q < total; q += G, ++tile) {
+                const Item it = next;
+                if (q + G < total) next = get_item(p, q + G);
+                ok = wait_bar(bar_dep + 8 * (tile % AHEAD), (tile / AHEAD) & 1, abort_flag, p.wait_ns, p.status);
+                if (!ok) break;
+                mbar_arrive(bar_dfree + 8 * (tile % AHEAD));
                 const int x = it.step & 1;
                 const CUtensorMap* ma = it.ph == 0 ? &maps.xk[x] : it.ph == 1 ? &maps.a : &maps.r;
-                const CUtensorMap* mb = it.ph == 2 ? &maps.xm[x] : ma;
-                const int ra = it.i * TILE + static_cast<int>(rank) * HALF, rb = it.j * TILE + static_cast<int>(rank) * HALF;
+                const CUtensorMap* mb = it.ph == 0 ? &maps.xkn[x] : it.ph == 1 ? &maps.an : &maps.xm[x];
+                const int ra = it.i * TILE + static_cast<int>(rank) * HALF, rb = it.j * p.tn + static_cast<int>(rank) * (p.tn / 2);
                 for (int k = 0; k < it.ksteps; ++k, ++c) {
                     ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
                     if (!ok) break;
                     const uint32_t da = sbase + st * 2 * OP_BYTES, db = da + OP_BYTES, fb = full_leader + 8 * st;
-                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 4 * OP_BYTES);
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 2 * (HALF + p.tn / 2) * KSTEP * 2);
                     tma_load_3d_pair(da, ma, fb, k * KSTEP, ra, it.e);
                     if (it.ph == 2) {
                         tma_load_3d_pair(db, mb, fb, rb, k * KSTEP, it.e);
-                        tma_load_3d_pair(db + OP_BYTES / 2, mb, fb, rb + 64, k * KSTEP, it.e);
+                        if (p.tn == TILE) tma_load_3d_pair(db + OP_BYTES / 2, mb, fb, rb + 64, k * KSTEP, it.e);
                     } else {
                         tma_load_3d_pair(db, mb, fb, k * KSTEP, rb, it.e);
                     }
@@ -377,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 tc_fence_after();
                 const uint32_t d = tmem + buf * TILE;
                 const bool mn = it.ph == 2;
-                const uint32_t idesc = IDESC | (mn ? 1u << 16 : 0u);
+                const uint32_t idesc = IDESC | (static_cast<uint32_t>(p.tn >> 3) << 17) | (mn ? 1u << 16 : 0u);
                 const uint32_t bstep = mn ? 2048 >> 4 : 32 >> 4;  // 16 contraction rows, or 32 bytes along a row
                 for (int k = 0; k < it.ksteps; ++k) {
                     ok = wait_bar(bar_full + 8 * st, ph, abort_flag, p.wait_ns, p.status);
@@ -400,48 +423,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
         __syncwarp();
+    } else if (warp == SCOUT) {
+        // ------------------------------------------------ scout (both CTAs)
+        // Waits, up to AHEAD tiles ahead, until the product before a tile's of the
+        // same matrix is complete: a round trip to L2 and a fence that would
+        // otherwise stand between two tiles' loads.
+        if (lane == 0) {
+            int tile = 0;
+            for (int q = pair; q < total; q += G, ++tile) {
+                const Item it = get_item(p, q);
+                const int gp = 3 * it.step + it.ph;
+                if (!wait_bar(bar_dfree + 8 * (tile % AHEAD), ((tile / AHEAD) & 1) ^ 1, abort_flag, p.wait_ns, p.status)) break;
+                if (gp) {
+                    if (!wait_count(p.done + it.e * 3 * p.steps + gp - 1, 2 * EPI_WARPS * (it.ph == 0 ? p.full : p.sym), abort_flag,
+                                    p.wait_ns, p.status))
+                        break;
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                }
+                mbar_arrive(bar_dep + 8 * (tile % AHEAD));
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------ epilogue (8 warps per CTA)
-        // A warp owns 32 rows (its TMEM quarter) x 128 columns of the CTA's half
+        // A warp owns 32 rows (its TMEM quarter) x half the columns of the CTA's
         // tile, in chunks of 64 columns. What a chunk adds to (A, or X's planes)
-        // is loaded by TMA into the warp's two slots, replaced there by the
-        // result and stored by TMA: whole lines either way (per-lane accesses to
-        // 32 rows at once took 13 us a tile, twice the products' time).
+        // is loaded by TMA into the warp's two slots (the first chunk's before the
+        // products are done), replaced there by the result and stored by TMA:
+        // whole 128-byte lines either way. (Measured at the 16B shape, whole call:
+        // this 0.60 ms; chunks of 32 columns, 64-byte lines, 0.65; from registers,
+        // 8 rows x 64 bytes at a time, 0.78; lane by lane 0.76.) A tile is reported
+        // done when its stores have arrived: after the next tile's first chunk
+        // where that tile is ready by then.
         const int q4 = warp & 3, h = (warp - EPI0) >> 2;
         const uint32_t tempty_leader = mapa_shared(bar_tempty, 0);
         const uint32_t slot = sbase + OFF_EPI + (warp - EPI0) * 2 * SLOT, slot2 = slot + SLOT, bar_in = bar_epi + 8 * (warp - EPI0);
         const uint32_t row_at = lane * 128, sw = lane & 7;  // 16-byte piece k of the lane's row: row_at + ((k ^ sw) << 4)
         const bool odd = lane & 1;
+        const int width = p.tn / 2;
         int tile = 0;
         uint32_t in_ph = 0;
         bool ok = true;
-        for (int q = pair; ok && q < total; q += G, ++tile) {
+        unsigned int* pending = nullptr;  // lane 0: the finished tile that is not reported yet
+        auto report = [&]() {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __threadfence();
+            red_release_gpu_add(pending, 1);
+            pending = nullptr;
+        };
+        for (int q = pair; q < total; q += G, ++tile) {
             const Item it = get_item(p, q);
             const int buf = tile & 1;
-            if (lane == 0) ok = wait_bar(bar_tfull + 8 * buf, (tile >> 1) & 1, abort_flag, p.wait_ns, p.status);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-            tc_fence_after();
             const int r0 = it.i * TILE + static_cast<int>(rank) * HALF + q4 * 32, r = r0 + lane;  // row of the product
             const bool last = it.step + 1 == p.steps;
             const float shift = last ? 0.875f * (p.b + p.c) : it.step + 2 == p.steps ? 0.4375f * (p.b + p.c) : 0.f;
-            const int cols = it.ph == 2 ? p.n : p.m, x = it.step & 1;
-            const bool mirror = it.ph < 2 && it.i != it.j;
-            const bool low_in = it.ph == 2 && (!last || p.steps == 1), low_out = it.ph == 2 && it.step + 2 < p.steps;
+            const int cols = it.ph == 2 ? p.n : p.m, x = it.step & 1, c0 = it.j * p.tn + h * width;
+            const int chunks = r0 < p.m && c0 < cols ? min(width, cols - c0 + 63) >> 6 : 0;
+            const bool mirror = it.ph < 2 && it.j * p.tn < it.i * TILE;
+            // the last step reads the upper plane only (its roundings are not amplified)
+            const bool low_in = it.ph == 2 && !last, low_out = it.ph == 2 && it.step + 2 < p.steps;
             const bool tall_out = it.ph == 2 && last && p.tall;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + buf * TILE + h * HALF;
-#pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch) {
-                const int c = it.j * TILE + h * HALF + 64 * ch;
-                if (c >= cols || r0 >= p.m) break;
-                if (lane == 0) {
-                    bulk_wait_group_read<0>();  // the slots' last stores have been read
-                    if (it.ph) {
-                        mbar_arrive_expect_tx(bar_in, low_in ? 2 * SLOT : SLOT);
-                        tma_load_3d_plain(slot, it.ph == 1 ? &maps.ea : &maps.exh[x], bar_in, c, r0, it.e);
-                        if (low_in) tma_load_3d_plain(slot2, &maps.exl[x], bar_in, c, r0, it.e);
-                    }
+            auto load = [&](int c) {
+                bulk_wait_group_read<0>();  // the slots' last stores have been read
+                if (!it.ph) return;
+                mbar_arrive_expect_tx(bar_in, low_in ? 2 * SLOT : SLOT);
+                tma_load_3d_plain(slot, it.ph == 1 ? &maps.ea : &maps.exh[x], bar_in, c, r0, it.e);
+                if (low_in) tma_load_3d_plain(slot2, &maps.exl[x], bar_in, c, r0, it.e);
+            };
+            if (lane == 0) {
+                const bool ready = mbar_try_wait(bar_tfull + 8 * buf, (tile >> 1) & 1);
+                if (pending && (!ready || !chunks)) {  // never wait with a tile unreported
+                    bulk_wait_group_all();
+                    report();
                 }
+                ok = wait_bar(bar_dep + 8 * (tile % AHEAD), (tile / AHEAD) & 1, abort_flag, p.wait_ns, p.status);
+                if (ok) {
+                    mbar_arrive(bar_dfree + 8 * (tile % AHEAD));
+                    if (chunks) load(c0);
+                    ok = ready || wait_bar(bar_tfull + 8 * buf, (tile >> 1) & 1, abort_flag, p.wait_ns, p.status);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + buf * TILE + h * width;
+#pragma unroll 1
+            for (int ch = 0; ch < chunks; ++ch) {
+                const int c = c0 + 64 * ch;
+                if (lane == 0 && ch) load(c);
                 __syncwarp();
                 if (it.ph) {
                     if (lane == 0) ok = wait_bar(bar_in, in_ph, abort_flag, p.wait_ns, p.status);
@@ -454,27 +523,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(taddr + 64 * ch + 32 * hf, v);
+                    uint32_t u[16], w[16];
+                    const uint32_t at = slot + row_at, at2 = slot2 + row_at;
+                    if (it.ph) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ld_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u + 4 * k);
+                    }
+                    if (low_in) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) ld_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), w + 4 * k);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = 0;
+                    }
                     tmem_wait_ld();
                     reg_fence(v);
                     float f[32];
-                    const uint32_t at = slot + row_at, at2 = slot2 + row_at;
                     if (it.ph == 0) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * (SA / (SX * SX));
                     } else if (it.ph == 1) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t u[4];
-                            ld_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-                                const int i = 8 * k + 2 * j;
-                                f[i] = fmaf(p.c / SA, __uint_as_float(v[i]), p.b * t.x);
-                                f[i + 1] = fmaf(p.c / SA, __uint_as_float(v[i + 1]), p.b * t.y);
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 t = bits_half2(u[i]);
+                            f[2 * i] = fmaf(p.c / SA, __uint_as_float(v[2 * i]), p.b * t.x);
+                            f[2 * i + 1] = fmaf(p.c / SA, __uint_as_float(v[2 * i + 1]), p.b * t.y);
                         }
-                        if (it.i == it.j) {
+                        if (!mirror) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (r == c + 32 * hf + i) f[i] -= shift * SA;
@@ -482,62 +557,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     } else {
                         const float ax = p.a + shift;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t u[4], w[4] = {0, 0, 0, 0};
-                            ld_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u);
-                            if (low_in) ld_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), w);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-                                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                                const int i = 8 * k + 2 * j;
-                                f[i] = fmaf(ax, fmaf(1.f / SLO, l.x, t.x), __uint_as_float(v[i]) * (1.f / SA));
-                                f[i + 1] = fmaf(ax, fmaf(1.f / SLO, l.y, t.y), __uint_as_float(v[i + 1]) * (1.f / SA));
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 t = bits_half2(u[i]), l = bits_half2(w[i]);
+                            f[2 * i] = fmaf(ax, fmaf(1.f / SLO, l.x, t.x), __uint_as_float(v[2 * i]) * (1.f / SA));
+                            f[2 * i + 1] = fmaf(ax, fmaf(1.f / SLO, l.y, t.y), __uint_as_float(v[2 * i + 1]) * (1.f / SA));
                         }
                     }
-                    uint32_t w[16];
                     if (it.ph == 2 && last) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            w[i] = pack_bf16x2(__float_as_uint(f[2 * i] * (1.f / SX)), __float_as_uint(f[2 * i + 1] * (1.f / SX)));
+                            u[i] = pack_bf16x2(__float_as_uint(f[2 * i] * (1.f / SX)), __float_as_uint(f[2 * i + 1] * (1.f / SX)));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                            w[i] = *reinterpret_cast<const uint32_t*>(&t);
-                        }
+                        for (int i = 0; i < 16; ++i) u[i] = half2_bits(f[2 * i], f[2 * i + 1]);
                     }
                     if (!tall_out) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            st_shared_v4(at + (((4 * hf + k) ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                            st_shared_v4(at + (((4 * hf + k) ^ sw) << 4), u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
                     }
                     if (low_out) {
-                        // the lower plane (the last step reads the upper one only)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t y[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int i = 8 * k + 2 * j;
-                                const float2 hv = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * k + j]));
-                                const __half2 t = __floats2half2_rn((f[i] - hv.x) * SLO, (f[i + 1] - hv.y) * SLO);
-                                y[j] = *reinterpret_cast<const uint32_t*>(&t);
-                            }
-                            st_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), y[0], y[1], y[2], y[3]);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 hv = bits_half2(u[i]);
+                            w[i] = half2_bits((f[2 * i] - hv.x) * SLO, (f[2 * i + 1] - hv.y) * SLO);
                         }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(at2 + (((4 * hf + k) ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                     }
                     if (mirror || tall_out) {
                         // transposed, 32 rows (this product's columns) of 64 bytes with
                         // the 64-byte swizzle; lanes r, r + 1 exchange halves: the even
                         // lane stores (r, r + 1) of row 2 i, the odd lane of 2 i + 1
-                        const uint32_t base = slot2 + hf * 2048, kb = static_cast<uint32_t>(lane & ~1) * 2;
-                        __syncwarp();
+                        const uint32_t base = slot2 + hf * (SLOT / 2), kb = static_cast<uint32_t>(lane & ~1) * 2;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, w[i], 1);
-                            const uint32_t y = odd ? __byte_perm(got, w[i], 0x7632) : __byte_perm(w[i], got, 0x5410);
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, u[i], 1);
+                            const uint32_t y = odd ? __byte_perm(got, u[i], 0x7632) : __byte_perm(u[i], got, 0x5410);
                             const uint32_t row = 2 * i + (odd ? 1 : 0);
                             st_shared_b32(base + row * 64 + (((kb >> 4) ^ ((row >> 1) & 3)) << 4) + (kb & 15), y);
                         }
@@ -546,33 +603,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    if (it.ph == 0) tma_store_3d(&maps.ea, slot, c, r0, it.e);
-                    else if (it.ph == 1) tma_store_3d(&maps.er, slot, c, r0, it.e);
-                    else if (!last) tma_store_3d(&maps.exh[x ^ 1], slot, c, r0, it.e);
-                    else if (!p.tall) tma_store_3d(&maps.eout, slot, c, r0, it.e);
+                    if (!tall_out)
+                        tma_store_3d(it.ph == 0 ? &maps.ea : it.ph == 1 ? &maps.er : last ? &maps.eout : &maps.exh[x ^ 1], slot, c, r0, it.e);
                     if (low_out) tma_store_3d(&maps.exl[x ^ 1], slot2, c, r0, it.e);
                     if (mirror || tall_out) {
                         const CUtensorMap* t = it.ph == 0 ? &maps.ta : it.ph == 1 ? &maps.tr : &maps.tout;
                         tma_store_3d(t, slot2, r0, c, it.e);
-                        if (c + 32 < cols) tma_store_3d(t, slot2 + 2048, r0, c + 32, it.e);
+                        if (c + 32 < cols) tma_store_3d(t, slot2 + SLOT / 2, r0, c + 32, it.e);
                     }
                     bulk_commit_group();
+                    if (pending) {  // all stores but this chunk's have arrived
+                        bulk_wait_group_but_one();
+                        report();
+                    }
                 }
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (leader) mbar_arrive(bar_tempty + 8 * buf);
                 else mbar_arrive_cluster(tempty_leader + 8 * buf);
-                // the stores have arrived (asynchronous proxy): others may load them
-                bulk_wait_group_all();
-                asm volatile("fence.proxy.async;" ::: "memory");
-                __threadfence();
-                red_release_gpu_add(p.done + it.e * 3 * p.steps + 3 * it.step + it.ph, 1);
+                pending = p.done + it.e * 3 * p.steps + 3 * it.step + it.ph;
             }
-            __syncwarp();
         }
-        if (lane == 0) bulk_wait_group_all();
+        if (lane == 0) {
+            bulk_wait_group_all();
+            if (pending) report();
+        }
+        __syncwarp();
     }
     tc_fence_before();
     cluster_sync_all();
@@ -606,7 +665,7 @@ void layout(int E, int N, int K, Layout* l) {
     l->total = at;
 }
 
-int map2(CUtensorMap* map, const void* base, int cols, int ld, int rows, int E, int box_cols, int box_rows, bool bf16 = false) {
+int map2(CUtensorMap* map, const void* base, int cols, int ld, int rows, int E, int box_rows, int box_cols = KSTEP, bool bf16 = false) {
     const uint64_t d[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(E)};
     const uint64_t s[2] = {2 * static_cast<uint64_t>(ld), 2 * static_cast<uint64_t>(ld) * rows};
     const uint32_t b[3] = {static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows), 1};
@@ -627,10 +686,15 @@ int launch_muon(const MuonArgs& a) {
     layout(a.E, a.N, a.K, &l);
     Params p{};
     p.E = a.E; p.m = l.m; p.n = l.n; p.ldm = l.ldm; p.ldn = l.ldn; p.steps = a.steps; p.tall = a.N > a.K;
-    p.T = (l.m + TILE - 1) / TILE;
-    p.Tn = (l.n + TILE - 1) / TILE;
-    p.sym = p.T * (p.T + 1) / 2;
-    p.full = p.T * p.Tn;
+    // Tiles of 128 columns where those of 256 would leave pairs without one: each
+    // then takes half the time to compute and store.
+    const int T = (l.m + TILE - 1) / TILE, wide = T * ((l.n + TILE - 1) / TILE);
+    p.tn = static_cast<long long>(a.E) * wide <= a.num_sms / 2 ? TILE / 2 : TILE;
+    const int Tm = (l.m + p.tn - 1) / p.tn;
+    p.T = T;
+    p.full = T * ((l.n + p.tn - 1) / p.tn);
+    p.sym = 0;
+    for (int i = 0; i < T; ++i) p.sym += Tm < (i + 1) * (TILE / p.tn) ? Tm : (i + 1) * (TILE / p.tn);
     if (static_cast<long long>(a.steps) * a.E * (2LL * p.sym + p.full) > 0x7fffffffLL / 2)
         return host_fail(MXFP8_EINVAL, "E=%d N=%d K=%d steps=%d: too many tiles", a.E, a.N, a.K, a.steps);
     p.a = a.a; p.b = a.b; p.c = a.c;
@@ -642,20 +706,23 @@ int launch_muon(const MuonArgs& a) {
     float* part = reinterpret_cast<float*>(a.ws + l.part);
     Maps maps;
     int rc = MXFP8_OK;
+    const int E = a.E;
     for (int i = 0; i < 2 && !rc; ++i) {
-        rc = map2(&maps.xk[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, KSTEP, HALF);
-        if (!rc) rc = map2(&maps.xm[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, 64, KSTEP);
-        if (!rc) rc = map2(&maps.exh[i], a.ws + l.xh[i], l.n, l.ldn, l.m, a.E, 64, 32);
-        if (!rc) rc = map2(&maps.exl[i], a.ws + l.xl[i], l.n, l.ldn, l.m, a.E, 64, 32);
+        rc = map2(&maps.xk[i], a.ws + l.xh[i], l.n, l.ldn, l.m, E, HALF);
+        if (!rc) rc = map2(&maps.xkn[i], a.ws + l.xh[i], l.n, l.ldn, l.m, E, p.tn / 2);
+        if (!rc) rc = map2(&maps.xm[i], a.ws + l.xh[i], l.n, l.ldn, l.m, E, KSTEP);
+        if (!rc) rc = map2(&maps.exh[i], a.ws + l.xh[i], l.n, l.ldn, l.m, E, 32);
+        if (!rc) rc = map2(&maps.exl[i], a.ws + l.xl[i], l.n, l.ldn, l.m, E, 32);
     }
-    if (!rc) rc = map2(&maps.a, a.ws + l.a, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
-    if (!rc) rc = map2(&maps.r, a.ws + l.r, l.m, l.ldm, l.m, a.E, KSTEP, HALF);
-    if (!rc) rc = map2(&maps.ea, a.ws + l.a, l.m, l.ldm, l.m, a.E, 64, 32);
-    if (!rc) rc = map2(&maps.er, a.ws + l.r, l.m, l.ldm, l.m, a.E, 64, 32);
-    if (!rc) rc = map2(&maps.ta, a.ws + l.a, l.m, l.ldm, l.m, a.E, 32, 32);
-    if (!rc) rc = map2(&maps.tr, a.ws + l.r, l.m, l.ldm, l.m, a.E, 32, 32);
-    if (!rc) rc = map2(&maps.eout, a.out, a.K, a.K, a.N, a.E, 64, 32, true);
-    if (!rc) rc = map2(&maps.tout, a.out, a.K, a.K, a.N, a.E, 32, 32, true);
+    if (!rc) rc = map2(&maps.a, a.ws + l.a, l.m, l.ldm, l.m, E, HALF);
+    if (!rc) rc = map2(&maps.an, a.ws + l.a, l.m, l.ldm, l.m, E, p.tn / 2);
+    if (!rc) rc = map2(&maps.r, a.ws + l.r, l.m, l.ldm, l.m, E, HALF);
+    if (!rc) rc = map2(&maps.ea, a.ws + l.a, l.m, l.ldm, l.m, E, 32);
+    if (!rc) rc = map2(&maps.er, a.ws + l.r, l.m, l.ldm, l.m, E, 32);
+    if (!rc) rc = map2(&maps.ta, a.ws + l.a, l.m, l.ldm, l.m, E, 32, 32);
+    if (!rc) rc = map2(&maps.tr, a.ws + l.r, l.m, l.ldm, l.m, E, 32, 32);
+    if (!rc) rc = map2(&maps.eout, a.out, a.K, a.K, a.N, E, 32, 64, true);
+    if (!rc) rc = map2(&maps.tout, a.out, a.K, a.K, a.N, E, 32, 32, true);
     if (rc) return rc;
 
     static std::atomic<int> max_pairs[64];
