@@ -144,9 +144,9 @@ cudaError_t set_suspend_hint(uint32_t ns);
 // Device status word (MXFP8_DEV_* bits).
 cudaError_t read_device_status(int32_t* status, int clear);
 
-// Device address of the status word on the current device, for kernels of
-// other translation units.
-cudaError_t device_status_address(int** addr);
+// Device address of the status word on the current device `dev`, for kernels
+// of other translation units.
+cudaError_t device_status_address(int dev, int** addr);
 
 // Host services of abi.cu shared by the other entry points: sets the message
 // of mxfp8_last_error() and returns `code`; checks the current device (sm_103)

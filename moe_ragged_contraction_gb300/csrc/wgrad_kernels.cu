@@ -1911,11 +1911,19 @@ cudaError_t launch_gemm(const GemmArgs& a, const CUtensorMap* maps, const char**
 
 cudaError_t set_suspend_hint(uint32_t ns) { return cudaMemcpyToSymbol(g_suspend_ns, &ns, sizeof(ns)); }
 
-cudaError_t device_status_address(int** addr) {
-    void* p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_device_status);
-    *addr = static_cast<int*>(p);
-    return e;
+cudaError_t device_status_address(int dev, int** addr) {
+    // (looked up once per device: the context keeps the address)
+    static std::atomic<int*> known[64];
+    int* p = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : nullptr;
+    if (!p) {
+        void* q = nullptr;
+        const cudaError_t e = cudaGetSymbolAddress(&q, g_device_status);
+        if (e != cudaSuccess) return e;
+        p = static_cast<int*>(q);
+        if (dev >= 0 && dev < 64) known[dev].store(p, std::memory_order_relaxed);
+    }
+    *addr = p;
+    return cudaSuccess;
 }
 
 cudaError_t read_device_status(int32_t* status, int clear) {

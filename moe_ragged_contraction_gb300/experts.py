@@ -9,21 +9,23 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 MAX_TOKENS = 128
 
 _torch = None
+_raw_stream = None  # device index -> handle of the current stream
 
 
 def _torch_module():
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
 
+        # the public call builds a Stream object, several microseconds on a slow host
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
         _torch = torch
     return _torch
 
 
 def _check(t, dtype, shape, name, device):
     """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device."""
-    torch = _torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+    if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
         _lib._expect(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -38,11 +40,9 @@ def _device_and_stream(t, name, stream):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     device = t.get_device()
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    if stream.device_index != device or torch.cuda.current_device() != device:
+    if torch.cuda.current_device() != device or (stream is not None and stream.device_index != device):
         raise ValueError(f"{name} is on cuda:{device}: make it the current device, with a stream of that device")
-    return device, stream.cuda_stream
+    return device, _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, score="softmax", renormalize=True,
@@ -63,7 +63,7 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
         raise ValueError("x must be [T, H], router [experts, H] and w13 [local, 2 I, H]")
     T, H = x.shape
     experts = router.shape[0]
-    local, I2, _ = w13.shape
+    local, I2 = w13.shape[:2]
     I = I2 // 2
     u8, bf16, f32 = torch.uint8, torch.bfloat16, torch.float32
     _check(x, bf16, (T, H), "x", device)
