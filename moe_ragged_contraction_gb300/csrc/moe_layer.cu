@@ -378,7 +378,7 @@ struct Lists {
     uint16_t* slot_of;   // [slots] position of the entry among the local pairs sorted by expert
     uint16_t* entry_of;  // [slots] entry of a position
     uint16_t* act_of;    // [local] chosen-expert index of a local expert
-    uint16_t* count;     // [local] tokens; then [chosen] tokens of a chosen expert
+    uint16_t* count;     // [chosen] tokens of a chosen expert
     uint16_t* act;       // [local] local expert of a chosen-expert index
     uint16_t* off;       // [local] first position of a chosen expert
     int* info;           // chosen experts, most tokens of one
@@ -542,27 +542,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             __syncthreads();
         }
-        // ---- the (token, expert) pairs sorted by expert, in token order
-        if (warp == 0) {
-            for (int e = lane; e < p.local; e += 32) L.count[e] = 0;
-            __syncwarp();
-            for (int b = 0; ok && b < p.slots; b += 32) {
-                const int i = b + lane;
-                const int e = i < p.slots ? L.eid[i] : 0xffff;
-                const unsigned same = __match_any_sync(0xffffffffu, e != 0xffff ? e : 0x10000 + lane);
-                const int before = __popc(same & ((1u << lane) - 1));
-                const int base = e != 0xffff ? L.count[e] : 0;
-                __syncwarp();
-                if (e != 0xffff) {
-                    L.slot_of[i] = static_cast<uint16_t>(base + before);
-                    if (before == 0) L.count[e] = static_cast<uint16_t>(base + __popc(same));
-                }
-                __syncwarp();
+        // ---- the (token, expert) pairs sorted by expert, in token order: a token
+        // mask per expert, whose bit counts are the experts' sizes and the pairs'
+        // ranks whatever the order in which the bits were set
+        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + p.off_ring);  // [local][4]
+        for (int i = threadIdx.x; i < 4 * p.local; i += THREADS) mask[i] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; ok && i < p.slots; i += THREADS)
+            if (L.eid[i] != 0xffff) {
+                const int t = i / p.top_k;
+                atomicOr(mask + 4 * L.eid[i] + (t >> 5), 1u << (t & 31));
             }
+        __syncthreads();
+        if (warp == 0) {
             int chosen = 0, first = 0, most = 0;
             for (int b = 0; b < p.local; b += 32) {
                 const int e = b + lane;
-                const int n = e < p.local ? L.count[e] : 0;
+                int n = 0;
+                if (e < p.local) {
+                    const uint4 m = *reinterpret_cast<const uint4*>(mask + 4 * e);
+                    n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+                }
                 const unsigned have = __ballot_sync(0xffffffffu, n > 0);
                 int incl = n;
 #pragma unroll
@@ -570,30 +570,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int v = __shfl_up_sync(0xffffffffu, incl, d);
                     if (lane >= d) incl += v;
                 }
-                __syncwarp();
                 if (n > 0) {
                     const int a = chosen + __popc(have & ((1u << lane) - 1));
                     L.act[a] = static_cast<uint16_t>(e);
                     L.act_of[e] = static_cast<uint16_t>(a);
                     L.off[a] = static_cast<uint16_t>(first + incl - n);
-                    L.count[a] = static_cast<uint16_t>(n);  // a <= e: the counts still to be read lie behind
+                    L.count[a] = static_cast<uint16_t>(n);
                 }
-                __syncwarp();
                 chosen += __popc(have);
                 first += __shfl_sync(0xffffffffu, incl, 31);
                 most = max(most, __reduce_max_sync(0xffffffffu, n));
             }
-            for (int i = lane; ok && i < p.slots; i += 32)
-                if (L.eid[i] != 0xffff) {
-                    const int s = L.off[L.act_of[L.eid[i]]] + L.slot_of[i];
-                    L.slot_of[i] = static_cast<uint16_t>(s);
-                    L.entry_of[s] = static_cast<uint16_t>(i);
-                }
             if (lane == 0) {
-                L.info[0] = ok ? chosen : 0;
+                L.info[0] = chosen;
                 L.info[1] = most;
             }
         }
+        __syncthreads();
+        for (int i = threadIdx.x; ok && i < p.slots; i += THREADS)
+            if (L.eid[i] != 0xffff) {
+                const int t = i / p.top_k;
+                const uint32_t* m = mask + 4 * L.eid[i];
+                int s = L.off[L.act_of[L.eid[i]]] + __popc(m[t >> 5] & ((1u << (t & 31)) - 1));
+                for (int w = 0; w < (t >> 5); ++w) s += __popc(m[w]);
+                L.slot_of[i] = static_cast<uint16_t>(s);
+                L.entry_of[s] = static_cast<uint16_t>(i);
+            }
         fence_proxy_async_shared();  // the ring's space held the scores
         __syncthreads();
     }
@@ -923,11 +925,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j * TILE + row] = v[j];
                     named_bar_sync(EPI_BAR, 128);
-                    // warp q: tokens j0 + 2q, j0 + 2q + 1, both halves of the 64 inner rows
+                    // (token, half of the 64 inner rows) pairs, dealt to the warps
 #pragma unroll 1
-                    for (int o = 0; o < 4; ++o) {
-                        const int j = 2 * q + (o >> 1), i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
-                        if (j0 + j < nt && i0 < p.I) store_h(p, off + j0 + j, i0, x[j * TILE + i], x[j * TILE + TILE / 2 + i]);
+                    for (int o = q; o < 2 * min(8, nt - j0); o += 4) {
+                        const int j = o >> 1, i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
+                        if (i0 < p.I) store_h(p, off + j0 + j, i0, x[j * TILE + i], x[j * TILE + TILE / 2 + i]);
                     }
                 }
             }
