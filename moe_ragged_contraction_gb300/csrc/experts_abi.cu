@@ -110,7 +110,7 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     a.wait_limit_ns = mxw::host_wait_limit_ns();
     const cudaError_t e = mxw::device_status_address(a.dev, &a.status);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "device status: %s", cudaGetErrorString(e));
-    return mxw::launch_muon(a);
+    return mxw::muon_fits_small(N, K) ? mxw::launch_muon_small(a) : mxw::launch_muon(a);
 }
 
 }  // namespace

@@ -45,4 +45,8 @@ struct MuonArgs {
 size_t muon_ws_bytes(int E, int N, int K);
 int launch_muon(const MuonArgs& a);
 
+// Matrices that one cluster holds on chip (muon_small.cu): no scratch.
+bool muon_fits_small(int N, int K);
+int launch_muon_small(const MuonArgs& a);
+
 }  // namespace mxw
