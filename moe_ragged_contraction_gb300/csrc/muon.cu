@@ -40,7 +40,7 @@
 namespace mxw {
 namespace {
 
-constexpr int NORM_BLOCKS = 64;      // partial sums per matrix
+constexpr int NORM_BLOCKS = 256;     // partial sums per matrix
 constexpr int TILE = 256;            // rows of a pair's tile (each CTA: 128); its columns: 256 or 128
 constexpr int HALF = TILE / 2;
 constexpr int KSTEP = 64;            // contraction columns of a stage (128 bytes)
@@ -105,9 +105,14 @@ __device__ __forceinline__ float4 load_u(const MuonArgs& a, size_t i) {
 }
 
 __global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* part, unsigned int* done, int n_done) {
+    griddep_launch_dependents();
+    griddep_wait();  // the gradient may come from the kernel before, and a call before may still use the scratch
     const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
     float s = 0.f;
-    for (size_t i = 4 * (blockIdx.x * 256 + threadIdx.x); i < per; i += 4 * NORM_BLOCKS * 256) {
+    // a block's share is contiguous, four loads of a thread in flight
+    const size_t share = (per / 4 + NORM_BLOCKS - 1) / NORM_BLOCKS * 4, end = min(per, (blockIdx.x + 1) * share);
+#pragma unroll 4
+    for (size_t i = blockIdx.x * share + 4 * threadIdx.x; i < end; i += 4 * 256) {
         const float4 u = load_u<true>(a, base + i);
         s += (u.x * u.x + u.y * u.y) + (u.z * u.z + u.w * u.w);
     }
@@ -129,9 +134,13 @@ __global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* pa
 __global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params p, const float* part) {
     __shared__ float t[64][65];
     __shared__ float s_inv;
+    griddep_launch_dependents();
+    griddep_wait();
     const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
     if (threadIdx.x < 32) {
-        float s = part[e * NORM_BLOCKS + threadIdx.x] + part[e * NORM_BLOCKS + 32 + threadIdx.x];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NORM_BLOCKS / 32; ++i) s += part[e * NORM_BLOCKS + 32 * i + threadIdx.x];
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         // NaN where the sum is not finite: the whole matrix comes out as NaN
@@ -739,9 +748,21 @@ int launch_muon(const MuonArgs& a) {
         if (e != cudaSuccess || pairs < 1) return host_fail(MXFP8_ECUDA, "update kernel: %s", cudaGetErrorString(e));
         max_pairs[a.dev].store(pairs, std::memory_order_relaxed);
     }
-    muon_momentum<<<dim3(NORM_BLOCKS, a.E), 256, 0, a.stream>>>(a, part, p.done, a.E * 3 * a.steps);
-    muon_scale<<<dim3((a.K + 63) / 64, (a.N + 63) / 64, a.E), 256, 0, a.stream>>>(a, p, part);
-    e = cudaGetLastError();
+    // each kernel a programmatic dependent of the one before
+    cudaLaunchConfig_t pre = {};
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    pre.attrs = &pdl;
+    pre.numAttrs = 1;
+    pre.stream = a.stream;
+    pre.blockDim = dim3(256);
+    pre.gridDim = dim3(NORM_BLOCKS, a.E);
+    e = cudaLaunchKernelEx(&pre, muon_momentum, a, part, p.done, a.E * 3 * a.steps);
+    if (e == cudaSuccess) {
+        pre.gridDim = dim3((a.K + 63) / 64, (a.N + 63) / 64, a.E);
+        e = cudaLaunchKernelEx(&pre, muon_scale, a, p, static_cast<const float*>(part));
+    }
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     const int items = a.E * (p.full > p.sym ? p.full : p.sym);
     cudaLaunchConfig_t cfg = {};
@@ -749,12 +770,13 @@ int launch_muon(const MuonArgs& a) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     // CTAs wait on one another: all of them resident at once
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1] = pdl;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, muon_main, maps, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;

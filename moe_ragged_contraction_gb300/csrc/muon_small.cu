@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8);
     float* red = reinterpret_cast<float*>(smem + OFF_BAR + 32);   // [8] warps' sums of squares
     float* norms = red + 8;                                        // [8] CTAs' sums
+    griddep_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(bar, 1);
         fence_mbar_init();
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
         tmem_alloc_single(smem_u32(tmem_slot), 512);
         tmem_relinquish_single();
     }
+    griddep_wait();  // the gradient may come from the kernel before
     const int q4 = warp & 3, h = warp >> 2;         // TMEM quarter, half of the columns
     const int row = q4 * 32 + lane, width = p.w / 2;  // this thread's row; columns h * width ..
 
@@ -410,12 +412,14 @@ int launch_muon_small(const MuonArgs& a) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.C;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, muon_small, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;
