@@ -993,25 +993,39 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int o = cta * THREADS + threadIdx.x; o < p.T * half; o += G * THREADS) {
         const int t = o / half, n = 2 * (o - t * half), rt = n / TILE, r = n - rt * TILE;
         float y0 = 0.f, y1 = 0.f;
-        for (int k = 0; k < p.top_k; ++k) {
-            const int i = t * p.top_k + k, e = L.eid[i];
-            if (e == 0xffff) continue;
-            const int a = L.act_of[e], slot = L.slot_of[i], tl = a * p.down_tiles + rt;
-            if (queue.down_parts == 1) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(p.y + static_cast<size_t>(slot) * p.Hp + n));
-                y0 += v.x;
-                y1 += v.y;
-            } else {
-                float z0 = 0.f, z1 = 0.f;
-                for (int c = 0; c < queue.down_parts; ++c) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(
-                        p.part_down + (static_cast<size_t>(tl) * queue.down_parts + c) * p.T * TILE +
-                        static_cast<size_t>(slot - L.off[a]) * TILE + r));
-                    z0 += v.x;
-                    z1 += v.y;
+        // four of the token's experts at a time, their loads in flight together
+        for (int k0 = 0; k0 < p.top_k; k0 += 4) {
+            float2 v[4];
+            int e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = t * p.top_k + k0 + j;
+                e[j] = k0 + j < p.top_k ? L.eid[i] : 0xffff;
+                v[j] = make_float2(0.f, 0.f);
+                if (e[j] != 0xffff && queue.down_parts == 1)
+                    v[j] = __ldcg(reinterpret_cast<const float2*>(p.y + static_cast<size_t>(L.slot_of[i]) * p.Hp + n));
+            }
+            if (queue.down_parts > 1) {
+                // the parts of each down tile, in order; then the expert's weight
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (e[j] == 0xffff) continue;
+                    const int i = t * p.top_k + k0 + j, a = L.act_of[e[j]];
+                    const float* src = p.part_down + static_cast<size_t>(a * p.down_tiles + rt) * queue.down_parts * p.T * TILE +
+                                       static_cast<size_t>(L.slot_of[i] - L.off[a]) * TILE + r;
+                    for (int c = 0; c < queue.down_parts; ++c) {
+                        const float2 z = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(c) * p.T * TILE));
+                        v[j].x += z.x;
+                        v[j].y += z.y;
+                    }
+                    v[j].x *= L.wts[i];
+                    v[j].y *= L.wts[i];
                 }
-                y0 += z0 * L.wts[i];
-                y1 += z1 * L.wts[i];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y0 += v[j].x;
+                y1 += v[j].y;
             }
         }
         reinterpret_cast<uint32_t*>(p.out)[static_cast<size_t>(t) * half + (n >> 1)] = pack_bf16x2(__float_as_uint(y0), __float_as_uint(y1));
