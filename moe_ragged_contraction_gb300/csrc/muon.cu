@@ -63,6 +63,9 @@ constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(TILE >> 4) << 24);
 
 struct Params {
     int E, m, n, ldm, ldn, steps, tall, tn, T, sym, full;  // columns of a tile; tiles along m; tiles of a symmetric product and of R X
+    int parts;           // pieces into which the contraction of X X^T is cut
+    float* part;         // [E][sym][parts][2 CTAs][8 warps][tn / 2 columns][32 rows]
+    unsigned int* arrived;  // [E][sym][2][8] pieces done
     float a, b, c;
     __half *Xh, *Xl;     // X0's planes
     unsigned int* done;  // [E][3 steps] epilogue warps' shares of tiles stored
@@ -280,17 +283,24 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
 
 // A tile of a product: ph 0: A = X X^T, 1: R = b A + c A A - beta I, 2: X <- (a + beta) X + R X.
 struct Item {
-    int step, ph, e, i, j, ksteps;
+    int step, ph, e, i, j, k0, ksteps, tile, part;  // first K-step and their number; index and piece of a tile of X X^T
 };
 
 __device__ __forceinline__ Item get_item(const Params& p, int q) {
     Item it;
-    const int sym = p.E * p.sym, per = 2 * sym + p.E * p.full;
+    const int first = p.E * p.sym * p.parts, sym = p.E * p.sym, per = first + sym + p.E * p.full;
     it.step = q / per;
     q -= it.step * per;
-    it.ph = q < sym ? 0 : q < 2 * sym ? 1 : 2;
-    q -= it.ph * sym;
+    it.ph = q < first ? 0 : q < first + sym ? 1 : 2;
+    q -= it.ph == 0 ? 0 : it.ph == 1 ? first : first + sym;
+    it.part = 0;
+    if (it.ph == 0 && p.parts > 1) {
+        const int t = q / p.parts;
+        it.part = q - t * p.parts;
+        q = t;
+    }
     const int tiles = it.ph == 2 ? p.full : p.sym;
+    it.tile = q;
     it.e = q / tiles;
     q -= it.e * tiles;
     if (it.ph == 2) {
@@ -310,6 +320,11 @@ __device__ __forceinline__ Item get_item(const Params& p, int q) {
         it.j = q - i * (i + 1);
     }
     it.ksteps = ((it.ph == 0 ? p.n : p.m) + KSTEP - 1) / KSTEP;
+    it.k0 = 0;
+    if (it.ph == 0 && p.parts > 1) {
+        it.k0 = it.ksteps * it.part / p.parts;
+        it.ksteps = it.ksteps * (it.part + 1) / p.parts - it.k0;
+    }
     return it;
 }
 
@@ -354,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t tmem = static_cast<uint32_t>(flags[1]);
     griddep_wait();
     const int G = gridDim.x / 2, pair = blockIdx.x / 2;
-    const int total = p.steps * p.E * (2 * p.sym + p.full);
+    const int total = p.steps * p.E * (p.sym * (p.parts + 1) + p.full);
 
     if (warp == 0) {
         // ------------------------------------------------ loads (both CTAs)
@@ -380,12 +395,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (!ok) break;
                     const uint32_t da = sbase + st * 2 * OP_BYTES, db = da + OP_BYTES, fb = full_leader + 8 * st;
                     if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 2 * (HALF + p.tn / 2) * KSTEP * 2);
-                    tma_load_3d_pair(da, ma, fb, k * KSTEP, ra, it.e);
+                    const int kc = (it.k0 + k) * KSTEP;
+                    tma_load_3d_pair(da, ma, fb, kc, ra, it.e);
                     if (it.ph == 2) {
-                        tma_load_3d_pair(db, mb, fb, rb, k * KSTEP, it.e);
-                        if (p.tn == TILE) tma_load_3d_pair(db + OP_BYTES / 2, mb, fb, rb + 64, k * KSTEP, it.e);
+                        tma_load_3d_pair(db, mb, fb, rb, kc, it.e);
+                        if (p.tn == TILE) tma_load_3d_pair(db + OP_BYTES / 2, mb, fb, rb + 64, kc, it.e);
                     } else {
-                        tma_load_3d_pair(db, mb, fb, k * KSTEP, rb, it.e);
+                        tma_load_3d_pair(db, mb, fb, kc, rb, it.e);
                     }
                     if (++st == STAGES) { st = 0; ph ^= 1; }
                 }
@@ -516,8 +532,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + buf * TILE + h * width;
+            const bool split = it.ph == 0 && p.parts > 1;
+            const size_t piece = static_cast<size_t>(2 * EPI_WARPS) * width * 32;  // floats of one piece of a tile
+            const float* sums = p.part;
+            bool finish = true;
+            if (split) {
+                // this piece's sums, a column of 32 rows (a line) at a time; the warp
+                // that brings the last piece of its share goes on with all of them, in
+                // order
+                const int share = (it.tile * 2 + static_cast<int>(rank)) * EPI_WARPS + warp - EPI0;
+                sums = p.part + it.tile * p.parts * piece + static_cast<size_t>(static_cast<int>(rank) * EPI_WARPS + warp - EPI0) * width * 32 + lane;
+                float* dst = const_cast<float*>(sums) + it.part * piece;
 #pragma unroll 1
-            for (int ch = 0; ch < chunks; ++ch) {
+                for (int c = 0; c < 64 * chunks; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) dst[(c + i) * 32] = __uint_as_float(v[i]);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (pending) {
+                        bulk_wait_group_all();
+                        report();
+                    }
+                    __threadfence();
+                    finish = atom_acq_rel_gpu_add(p.arrived + share, 1) == static_cast<uint32_t>(p.parts - 1);
+                    if (finish) p.arrived[share] = 0;  // (the next step's pieces come long after)
+                    __threadfence();
+                }
+                finish = __shfl_sync(0xffffffffu, finish ? 1 : 0, 0) != 0;
+            }
+#pragma unroll 1
+            for (int ch = 0; finish && ch < chunks; ++ch) {
                 const int c = c0 + 64 * ch;
                 if (lane == 0 && ch) load(c);
                 __syncwarp();
@@ -531,7 +580,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
                     uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + 64 * ch + 32 * hf, v);
+                    if (split) {
+                        const float* src = sums + (64 * ch + 32 * hf) * 32;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0;
+#pragma unroll 1
+                        for (int s = 0; s < p.parts; ++s, src += piece)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(src + i * 32));
+                    } else {
+                        tmem_ld_32x32b_x32(taddr + 64 * ch + 32 * hf, v);
+                    }
                     uint32_t u[16], w[16];
                     const uint32_t at = slot + row_at, at2 = slot2 + row_at;
                     if (it.ph) {
@@ -633,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (lane == 0) {
                 if (leader) mbar_arrive(bar_tempty + 8 * buf);
                 else mbar_arrive_cluster(tempty_leader + 8 * buf);
-                pending = p.done + it.e * 3 * p.steps + 3 * it.step + it.ph;
+                if (finish) pending = p.done + it.e * 3 * p.steps + 3 * it.step + it.ph;
             }
         }
         if (lane == 0) {
@@ -653,20 +712,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct Layout {
-    int m, n, ldm, ldn;
-    size_t part, done, xh[2], xl[2], a, r, total;
+    int m, n, ldm, ldn, tn, T, sym, full, parts;
+    size_t norm, done, arrived, xh[2], xl[2], a, r, part, total;
 };
+
+constexpr int PAIRS = 76;  // CTA pairs that the tiling reckons with
 
 void layout(int E, int N, int K, Layout* l) {
     l->m = N < K ? N : K;
     l->n = N < K ? K : N;
     l->ldm = (l->m + 63) & ~63;
     l->ldn = (l->n + 63) & ~63;
+    // Tiles of 128 columns where those of 256 would leave pairs without one: each
+    // then takes half the time to compute and store.
+    l->T = (l->m + TILE - 1) / TILE;
+    l->tn = static_cast<long long>(E) * l->T * ((l->n + TILE - 1) / TILE) <= PAIRS ? TILE / 2 : TILE;
+    const int Tm = (l->m + l->tn - 1) / l->tn, ksteps = (l->n + KSTEP - 1) / KSTEP;
+    l->full = l->T * ((l->n + l->tn - 1) / l->tn);
+    l->sym = 0;
+    for (int i = 0; i < l->T; ++i) l->sym += Tm < (i + 1) * (TILE / l->tn) ? Tm : (i + 1) * (TILE / l->tn);
+    // The contraction of X X^T in pieces of sixteen K-steps or more where its tiles
+    // occupy less than half of the pairs.
+    const long long tiles = static_cast<long long>(E) * l->sym;
+    l->parts = 1;
+    if (2 * tiles <= PAIRS) {
+        l->parts = static_cast<int>(PAIRS / tiles);
+        if (l->parts > ksteps / 16) l->parts = ksteps / 16;
+        if (l->parts > 8) l->parts = 8;
+        if (l->parts < 1) l->parts = 1;
+    }
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
     const size_t e = E;
-    l->part = take(4 * e * NORM_BLOCKS);
-    l->done = take(4 * e * 3 * MXFP8_MUON_MAX_STEPS);
+    l->norm = take(4 * e * NORM_BLOCKS);
+    l->done = take(4 * e * 3 * MXFP8_MUON_MAX_STEPS);  // (done and arrived: zeroed together)
+    l->arrived = take(4 * e * l->sym * 2 * EPI_WARPS);
+    l->part = take(l->parts > 1 ? 4 * e * l->sym * l->parts * TILE * l->tn : 0);
     for (int i = 0; i < 2; ++i) l->xh[i] = take(2 * e * l->m * l->ldn);
     for (int i = 0; i < 2; ++i) l->xl[i] = take(2 * e * l->m * l->ldn);
     l->a = take(2 * e * l->m * l->ldm);
@@ -695,16 +776,10 @@ int launch_muon(const MuonArgs& a) {
     layout(a.E, a.N, a.K, &l);
     Params p{};
     p.E = a.E; p.m = l.m; p.n = l.n; p.ldm = l.ldm; p.ldn = l.ldn; p.steps = a.steps; p.tall = a.N > a.K;
-    // Tiles of 128 columns where those of 256 would leave pairs without one: each
-    // then takes half the time to compute and store.
-    const int T = (l.m + TILE - 1) / TILE, wide = T * ((l.n + TILE - 1) / TILE);
-    p.tn = static_cast<long long>(a.E) * wide <= a.num_sms / 2 ? TILE / 2 : TILE;
-    const int Tm = (l.m + p.tn - 1) / p.tn;
-    p.T = T;
-    p.full = T * ((l.n + p.tn - 1) / p.tn);
-    p.sym = 0;
-    for (int i = 0; i < T; ++i) p.sym += Tm < (i + 1) * (TILE / p.tn) ? Tm : (i + 1) * (TILE / p.tn);
-    if (static_cast<long long>(a.steps) * a.E * (2LL * p.sym + p.full) > 0x7fffffffLL / 2)
+    p.tn = l.tn; p.T = l.T; p.full = l.full; p.sym = l.sym; p.parts = l.parts;
+    p.part = reinterpret_cast<float*>(a.ws + l.part);
+    p.arrived = reinterpret_cast<unsigned int*>(a.ws + l.arrived);
+    if (static_cast<long long>(a.steps) * a.E * (9LL * p.sym + p.full) > 0x7fffffffLL / 2)
         return host_fail(MXFP8_EINVAL, "E=%d N=%d K=%d steps=%d: too many tiles", a.E, a.N, a.K, a.steps);
     p.a = a.a; p.b = a.b; p.c = a.c;
     p.Xh = reinterpret_cast<__half*>(a.ws + l.xh[0]);
@@ -712,7 +787,8 @@ int launch_muon(const MuonArgs& a) {
     p.done = reinterpret_cast<unsigned int*>(a.ws + l.done);
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
-    float* part = reinterpret_cast<float*>(a.ws + l.part);
+    float* norm = reinterpret_cast<float*>(a.ws + l.norm);
+    const int zeroed = static_cast<int>((l.arrived - l.done) / 4 + static_cast<size_t>(a.E) * l.sym * 2 * EPI_WARPS);
     Maps maps;
     int rc = MXFP8_OK;
     const int E = a.E;
@@ -758,13 +834,13 @@ int launch_muon(const MuonArgs& a) {
     pre.stream = a.stream;
     pre.blockDim = dim3(256);
     pre.gridDim = dim3(NORM_BLOCKS, a.E);
-    e = cudaLaunchKernelEx(&pre, muon_momentum, a, part, p.done, a.E * 3 * a.steps);
+    e = cudaLaunchKernelEx(&pre, muon_momentum, a, norm, p.done, zeroed);
     if (e == cudaSuccess) {
         pre.gridDim = dim3((a.K + 63) / 64, (a.N + 63) / 64, a.E);
-        e = cudaLaunchKernelEx(&pre, muon_scale, a, p, static_cast<const float*>(part));
+        e = cudaLaunchKernelEx(&pre, muon_scale, a, p, static_cast<const float*>(norm));
     }
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
-    const int items = a.E * (p.full > p.sym ? p.full : p.sym);
+    const int items = a.E * (p.full > p.sym * p.parts ? p.full : p.sym * p.parts);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (items < pairs ? items : pairs));
     cfg.blockDim = dim3(THREADS);
