@@ -526,7 +526,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (p.user_ids) p.user_ids[t * p.top_k + lane] = ids[lane];
                         if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
                     }
-                    __threadfence();
                     __syncwarp();
                     if (lane == 0) red_release_gpu_add(p.counters + C_CHOSEN, 1);
                 }
@@ -938,20 +937,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(bar_tempty + 8 * buf);
             if (g.phase) {
                 named_bar_sync(EPI_BAR, 128);
-                if (q == 0 && lane == 0) {
-                    __threadfence();
-                    red_release_gpu_add(p.counters + C_DONE, 1);
-                }
+                if (q == 0 && lane == 0) red_release_gpu_add(p.counters + C_DONE, 1);
             } else {
                 bool finish = whole;
                 if (!whole) {
                     // the part that ends last sums all of them, in order
                     named_bar_sync(EPI_BAR, 128);
-                    if (q == 0 && lane == 0) {
-                        __threadfence();
+                    if (q == 0 && lane == 0)
                         flags[8] = atom_acq_rel_gpu_add(p.counters + C_H + p.local + g.tile, 1) == static_cast<uint32_t>(g.parts - 1) ? 1 : 0;
-                        __threadfence();
-                    }
                     named_bar_sync(EPI_BAR, 128);
                     finish = flags[8] != 0;
                     for (int o = q; finish && o < 2 * nt; o += 4) {
@@ -968,10 +961,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if (finish) {
                     named_bar_sync(EPI_BAR, 128);
-                    if (q == 0 && lane == 0) {
-                        __threadfence();
-                        red_release_gpu_add(p.counters + C_H + g.a, 1);
-                    }
+                    if (q == 0 && lane == 0) red_release_gpu_add(p.counters + C_H + g.a, 1);
                 }
             }
         }

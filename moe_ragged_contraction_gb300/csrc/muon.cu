@@ -492,7 +492,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         unsigned int* pending = nullptr;  // lane 0: the finished tile that is not reported yet
         auto report = [&]() {
             asm volatile("fence.proxy.async;" ::: "memory");
-            __threadfence();
             red_release_gpu_add(pending, 1);
             pending = nullptr;
         };
@@ -558,10 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         bulk_wait_group_all();
                         report();
                     }
-                    __threadfence();
                     finish = atom_acq_rel_gpu_add(p.arrived + share, 1) == static_cast<uint32_t>(p.parts - 1);
                     if (finish) p.arrived[share] = 0;  // (the next step's pieces come long after)
-                    __threadfence();
                 }
                 finish = __shfl_sync(0xffffffffu, finish ? 1 : 0, 0) != 0;
             }
