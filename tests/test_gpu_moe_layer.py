@@ -231,6 +231,32 @@ def test_two_streams_at_once():
     assert mx.device_status(clear=True) == 0
 
 
+def test_few_long_tiles_are_cut_into_parts():
+    """One chosen expert with few, long tiles: parts along both contractions, summed in order."""
+    for T, H, I in ((1, 2048, 64), (3, 96, 2048), (2, 1312, 800)):
+        ops = make(T, H, I, 6, 2, seed=H + I)
+        args = device_args(*ops)
+        bias = torch.tensor([0, 0, 9.0, 0, 0, 0], device="cuda")
+        out, ids, weights = run(args, 2, bias=bias, first_expert=2)
+        check(*ops, 2, out, ids, weights, first=2, bias=bias.cpu().numpy())
+        again, _, _ = run(args, 2, bias=bias, first_expert=2)
+        assert torch.equal(out, again)
+
+
+def test_example_runs():
+    """The example's path: gradients, update, quantised weights, layer; an expert without tokens stays as it was."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_step.py")
+    spec = importlib.util.spec_from_file_location("expert_step", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    before, after, moms, update = m.main(E=4, H=256, I=128, tokens_per_expert=64, steps=2)
+    assert torch.isfinite(after).all() and not torch.equal(before, after)
+    assert not update[2].any() and not moms[1][2].any() and update[1].any()
+
+
 def test_no_tokens():
     ops = make(1, 64, 32, 4, 4, seed=14)
     args = list(device_args(*ops))

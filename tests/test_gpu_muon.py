@@ -154,6 +154,32 @@ def test_one_matrix_and_out():
     assert b is out and torch.equal(a[0], b)
 
 
+@pytest.mark.parametrize("E,N,K", [
+    (1, 130, 2600), (2, 260, 2104), (1, 2111, 136),   # few long tiles: the contraction of X X^T in pieces
+    (3, 100, 2056), (1, 4097, 96),                    # too long for one cluster by a little, and tall
+    (2, 128, 2048), (1, 2048, 8), (7, 77, 520),       # one cluster a matrix: its largest size, its thinnest, three CTAs
+    (90, 40, 264),                                    # more clusters than fit at once
+])
+def test_long_matrices(E, N, K):
+    g = bf16_round(gradient(E, N, K, seed=N + K, kind="strong"))
+    out = mx.muon_update(cuda(g, torch.bfloat16))
+    close(out, muon(g)[0])
+    assert torch.equal(out, mx.muon_update(cuda(g, torch.bfloat16)))
+    assert mx.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("N,K", [(40, 96), (96, 40), (300, 200), (200, 304)])
+def test_one_step_against_differences(N, K):
+    """One step is odd in u and its derivative at u in direction d is what the formula's differences give."""
+    g, d = gradient(1, N, K, seed=20, kind="strong"), gradient(1, N, K, seed=21)
+    run = lambda x: mx.muon_update(cuda(x.astype(np.float32)), steps=1).float().cpu().numpy().astype(np.float64)  # noqa: E731
+    assert np.array_equal(run(-g), -run(g))
+    t = 0.25
+    got, want = run(g + t * d) - run(g - t * d), muon(g + t * d, steps=1)[0] - muon(g - t * d, steps=1)[0]
+    # each side is off by at most REL of its norm, the outputs' norms are alike
+    assert np.linalg.norm(got - want) <= 2 * REL * np.linalg.norm(muon(g, steps=1)[0])
+
+
 def test_large_sampled():
     """One full-size tall matrix against the iteration in 64 bits on the GPU."""
     gen = torch.Generator(device="cuda")
