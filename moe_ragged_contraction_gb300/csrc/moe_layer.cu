@@ -245,18 +245,18 @@ __device__ __forceinline__ uint32_t sort_key(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// The CTA: logits of token t (sums of the slices, in order) into shared memory.
-__device__ __forceinline__ void gather_logits(const Params& p, int t, float* score) {
+// The CTA: logits of n tokens from t on (sums of the slices, in order) into shared memory.
+__device__ __forceinline__ void gather_logits(const Params& p, int t, int n, float* score) {
     const float* src = p.logits + static_cast<size_t>(t) * p.experts;
     const size_t slice = static_cast<size_t>(p.T) * p.experts;
-#pragma unroll 1
-    for (int e = threadIdx.x; e < p.experts; e += THREADS) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n * p.experts; i += THREADS) {
         float v[8], s = 0.f;  // (at most 8 slices: all loads in flight together)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = k < p.ksplit ? __ldcg(src + k * slice + e) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = k < p.ksplit ? __ldcg(src + k * slice + i) : 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += v[k];
-        score[e] = s;
+        score[i] = s;
     }
 }
 
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float* scores = reinterpret_cast<float*>(smem + p.off_ring);  // [tokens in hand][experts], then as many keys
         bool ok = true;
         if (p.T <= 8) {
-            for (int t = 0; t < p.T; ++t) gather_logits(p, t, scores + t * p.experts);
+            gather_logits(p, 0, p.T, scores);
             __syncthreads();
             if (warp < p.T) {
                 int32_t* ids = reinterpret_cast<int32_t*>(smem + p.off_epi) + warp * MXFP8_MOE_MAX_TOPK;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncthreads();
                 const int t = flags[7];
                 if (t >= p.T) break;
-                gather_logits(p, t, scores);
+                gather_logits(p, t, 1, scores);
                 __syncthreads();
                 if (warp == 0) {
                     int32_t* ids = p.ids + t * p.top_k;
