@@ -227,14 +227,14 @@ __device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int targ
                                         int* status) {
     const uint64_t t0 = global_timer_ns();
     for (;;) {
-        if (ld_acquire_gpu(p) >= target) return true;
+        // (polled relaxed: an acquire each time makes every poll slower)
+        if (ld_relaxed_gpu(p) >= target && ld_acquire_gpu(p) >= target) return true;
         if (*abort_flag) return false;
         if (global_timer_ns() - t0 > ns) {
             *abort_flag = 1;
             atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
             return false;
         }
-        __nanosleep(20);
     }
 }
 
@@ -491,7 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         bool ok = true;
         unsigned int* pending = nullptr;  // lane 0: the finished tile that is not reported yet
         auto report = [&]() {
-            asm volatile("fence.proxy.async;" ::: "memory");
+            // (the stores went through the asynchronous proxy and have completed: the
+            // reader's proxy fence, in the scout, is the one that is needed)
             red_release_gpu_add(pending, 1);
             pending = nullptr;
         };
