@@ -431,6 +431,12 @@ int mxw::host_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
 
 uint64_t mxw::host_wait_limit_ns() { return wait_limit_ns(); }
 
+int mxw::host_take_stall() {
+    const int s = g_stall_next;
+    g_stall_next = 0;
+    return s;
+}
+
 int mxw::host_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
                          const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
@@ -648,8 +654,8 @@ int mxfp8_device_status(int32_t* status, int clear) {
     return MXFP8_OK;
 }
 
-// Failure-path test hook (not part of the public header): the next wgrad
-// call on this thread declares 16 more bytes than its first pipeline stage
+// Failure-path test hook (not part of the public header): the next wgrad,
+// expert layer or (general) update call on this thread declares 16 more bytes than its first pipeline stage
 // receives, so that stage's wait can never complete and runs out after the
 // configured limit (MXFP8_WAIT_LIMIT_MS). The kernel then stops its pipeline,
 // sets MXFP8_DEV_WAIT_TIMEOUT and returns; nothing faults or hangs.

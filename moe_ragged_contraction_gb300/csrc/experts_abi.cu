@@ -60,6 +60,7 @@ int moe(const uint16_t* x, int T, const uint16_t* router, const float* bias, con
     a.out = out; a.ids = ids; a.weights = weights;
     a.ws = static_cast<uint8_t*>(ws);
     a.wait_limit_ns = mxw::host_wait_limit_ns();
+    a.stall = mxw::host_take_stall();
     const cudaError_t e = mxw::device_status_address(a.dev, &a.status);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "device status: %s", cudaGetErrorString(e));
     return mxw::launch_moe(a);
@@ -108,6 +109,7 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     a.out = out;
     a.ws = static_cast<uint8_t*>(ws);
     a.wait_limit_ns = mxw::host_wait_limit_ns();
+    a.stall = mxw::host_take_stall();
     const cudaError_t e = mxw::device_status_address(a.dev, &a.status);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "device status: %s", cudaGetErrorString(e));
     return mxw::muon_fits_small(N, K) ? mxw::launch_muon_small(a) : mxw::launch_muon(a);

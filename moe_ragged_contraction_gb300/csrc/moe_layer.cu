@@ -85,6 +85,7 @@ struct Params {
     uint32_t off_lists, off_epi, off_rows, off_ring, smem;
     unsigned long long wait_ns;
     int* status;
+    int stall;               // test hook: over-declare the first stage's bytes so that its wait runs out
 };
 
 __device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
                     if (!ok) break;
                     const uint32_t dst = ring + st * ab_stage, bar = bar_w + 8 * st;
-                    mbar_arrive_expect_tx(bar, A_BYTES);
+                    mbar_arrive_expect_tx(bar, A_BYTES + (p.stall && c == 0 ? 16 : 0));
                     if (g.phase) tma_load_3d(dst, &tm2, bar, k * STEP, g.rt * TILE, e, once);
                     else tma_load_4d(dst, &tm13, bar, k * STEP, g.rt * (TILE / 2), 0, e, once);
                     ++c;
@@ -1102,6 +1103,7 @@ int launch_moe(const MoeArgs& a) {
     p.smem = l.mf == 1 ? SMEM_FEW : SMEM_MAX;
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
+    p.stall = a.stall;
 
     CUtensorMap m13, m2;
     // w13 as [local][2][I][H]: one box holds 64 gate rows and the same 64 up rows

@@ -71,6 +71,7 @@ struct Params {
     unsigned int* done;  // [E][3 steps] epilogue warps' shares of tiles stored
     unsigned long long wait_ns;
     int* status;
+    int stall;           // test hook: over-declare the first stage's bytes so that its wait runs out
 };
 
 struct Maps {
@@ -394,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     ok = wait_bar(bar_empty + 8 * st, ph, abort_flag, p.wait_ns, p.status);
                     if (!ok) break;
                     const uint32_t da = sbase + st * 2 * OP_BYTES, db = da + OP_BYTES, fb = full_leader + 8 * st;
-                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 2 * (HALF + p.tn / 2) * KSTEP * 2);
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * st, 2 * (HALF + p.tn / 2) * KSTEP * 2 + (p.stall && c == 0 ? 16 : 0));
                     const int kc = (it.k0 + k) * KSTEP;
                     tma_load_3d_pair(da, ma, fb, kc, ra, it.e);
                     if (it.ph == 2) {
@@ -785,6 +786,7 @@ int launch_muon(const MuonArgs& a) {
     p.done = reinterpret_cast<unsigned int*>(a.ws + l.done);
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
+    p.stall = a.stall;
     float* norm = reinterpret_cast<float*>(a.ws + l.norm);
     const int zeroed = static_cast<int>((l.arrived - l.done) / 4 + static_cast<size_t>(a.E) * l.sym * 2 * EPI_WARPS);
     Maps maps;

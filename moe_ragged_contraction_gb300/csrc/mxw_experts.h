@@ -18,7 +18,7 @@ struct MoeArgs {
     int32_t* ids;
     float* weights;
     uint8_t* ws;
-    int dev, num_sms;
+    int dev, num_sms, stall;
     uint64_t wait_limit_ns;
     int* status;
     cudaStream_t stream;
@@ -36,7 +36,7 @@ struct MuonArgs {
     float mu, a, b, c, eps;
     uint16_t* out;
     uint8_t* ws;
-    int dev, num_sms;
+    int dev, num_sms, stall;
     uint64_t wait_limit_ns;
     int* status;
     cudaStream_t stream;

@@ -156,6 +156,7 @@ int host_fail(int code, const char* fmt, ...);
 int host_device(int* dev, int* sms);
 int host_workspace(int dev, cudaStream_t stream, size_t need, void** out);
 uint64_t host_wait_limit_ns();
+int host_take_stall();  // the failure-path test hook, taken by this call
 int host_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
