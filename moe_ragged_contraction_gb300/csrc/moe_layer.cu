@@ -58,7 +58,8 @@ constexpr uint32_t TMEM_ALL = 512;
 // counters: tokens claimed and chosen for, units claimed, down units done
 constexpr int C_CLAIM = 0, C_CHOSEN = 1, C_QUEUE = 2, C_DONE = 3, C_H = 4;
 constexpr int NQ = 4;                // queue entries in flight in a CTA
-constexpr int EPI_BAR = 1;           // named barrier of the epilogue warps
+constexpr int EPI_BAR = 1;           // named barriers: the epilogue warps; the lists are made; the pairs are placed
+constexpr int LIST_BAR = 2, PLACE_BAR = 3;
 // kind::mxf8f6f4, E4M3 x E4M3, both K-major, E8M0 scales, M = 128
 constexpr uint32_t IDESC = (1u << 23) | (static_cast<uint32_t>(TILE >> 4) << 24);
 
@@ -82,7 +83,7 @@ struct Params {
     float *part_up, *part_down;  // [unit][T][128]
     int Hp, Ip, sh_stride, ksplit, slots, n_counters;
     int up_tiles, down_tiles, up_steps, down_steps;
-    uint32_t off_lists, off_epi, off_rows, off_ring, smem;
+    uint32_t off_lists, off_mask, off_epi, off_rows, off_ring, smem;
     unsigned long long wait_ns;
     int* status;
     int stall;               // test hook: over-declare the first stage's bytes so that its wait runs out
@@ -261,9 +262,15 @@ __device__ __forceinline__ void gather_logits(const Params& p, int t, int n, flo
     }
 }
 
+struct Choice {
+    int id;        // lane k < top_k: the k-th chosen expert and its weight
+    float weight;
+};
+
 // One warp: the choice for one token from its logits (score: [experts], shared; key: [experts], shared scratch).
-// Lane l holds experts l, l + 32, ...
-__device__ __noinline__ void choose(const Params& p, float* score, uint32_t* key, int32_t* ids, float* wts) {
+// Lane l holds experts l, l + 32, ... (Loops, not registers: unrolled for eight experts a lane this took
+// 13 us longer, all of it misses of the instruction cache.)
+__device__ __noinline__ Choice choose(const Params& p, float* score, uint32_t* key) {
     const int lane = threadIdx.x & 31;
     const unsigned full = 0xffffffffu;
     float m = -CUDART_INF_F;
@@ -303,11 +310,8 @@ __device__ __noinline__ void choose(const Params& p, float* score, uint32_t* key
             scan();
         }
     }
-    if (lane < p.top_k) {
-        ids[lane] = my_id;
-        wts[lane] = (p.renormalize ? mine / total : mine) * p.scale;
-    }
     __syncwarp();
+    return Choice{my_id, (p.renormalize ? mine / total : mine) * p.scale};
 }
 
 // ============================================================== experts
@@ -473,6 +477,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tma_prefetch_desc(&tm13);
         tma_prefetch_desc(&tm2);
     }
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + p.off_mask);  // [local][4] tokens of a local expert
+    for (int i = threadIdx.x; i < 4 * p.local; i += THREADS) mask[i] = 0;
     if (warp == 1) {
         tmem_alloc_single(smem_u32(flags + 1), TMEM_ALL);
         tmem_relinquish_single();
@@ -492,25 +498,31 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) first_unit = atomicAdd(p.counters + C_QUEUE, 1u);
     if (warp == 0) first_unit = __shfl_sync(0xffffffffu, first_unit, 0);
     {
+        // entry (token, k) of the routing: its expert if it lives here, its weight,
+        // and the token's bit in the expert's mask. Bit counts are then the experts'
+        // sizes and the pairs' ranks, whatever the order in which the bits were set.
+        auto enter = [&](int t, int k, int e, float w) {
+            const int i = t * p.top_k + k;
+            const bool here = e >= p.first && e < p.first + p.local;
+            L.eid[i] = here ? static_cast<uint16_t>(e - p.first) : 0xffff;
+            L.wts[i] = w;
+            if (here) atomicOr(mask + 4 * (e - p.first) + (t >> 5), 1u << (t & 31));
+        };
         float* scores = reinterpret_cast<float*>(smem + p.off_ring);  // [tokens in hand][experts], then as many keys
-        bool ok = true;
+        auto tell_user = [&](int t, const Choice& c) {
+            if (p.user_ids) p.user_ids[t * p.top_k + lane] = c.id;
+            if (p.user_weights) p.user_weights[t * p.top_k + lane] = c.weight;
+        };
         if (p.T <= 8) {
             gather_logits(p, 0, p.T, scores);
             __syncthreads();
             if (warp < p.T) {
-                int32_t* ids = reinterpret_cast<int32_t*>(smem + p.off_epi) + warp * MXFP8_MOE_MAX_TOPK;
-                choose(p, scores + warp * p.experts, reinterpret_cast<uint32_t*>(scores) + (p.T + warp) * p.experts, ids,
-                       L.wts + warp * p.top_k);
+                const Choice c = choose(p, scores + warp * p.experts, reinterpret_cast<uint32_t*>(scores) + (p.T + warp) * p.experts);
                 if (lane < p.top_k) {
-                    const int e = ids[lane];
-                    L.eid[warp * p.top_k + lane] = e >= p.first && e < p.first + p.local ? static_cast<uint16_t>(e - p.first) : 0xffff;
-                    if (cta == 0) {
-                        if (p.user_ids) p.user_ids[warp * p.top_k + lane] = e;
-                        if (p.user_weights) p.user_weights[warp * p.top_k + lane] = L.wts[warp * p.top_k + lane];
-                    }
+                    enter(warp, lane, c.id, c.weight);
+                    if (cta == 0) tell_user(warp, c);
                 }
             }
-            __syncthreads();
         } else {
             for (;;) {
                 if (threadIdx.x == 0) flags[7] = static_cast<int>(atomicAdd(p.counters + C_CLAIM, 1u));
@@ -520,12 +532,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 gather_logits(p, t, 1, scores);
                 __syncthreads();
                 if (warp == 0) {
-                    int32_t* ids = p.ids + t * p.top_k;
-                    float* wts = p.weights + t * p.top_k;
-                    choose(p, scores, reinterpret_cast<uint32_t*>(scores) + p.experts, ids, wts);
+                    const Choice c = choose(p, scores, reinterpret_cast<uint32_t*>(scores) + p.experts);
                     if (lane < p.top_k) {
-                        if (p.user_ids) p.user_ids[t * p.top_k + lane] = ids[lane];
-                        if (p.user_weights) p.user_weights[t * p.top_k + lane] = wts[lane];
+                        p.ids[t * p.top_k + lane] = c.id;
+                        p.weights[t * p.top_k + lane] = c.weight;
+                        tell_user(t, c);
                     }
                     __syncwarp();
                     if (lane == 0) red_release_gpu_add(p.counters + C_CHOSEN, 1);
@@ -533,27 +544,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (threadIdx.x == 0) flags[6] = wait_count(p.counters + C_CHOSEN, p.T, abort_flag, p.wait_ns, p.status) ? 1 : 0;
             __syncthreads();
-            ok = flags[6] != 0;
-            if (ok)
+            if (flags[6])
                 for (int i = threadIdx.x; i < p.slots; i += THREADS) {
-                    const int e = __ldcg(p.ids + i);
-                    L.eid[i] = e >= p.first && e < p.first + p.local ? static_cast<uint16_t>(e - p.first) : 0xffff;
-                    L.wts[i] = __ldcg(p.weights + i);
+                    const int t = i / p.top_k;
+                    enter(t, i - t * p.top_k, __ldcg(p.ids + i), __ldcg(p.weights + i));
                 }
-            __syncthreads();
         }
-        // ---- the (token, expert) pairs sorted by expert, in token order: a token
-        // mask per expert, whose bit counts are the experts' sizes and the pairs'
-        // ranks whatever the order in which the bits were set
-        uint32_t* mask = reinterpret_cast<uint32_t*>(smem + p.off_ring);  // [local][4]
-        for (int i = threadIdx.x; i < 4 * p.local; i += THREADS) mask[i] = 0;
+        fence_proxy_async_shared();  // the ring's space held the scores
         __syncthreads();
-        for (int i = threadIdx.x; ok && i < p.slots; i += THREADS)
-            if (L.eid[i] != 0xffff) {
-                const int t = i / p.top_k;
-                atomicOr(mask + 4 * L.eid[i] + (t >> 5), 1u << (t & 31));
-            }
-        __syncthreads();
+        // ---- the (token, expert) pairs sorted by expert, in token order. Warp 0
+        // lists the chosen experts and goes on to load their weights; the others
+        // place the pairs.
         if (warp == 0) {
             int chosen = 0, first = 0, most = 0;
             for (int b = 0; b < p.local; b += 32) {
@@ -585,19 +586,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 L.info[0] = chosen;
                 L.info[1] = most;
             }
+            __syncwarp();
+            named_bar_arrive(LIST_BAR, THREADS);
+        } else {
+            named_bar_sync(LIST_BAR, THREADS);
+            for (int i = threadIdx.x - 32; i < p.slots; i += THREADS - 32)
+                if (p.T <= 8 || flags[6]) {
+                    const int e = L.eid[i];
+                    if (e == 0xffff) continue;
+                    const int t = i / p.top_k;
+                    const uint32_t* m = mask + 4 * e;
+                    int s = L.off[L.act_of[e]] + __popc(m[t >> 5] & ((1u << (t & 31)) - 1));
+                    for (int w = 0; w < (t >> 5); ++w) s += __popc(m[w]);
+                    L.slot_of[i] = static_cast<uint16_t>(s);
+                    L.entry_of[s] = static_cast<uint16_t>(i);
+                }
+            named_bar_sync(PLACE_BAR, THREADS - 32);
         }
-        __syncthreads();
-        for (int i = threadIdx.x; ok && i < p.slots; i += THREADS)
-            if (L.eid[i] != 0xffff) {
-                const int t = i / p.top_k;
-                const uint32_t* m = mask + 4 * L.eid[i];
-                int s = L.off[L.act_of[L.eid[i]]] + __popc(m[t >> 5] & ((1u << (t & 31)) - 1));
-                for (int w = 0; w < (t >> 5); ++w) s += __popc(m[w]);
-                L.slot_of[i] = static_cast<uint16_t>(s);
-                L.entry_of[s] = static_cast<uint16_t>(i);
-            }
-        fence_proxy_async_shared();  // the ring's space held the scores
-        __syncthreads();
     }
     const int nact = L.info[0];
     // MMA width for the expert with the most tokens; ring of K-step stages
@@ -1097,7 +1102,8 @@ int launch_moe(const MoeArgs& a) {
     p.Hp = l.Hp; p.Ip = l.Ip; p.sh_stride = l.sh_stride; p.ksplit = l.ksplit; p.slots = l.slots; p.n_counters = l.n_counters;
     p.up_tiles = l.up_tiles; p.down_tiles = l.down_tiles; p.up_steps = l.up_steps; p.down_steps = l.down_steps;
     p.off_lists = 512;
-    p.off_epi = (p.off_lists + l.slots * 10 + a.local * 8 + 127) & ~127u;
+    p.off_mask = (p.off_lists + l.slots * 10 + a.local * 8 + 127) & ~127u;
+    p.off_epi = (p.off_mask + a.local * 16 + 127) & ~127u;
     p.off_rows = p.off_epi + 2 * 8 * TILE * 4;
     p.off_ring = (p.off_rows + LOADERS * 1024 + 1023) & ~1023u;
     p.smem = l.mf == 1 ? SMEM_FEW : SMEM_MAX;
