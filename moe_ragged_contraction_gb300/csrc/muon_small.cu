@@ -18,8 +18,6 @@
 // the two transposes of tall matrices happen on the way in and out. The same
 // scaling and shift beta as in the general kernel.
 //
-// Measured on GB300: 4 matrices of 128 x 256, whole call: see the table of the
-// operators' cases.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,7 +34,7 @@ namespace {
 constexpr int M = 128;               // rows of a CTA's operands
 constexpr int MAXW = 256;            // columns of a CTA's slice
 constexpr int MAXC = 8;              // CTAs of a cluster
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;         // 16 warps: a TMEM quarter (32 rows) and a quarter of the columns each
 constexpr int ATOM = M * 128;        // 128 rows of 64 fp16 values, 128-byte swizzle
 constexpr float SX = 2048.f, SA = 4096.f;  // as in muon.cu
 // shared memory: X's slice; then either u on the way in (fp32, rows padded by
@@ -44,6 +42,7 @@ constexpr float SX = 2048.f, SA = 4096.f;  // as in muon.cu
 constexpr int OFF_A = MAXW / 64 * ATOM, OFF_R = OFF_A + 2 * ATOM, OFF_P = OFF_R + 2 * ATOM;
 constexpr int OFF_BAR = OFF_A + M * (MAXW + 1) * 4 > OFF_P + M * M * 4 ? OFF_A + M * (MAXW + 1) * 4 : OFF_P + M * M * 4;
 constexpr int SMEM = OFF_BAR + 256 + 1024;
+constexpr int CH = 16;               // columns that a thread handles at a time (short code: its first pass misses the instruction cache)
 static_assert(SMEM <= 232448, "shared memory of a CTA");
 constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(M >> 4) << 24);  // kind::f16, fp16 x fp16 -> fp32, M = 128
 constexpr uint32_t X_COL = 256;      // TMEM: accumulator in columns 0 .. 255, X in fp32 from here on
@@ -63,16 +62,27 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr) {
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+// 32 lanes x 16 consecutive 32-bit columns: thread i of the warp holds lane (base lane + i).
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&v)[CH]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-          "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-          "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[CH]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void fence16(uint32_t (&v)[CH]) {  // ties loaded registers to a point after the wait
+#pragma unroll
+    for (int i = 0; i < CH; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -97,22 +107,16 @@ struct Small {
     int m, n, w, C, tall;
 };
 
-// Four values of u from element i of the gradient (a multiple of 4); updates the momentum.
-__device__ __forceinline__ float4 take_u(const MuonArgs& a, size_t i) {
-    float4 g;
-    if (a.grad_f32) {
-        g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i));
-    } else {
-        const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i));
-        g = make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
-                        __uint_as_float(r.y & 0xFFFF0000u));
-    }
-    if (!a.momentum) return g;
-    float4 m = *reinterpret_cast<const float4*>(a.momentum + i);
-    m = make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
-    *reinterpret_cast<float4*>(a.momentum + i) = m;
-    if (!a.nesterov) return m;
-    return make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
+// Four values of the gradient from element i on (a multiple of 4).
+__device__ __forceinline__ float4 load_grad(const MuonArgs& a, size_t i) {
+    if (a.grad_f32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i));
+    const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i));
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ float4 axpy4(float s, const float4& x, const float4& y) {
+    return make_float4(fmaf(s, x.x, y.x), fmaf(s, x.y, y.y), fmaf(s, x.z, y.z), fmaf(s, x.w, y.w));
 }
 
 __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
@@ -123,8 +127,8 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
     const int rank = p.C > 1 ? static_cast<int>(cluster_ctarank()) : 0, e = blockIdx.x / p.C;
     const uint32_t bar = sbase + OFF_BAR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8);
-    float* red = reinterpret_cast<float*>(smem + OFF_BAR + 32);   // [8] warps' sums of squares
-    float* norms = red + 8;                                        // [8] CTAs' sums
+    float* red = reinterpret_cast<float*>(smem + OFF_BAR + 32);   // [16] warps' sums of squares
+    float* norms = red + 16;                                       // [8] CTAs' sums
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(bar, 1);
@@ -135,8 +139,8 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
         tmem_relinquish_single();
     }
     griddep_wait();  // the gradient may come from the kernel before
-    const int q4 = warp & 3, h = warp >> 2;         // TMEM quarter, half of the columns
-    const int row = q4 * 32 + lane, width = p.w / 2;  // this thread's row; columns h * width ..
+    const int q4 = warp & 3, h = warp >> 2;         // TMEM quarter, quarter of the columns
+    const int row = q4 * 32 + lane, width = p.w / 4;  // this thread's row; columns h * width ..
 
     // ---- u into shared memory as X's rows, the sum of its squares
     float* u = reinterpret_cast<float*>(smem + OFF_A);
@@ -148,19 +152,38 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
     }
     float sq = 0.f;
     {
-        // four neighbours along the gradient's rows: X's columns, or (tall) X's rows
+        // four neighbours along the gradient's rows: X's columns, or (tall) X's rows;
+        // a warp per line, four lines' loads in flight (the momentum's stores
+        // would otherwise hold back the loads behind them)
+        constexpr int BATCH = 4, WARPS = THREADS / 32;
         const int groups = (p.tall ? p.m : p.n) / 4, lines = p.tall ? cols : p.m;
         const int g0 = p.tall ? 0 : col0 / 4, ng = p.tall ? groups : min(p.w / 4, groups - g0);
-#pragma unroll 4
-        for (int i = threadIdx.x; i < lines * ng; i += THREADS) {
-            const int l = i / ng, g = i - l * ng;
-            const size_t at = p.tall ? static_cast<size_t>(col0 + l) * p.m + 4 * g : static_cast<size_t>(l) * p.n + 4 * (g0 + g);
-            const float4 v = take_u(p.a, base + at);
-            sq += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
-            float* d = p.tall ? u + 4 * g * pitch + l : u + l * pitch + 4 * g;
-            const int s = p.tall ? pitch : 1;
-            d[0] = v.x; d[s] = v.y; d[2 * s] = v.z; d[3 * s] = v.w;
-        }
+        const size_t first = base + (p.tall ? static_cast<size_t>(col0) * p.m : 4 * static_cast<size_t>(g0)), line = p.tall ? p.m : p.n;
+        for (int l0 = warp; l0 < lines; l0 += WARPS * BATCH)
+            for (int g = lane; g < ng; g += 32) {
+                float4 v[BATCH], mo[BATCH];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const int l = l0 + WARPS * j;
+                    const size_t at = first + l * line + 4 * g;
+                    v[j] = l < lines ? load_grad(p.a, at) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p.a.momentum && l < lines) mo[j] = *reinterpret_cast<const float4*>(p.a.momentum + at);
+                }
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const int l = l0 + WARPS * j;
+                    if (l >= lines) continue;
+                    if (p.a.momentum) {
+                        mo[j] = axpy4(p.a.mu, mo[j], v[j]);
+                        *reinterpret_cast<float4*>(p.a.momentum + first + l * line + 4 * g) = mo[j];
+                        v[j] = p.a.nesterov ? axpy4(p.a.mu, mo[j], v[j]) : mo[j];
+                    }
+                    sq += (v[j].x * v[j].x + v[j].y * v[j].y) + (v[j].z * v[j].z + v[j].w * v[j].w);
+                    float* d = p.tall ? u + 4 * g * pitch + l : u + l * pitch + 4 * g;
+                    const int st = p.tall ? pitch : 1;
+                    d[0] = v[j].x; d[st] = v[j].y; d[2 * st] = v[j].z; d[3 * st] = v[j].w;
+                }
+            }
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
@@ -172,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
     if (p.C > 1) cluster_sync_all();  // the other CTAs run: their shared memory may be written
     if (threadIdx.x < p.C) {
         float s = 0.f;
-        for (int w = 0; w < 8; ++w) s += red[w];
+        for (int w = 0; w < THREADS / 32; ++w) s += red[w];
         if (p.C > 1) st_cluster_f32(mapa_shared(smem_u32(norms + rank), threadIdx.x), s);
         else norms[0] = s;
     }
@@ -186,25 +209,26 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
 
     const uint32_t tacc = tmem + (static_cast<uint32_t>(q4 * 32) << 16), tx = tacc + X_COL;
     const uint32_t row_at = row * 128, sw = row & 7;  // 16-byte piece k of the row in an atom: row_at + ((k ^ sw) << 4)
-    // 32 columns of the thread's row as fp16 into X's slice (column c, a multiple of 32)
-    auto put_x = [&](int c, const float (&f)[32]) {
-        const uint32_t at = sbase + (c >> 6) * ATOM + row_at;
+    // offset of 16-byte piece k of columns c .. c + 15 of the thread's row in a matrix of atoms
+    auto piece = [&](int c, int k) { return (c >> 6) * ATOM + row_at + ((((c >> 3) & 7) + k) ^ sw) * 16; };
+    // those columns as fp16 into X's slice
+    auto put_x = [&](int c, const float (&f)[CH]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            st_shared_v4(at + ((((c >> 3) & 7) + k) ^ sw) * 16, half2_bits(f[8 * k], f[8 * k + 1]), half2_bits(f[8 * k + 2], f[8 * k + 3]),
+        for (int k = 0; k < CH / 8; ++k)
+            st_shared_v4(sbase + piece(c, k), half2_bits(f[8 * k], f[8 * k + 1]), half2_bits(f[8 * k + 2], f[8 * k + 3]),
                          half2_bits(f[8 * k + 4], f[8 * k + 5]), half2_bits(f[8 * k + 6], f[8 * k + 7]));
     };
 #pragma unroll 1
-    for (int c = h * width; c < (h + 1) * width; c += 32) {
-        float f[32];
-        uint32_t b[32];
+    for (int c = h * width; c < (h + 1) * width; c += CH) {
+        float f[CH];
+        uint32_t b[CH];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < CH; ++i) {
             const float v = u[row * pitch + c + i];
             f[i] = v == 0.f && inv == inv ? 0.f : v * inv;  // (eps = 0 and a zero matrix: 0 * inf would be NaN)
             b[i] = __float_as_uint(f[i]);
         }
-        tmem_st_32x32b_x32(tx + c, b);
+        tmem_st_x16(tx + c, b);
         put_x(c, f);
     }
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -224,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
             __syncwarp();
         }
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait_suspend(bar, phase, 20000))
+        while (!mbar_try_wait(bar, phase))
             if (global_timer_ns() - t0 > p.a.wait_limit_ns) {
                 // (no early exit: the CTAs of the cluster meet at its barriers)
                 atomicOr(p.a.status, MXFP8_DEV_WAIT_TIMEOUT);
@@ -247,32 +271,31 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
         });
         if (p.C == 1) {
 #pragma unroll 1
-            for (int c = h * 64; c < (h + 1) * 64; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tacc + c, v);
+            for (int c = h * (M / 4); c < (h + 1) * (M / 4); c += CH) {
+                uint32_t v[CH];
+                tmem_ld_x16(tacc + c, v);
                 tmem_wait_ld();
-                reg_fence(v);
-                const uint32_t at = sa + (c >> 6) * ATOM + row_at;
+                fence16(v);
                 constexpr float S = SA / (SX * SX);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < CH / 8; ++k) {
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         w[j] = half2_bits(__uint_as_float(v[8 * k + 2 * j]) * S, __uint_as_float(v[8 * k + 2 * j + 1]) * S);
-                    st_shared_v4(at + ((((c >> 3) & 7) + k) ^ sw) * 16, w[0], w[1], w[2], w[3]);
+                    st_shared_v4(sa + piece(c, k), w[0], w[1], w[2], w[3]);
                 }
             }
         } else {
             float* part = reinterpret_cast<float*>(smem + OFF_P);  // [column][row]
 #pragma unroll 1
-            for (int c = h * 64; c < (h + 1) * 64; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tacc + c, v);
+            for (int c = h * (M / 4); c < (h + 1) * (M / 4); c += CH) {
+                uint32_t v[CH];
+                tmem_ld_x16(tacc + c, v);
                 tmem_wait_ld();
-                reg_fence(v);
+                fence16(v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) part[(c + i) * M + row] = __uint_as_float(v[i]);
+                for (int i = 0; i < CH; ++i) part[(c + i) * M + row] = __uint_as_float(v[i]);
             }
             cluster_sync_all();
             // eight rows of a column of A at a time: its sum over the CTAs, in their
@@ -310,15 +333,14 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
             }
         });
 #pragma unroll 1
-        for (int c = h * 64; c < (h + 1) * 64; c += 32) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(tacc + c, v);
+        for (int c = h * (M / 4); c < (h + 1) * (M / 4); c += CH) {
+            uint32_t v[CH];
+            tmem_ld_x16(tacc + c, v);
             tmem_wait_ld();
-            reg_fence(v);
+            fence16(v);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t off = (c >> 6) * ATOM + row_at + ((((c >> 3) & 7) + k) ^ sw) * 16;
-                const uint4 s = *reinterpret_cast<const uint4*>(smem + OFF_A + off);
+            for (int k = 0; k < CH / 8; ++k) {
+                const uint4 s = *reinterpret_cast<const uint4*>(smem + OFF_A + piece(c, k));
                 const uint32_t in[4] = {s.x, s.y, s.z, s.w};
                 uint32_t w[4];
 #pragma unroll
@@ -331,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
                     if (c + i + 1 == row) f1 -= shift * SA;
                     w[j] = half2_bits(f0, f1);
                 }
-                st_shared_v4(sr + off, w[0], w[1], w[2], w[3]);
+                st_shared_v4(sr + piece(c, k), w[0], w[1], w[2], w[3]);
             }
         }
         // R X: rows of X are the contraction
@@ -342,26 +364,26 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
                            IDESC | (1u << 16) | (static_cast<uint32_t>(p.w >> 3) << 17), k > 0 ? 1u : 0u);
         });
 #pragma unroll 1
-        for (int c = h * width; c < (h + 1) * width; c += 32) {
-            uint32_t v[32], xv[32];
-            tmem_ld_32x32b_x32(tacc + c, v);
-            tmem_ld_32x32b_x32(tx + c, xv);
+        for (int c = h * width; c < (h + 1) * width; c += CH) {
+            uint32_t v[CH], xv[CH];
+            tmem_ld_x16(tacc + c, v);
+            tmem_ld_x16(tx + c, xv);
             tmem_wait_ld();
-            reg_fence(v);
-            reg_fence(xv);
-            float f[32];
+            fence16(v);
+            fence16(xv);
+            float f[CH];
             const float ax = p.a.a + shift;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = fmaf(ax, __uint_as_float(xv[i]), __uint_as_float(v[i]) * (1.f / SA));
+            for (int i = 0; i < CH; ++i) f[i] = fmaf(ax, __uint_as_float(xv[i]), __uint_as_float(v[i]) * (1.f / SA));
             if (!last) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) xv[i] = __float_as_uint(f[i]);
-                tmem_st_32x32b_x32(tx + c, xv);
+                for (int i = 0; i < CH; ++i) xv[i] = __float_as_uint(f[i]);
+                tmem_st_x16(tx + c, xv);
                 put_x(c, f);
             } else if (row < p.m && !p.tall) {
                 uint16_t* dst = p.a.out + base + static_cast<size_t>(row) * p.n + col0 + c;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8)
+                for (int i = 0; i < CH; i += 8)
                     if (c + i < cols) {
                         uint32_t w[4];
 #pragma unroll
@@ -372,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
             } else if (row < p.m) {
                 uint16_t* dst = p.a.out + base + static_cast<size_t>(col0 + c) * p.m + row;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < CH; ++i)
                     if (c + i < cols) dst[static_cast<size_t>(i) * p.m] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i] * (1.f / SX)));
             }
         }
