@@ -30,6 +30,15 @@
 //                 last. No atomics on data: bit-reproducible whoever computes
 //                 what. Last, when all tiles are done, the weighted sum over
 //                 each token's experts.
+//
+// Measured, bytes of the chosen experts' weights over the whole call's time:
+// 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 115 us
+// (5.0 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
+// token 53.5 MB in 29 to 33 us; 32 of 256 experts here, H = 7168, I = 2048,
+// top 8: 128 tokens 1.44 GB in 226 us (6.3 TB/s). A fixed chain of 15 to 16 us
+// stands beside the stream: launches, routing (4 us at one token, 9 at 128),
+// lists, the hand-over of h, the last sum. Small layers are that chain alone
+// (H = 256: 15 us on the GPU, 17 to 19 with the host's launches).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
@@ -176,7 +185,8 @@ __device__ __forceinline__ void split_rows(const Params& p, int first, int strid
 // thread's 16 bytes hold eight consecutive values of a row: the same
 // assignment of columns to the MMA's K on both sides, so the sum is the dot
 // product whatever the order. The blocks after those split x into pieces and
-// zero the counters.
+// zero the counters. Latency-bound: 6.7 us at 64 tokens, 64 experts, H = 2048
+// with a cold L2. Larger blocks above 16 tokens re-read x and the router less.
 template <int MF, int NF>
 __global__ void __launch_bounds__(256) moe_logits(const Params p) {
     __shared__ float red[8][16 * MF][8 * NF];
@@ -781,7 +791,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int wr = b.g.phase ? min(b.g.rt * TILE + 32 * h + lane, p.H - 1)
                                          : (h >> 1) * p.I + min(b.g.rt * (TILE / 2) + 32 * (h & 1) + lane, p.I - 1);
                 const size_t at = (base + wr) * K32 + 4 * k;
-                if ((K32 & 7) == 0) {
+                if (((K32 | static_cast<int>(reinterpret_cast<uintptr_t>(plane))) & 7) == 0) {  // (the planes: 4-byte aligned)
                     const uint2 u = __ldg(reinterpret_cast<const uint2*>(plane + at));
                     v[h][0] = u.x; v[h][1] = u.y;
                 } else {

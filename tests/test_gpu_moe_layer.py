@@ -257,6 +257,21 @@ def test_example_runs():
     assert not update[2].any() and not moms[1][2].any() and update[1].any()
 
 
+def test_scale_planes_off_by_a_word():
+    """Scale planes are 4-byte aligned, no more, also where their rows are whole 8-byte words."""
+    T, H, I, experts = 3, 512, 256, 4
+    x, router, w13, s13, w2, s2 = make(T, H, I, experts, experts, 31)
+    args = list(device_args(x, router, w13, s13, w2, s2))
+    want = run(args, 2)[0]
+    for i in (3, 5):
+        room = torch.zeros(args[i].numel() + 4, dtype=torch.uint8, device="cuda")
+        off = room[4:].view(args[i].shape)
+        off.copy_(args[i])
+        assert off.data_ptr() % 8 == 4
+        args[i] = off
+    assert torch.equal(run(args, 2)[0], want)
+
+
 def test_no_tokens():
     ops = make(1, 64, 32, 4, 4, seed=14)
     args = list(device_args(*ops))
