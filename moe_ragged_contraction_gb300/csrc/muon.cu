@@ -27,6 +27,16 @@
 // matrix only, so with several matrices the pairs never drain between
 // products. A A^T-type products are symmetric: only tiles on and below the
 // diagonal are computed and each is stored twice.
+//
+// What bounds it (five steps, momentum). Many tiles, 8 x 1408 x 2048: 584 us a
+// call, of which muon_main 480 for 599 GFLOP, 1.25 PFLOP/s; its tensor pipe is
+// active in 72% of the cycles. The rest is the SM's intake: operands at the full
+// rate of the MMA use all of its 64 bytes a clock, and the epilogue's reads of
+// earlier products and planes compete with them (without an epilogue the
+// same list of products takes 330 us). 32 x 7168 x 2048: 13.7 ms for 15.8 TFLOP.
+// Few tiles, 3 x 331 x 1000: 119 us, a chain of 15 products of 7 to 7.6 us each:
+// hand-over 1.2, first operands 0.85, products 1.75, epilogue 2.2, stores
+// and their report 1.3 to 2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -108,12 +118,15 @@ __device__ __forceinline__ float4 load_u(const MuonArgs& a, size_t i) {
     return make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
 }
 
+// One pass: momentum in place, a block's partial sum of u^2. HBM-bound: 10 bytes
+// an element with bf16 gradients, 35 us at 8 x 1408 x 2048 (6.6 TB/s). A block's
+// share is contiguous and the partial sums are joined in block order by
+// muon_scale: the same bits on every run.
 __global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* part, unsigned int* done, int n_done) {
     griddep_launch_dependents();
     griddep_wait();  // the gradient may come from the kernel before, and a call before may still use the scratch
     const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
     float s = 0.f;
-    // (a block's share is contiguous; at the 16B shape 6.6 TB/s)
     const size_t share = (per / 4 + NORM_BLOCKS - 1) / NORM_BLOCKS * 4, end = min(per, (blockIdx.x + 1) * share);
     for (size_t i = blockIdx.x * share + 4 * threadIdx.x; i < end; i += 4 * 256) {
         const float4 u = load_u<true>(a, base + i);
@@ -134,6 +147,9 @@ __global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* pa
 }
 
 // X0 in two planes; tall matrices are transposed on the way, 64 x 64 at a time.
+// u is formed again from gradient and momentum (a third array of u would cost as
+// much to write as this saves). HBM-bound: 10 bytes an element, 41 us at
+// 8 x 1408 x 2048 (5.6 TB/s).
 __global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params p, const float* part) {
     __shared__ float t[64][65];
     __shared__ float s_inv;
@@ -281,7 +297,7 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
-// A tile of a product: ph 0: A = X X^T, 1: R = b A + c A A - beta I, 2: X <- (a + beta) X + R X.
+// A tile of a product. ph 0: A = X X^T, 1: R = b A + c A A - beta I, 2: X <- (a + beta) X + R X.
 struct Item {
     int step, ph, e, i, j, k0, ksteps, tile, part;  // first K-step and their number; index and piece of a tile of X X^T
 };
@@ -722,7 +738,9 @@ void layout(int E, int N, int K, Layout* l) {
     l->ldm = (l->m + 63) & ~63;
     l->ldn = (l->n + 63) & ~63;
     // Tiles of 128 columns where those of 256 would leave pairs without one: each
-    // then takes half the time to compute and store.
+    // then takes half the time to compute and store (5 steps: 1 x 2048 x 1408 256
+    // -> 218 us, 3 x 331 x 1000 165 -> 125 us). With more tiles the wider ones
+    // win: they need three quarters of the operand bytes for the same products.
     l->T = (l->m + TILE - 1) / TILE;
     l->tn = static_cast<long long>(E) * l->T * ((l->n + TILE - 1) / TILE) <= PAIRS ? TILE / 2 : TILE;
     const int Tm = (l->m + l->tn - 1) / l->tn, ksteps = (l->n + KSTEP - 1) / KSTEP;
@@ -730,7 +748,9 @@ void layout(int E, int N, int K, Layout* l) {
     l->sym = 0;
     for (int i = 0; i < l->T; ++i) l->sym += Tm < (i + 1) * (TILE / l->tn) ? Tm : (i + 1) * (TILE / l->tn);
     // The contraction of X X^T in pieces of sixteen K-steps or more where its tiles
-    // occupy less than half of the pairs.
+    // occupy less than half of the pairs: the piece that ends last adds them up in
+    // order (1 x 129 x 7032 290 -> 166 us; pieces of eight K-steps cost more to
+    // join than they save, 3 x 331 x 1000 129 -> 146 us).
     const long long tiles = static_cast<long long>(E) * l->sym;
     l->parts = 1;
     if (2 * tiles <= PAIRS) {

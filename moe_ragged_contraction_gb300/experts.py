@@ -6,7 +6,6 @@ from __future__ import annotations
 from . import _lib
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
-MAX_TOKENS = 128
 
 _torch = None
 _raw_stream = None  # device index -> handle of the current stream
