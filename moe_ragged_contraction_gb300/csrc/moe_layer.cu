@@ -61,11 +61,12 @@ constexpr int MAX_ST = 12;           // pipeline stages
 constexpr int THREADS = 288;         // warps: 0 weight producer, 1 MMA issuer, 2, 3, 8 loaders, 4 .. 7 epilogue
 constexpr int LOADERS = 3;
 constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (rings of 6 stages or more; else 1)
-constexpr int SMEM_MAX = 232448;
-constexpr int SMEM_FEW = 221184;      // leaves room beside a moe_logits<1, 2> block: the next kernel's CTAs start under it
+constexpr int SMEM = 221184;         // leaves room beside a moe_logits<1, 2> block: moe_experts' CTAs start under it (all of
+                                     // it instead: 95.5 -> 99 us for 16 tokens of the 671B rank, equal from 64 tokens on)
 constexpr uint32_t TMEM_ALL = 512;
 // counters: tokens claimed and chosen for, units claimed, down units done
 constexpr int C_CLAIM = 0, C_CHOSEN = 1, C_QUEUE = 2, C_DONE = 3, C_H = 4;
+constexpr int MAX_PARTS = 8;         // pieces of a tile's contraction
 constexpr int NQ = 4;                // queue entries in flight in a CTA
 constexpr int EPI_BAR = 1;           // named barriers: the epilogue warps; the lists are made; the pairs are placed
 constexpr int LIST_BAR = 2, PLACE_BAR = 3;
@@ -92,7 +93,7 @@ struct Params {
     float *part_up, *part_down;  // [unit][T][128]
     int Hp, Ip, sh_stride, ksplit, slots, n_counters;
     int up_tiles, down_tiles, up_steps, down_steps;
-    uint32_t off_lists, off_mask, off_epi, off_rows, off_ring, smem;
+    uint32_t off_lists, off_mask, off_epi, off_rows, off_ring;
     unsigned long long wait_ns;
     int* status;
     int stall;               // test hook: over-declare the first stage's bytes so that its wait runs out
@@ -186,7 +187,7 @@ __device__ __forceinline__ void split_rows(const Params& p, int first, int strid
 // assignment of columns to the MMA's K on both sides, so the sum is the dot
 // product whatever the order. The blocks after those split x into pieces and
 // zero the counters. Latency-bound: 6.7 us at 64 tokens, 64 experts, H = 2048
-// with a cold L2. Larger blocks above 16 tokens re-read x and the router less.
+// with a cold L2.
 template <int MF, int NF>
 __global__ void __launch_bounds__(256) moe_logits(const Params p) {
     __shared__ float red[8][16 * MF][8 * NF];
@@ -403,7 +404,7 @@ struct Lists {
 // give every CTA one, at least four K-steps each. Handing a partial sum over
 // costs several K-steps' time, so tiles that outnumber half the CTAs stay whole.
 __device__ __forceinline__ int parts_of(int tiles, int steps, int G) {
-    return 2 * tiles > G ? 1 : max(1, min(min(G / max(tiles, 1), steps / 4), 8));
+    return 2 * tiles > G ? 1 : max(1, min(min(G / max(tiles, 1), steps / 4), MAX_PARTS));
 }
 
 // A unit of the queue: K-steps [k0, k1) of a tile.
@@ -411,13 +412,14 @@ struct Seg {
     int phase, tile, a, rt, part, parts, k0, k1, steps;
 };
 
+template <bool PARTS>
 struct Queue {
     int nact, up_parts, down_parts, up_units, units;
     const Params& p;
 
     __device__ __forceinline__ Queue(const Params& p_, int G, int nact_) : nact(nact_), p(p_) {
-        up_parts = parts_of(nact * p.up_tiles, p.up_steps, G);
-        down_parts = parts_of(nact * p.down_tiles, p.down_steps, G);
+        up_parts = PARTS ? parts_of(nact * p.up_tiles, p.up_steps, G) : 1;
+        down_parts = PARTS ? parts_of(nact * p.down_tiles, p.down_steps, G) : 1;
         up_units = nact * p.up_tiles * up_parts;
         units = up_units + nact * p.down_tiles * down_parts;
     }
@@ -426,12 +428,12 @@ struct Queue {
         Seg g;
         g.phase = u >= up_units;
         const int v = g.phase ? u - up_units : u, tiles = g.phase ? p.down_tiles : p.up_tiles;
-        g.parts = g.phase ? down_parts : up_parts;
+        g.parts = PARTS ? (g.phase ? down_parts : up_parts) : 1;
         g.steps = g.phase ? p.down_steps : p.up_steps;
         g.tile = v;
         g.part = g.k0 = 0;
         g.k1 = g.steps;
-        if (g.parts > 1) {
+        if (PARTS && g.parts > 1) {
             g.tile = v / g.parts;
             g.part = v - g.tile * g.parts;
             g.k0 = g.steps * g.part / g.parts;
@@ -443,6 +445,8 @@ struct Queue {
     }
 };
 
+// PARTS: tiles may be cut along the contraction (see cuts()).
+template <bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
     moe_experts(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2, const Params p) {
     extern __shared__ uint8_t raw_smem[];
@@ -620,12 +624,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t nblk = (nmax + 127) / 128;
     const uint32_t sf_stage = 512 * (1 + nblk);
     const uint32_t ab_stage = A_BYTES + nmax * STEP;
-    const int S = min(MAX_ST, static_cast<int>((p.smem - 1024 - p.off_ring) / (ab_stage + sf_stage)));
+    const int S = min(MAX_ST, static_cast<int>((SMEM - 1024 - p.off_ring) / (ab_stage + sf_stage)));
     const uint32_t ring = sbase + p.off_ring, sf_ring = ring + S * ab_stage;
     const uint32_t sf_cols = 4 * (1 + nblk);
     const int nbuf = 2 * nmax + S * static_cast<int>(sf_cols) <= 512 ? 2 : 1;  // accumulators
     const uint32_t sf_tmem = tmem + nbuf * nmax;
-    const Queue queue(p, G, nact);
+    const Queue<PARTS> queue(p, G, nact);
     volatile int* entry = flags + 9;  // [NQ] units; -1: no more
 
     // Reader's side of the queue: the next entry (-1 at the end), or -2 after an abort.
@@ -909,7 +913,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (unit < 0) break;
             const Seg g = queue.get(unit);
             const int nt = L.count[g.a], off = L.off[g.a];
-            const bool whole = g.parts == 1;
+            const bool whole = !PARTS || g.parts == 1;
             ++tile;
             tc_fence_after();
             const uint32_t d = tmem + buf * nmax + (static_cast<uint32_t>(q * 32) << 16);
@@ -966,11 +970,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int o = q; finish && o < 2 * nt; o += 4) {
                         const int j = o >> 1, i = 32 * (o & 1) + lane, i0 = g.rt * (TILE / 2) + 32 * (o & 1);
                         if (i0 >= p.I) continue;
-                        float gate = 0.f, up = 0.f;
-                        const float* src = p.part_up + static_cast<size_t>(g.tile * g.parts) * p.T * TILE + static_cast<size_t>(j) * TILE;
-                        for (int c = 0; c < g.parts; ++c, src += static_cast<size_t>(p.T) * TILE) {
-                            gate += __ldcg(src + i);
-                            up += __ldcg(src + TILE / 2 + i);
+                        const float* src = p.part_up + static_cast<size_t>(g.tile * g.parts) * p.T * TILE + static_cast<size_t>(j) * TILE + i;
+                        const size_t piece = static_cast<size_t>(p.T) * TILE;
+                        float vg[MAX_PARTS], vu[MAX_PARTS], gate = 0.f, up = 0.f;  // (all loads in flight together)
+#pragma unroll
+                        for (int c = 0; c < MAX_PARTS; ++c) {
+                            vg[c] = c < g.parts ? __ldcg(src + c * piece) : 0.f;
+                            vu[c] = c < g.parts ? __ldcg(src + c * piece + TILE / 2) : 0.f;
+                        }
+#pragma unroll
+                        for (int c = 0; c < MAX_PARTS; ++c) {
+                            gate += vg[c];
+                            up += vu[c];
                         }
                         store_h(p, off + j, i0, gate, up);
                     }
@@ -1008,10 +1019,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int i = t * p.top_k + k0 + j;
                 e[j] = k0 + j < p.top_k ? L.eid[i] : 0xffff;
                 v[j] = make_float2(0.f, 0.f);
-                if (e[j] != 0xffff && queue.down_parts == 1)
+                if (e[j] != 0xffff && (!PARTS || queue.down_parts == 1))
                     v[j] = __ldcg(reinterpret_cast<const float2*>(p.y + static_cast<size_t>(L.slot_of[i]) * p.Hp + n));
             }
-            if (queue.down_parts > 1) {
+            if (PARTS && queue.down_parts > 1) {
                 // the parts of each down tile, in order; then the expert's weight
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -1019,10 +1030,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const int i = t * p.top_k + k0 + j, a = L.act_of[e[j]];
                     const float* src = p.part_down + static_cast<size_t>(a * p.down_tiles + rt) * queue.down_parts * p.T * TILE +
                                        static_cast<size_t>(L.slot_of[i] - L.off[a]) * TILE + r;
-                    for (int c = 0; c < queue.down_parts; ++c) {
-                        const float2 z = __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(c) * p.T * TILE));
-                        v[j].x += z.x;
-                        v[j].y += z.y;
+                    float2 z[MAX_PARTS];
+#pragma unroll
+                    for (int c = 0; c < MAX_PARTS; ++c)
+                        z[c] = c < queue.down_parts ? __ldcg(reinterpret_cast<const float2*>(src + static_cast<size_t>(c) * p.T * TILE))
+                                                    : make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < MAX_PARTS; ++c) {
+                        v[j].x += z[c].x;
+                        v[j].y += z[c].y;
                     }
                     v[j].x *= L.wts[i];
                     v[j].y *= L.wts[i];
@@ -1048,12 +1064,19 @@ struct Layout {
 };
 
 void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Layout* l) {
-    l->mf = T > 16 ? 2 : 1;
-    l->nf = T > 16 ? 4 : 2;
-    // slices of H so that about 300 blocks share the logits, each of their 8 warps at least one 32-column chunk
-    const int tiles = ((experts + 8 * l->nf - 1) / (8 * l->nf)) * ((T + 16 * l->mf - 1) / (16 * l->mf));
-    int ks = 300 / tiles;
-    if (ks > 8) ks = 8;
+    // Logits: tiles of 16 tokens x 16 experts, H in up to 8 slices so that about 300
+    // blocks share them, each of their 8 warps at least one 32-column chunk. Tiles
+    // of 32 x 32, which read x and the router half as often, where the small ones
+    // are so many that they would get fewer slices (whole call, 32 x 32 / 16 x 16: H = 7168,
+    // 256 experts, 128 tokens 229 / 235 us, 32 tokens 151.4 / 147.7; H = 2048, 64
+    // experts, 64 tokens 122.0 / 119.8).
+    auto tiles_of = [&](int mf, int nf) { return ((experts + 8 * nf - 1) / (8 * nf)) * ((T + 16 * mf - 1) / (16 * mf)); };
+    constexpr int BLOCKS = 300, SLICES = 8;
+    const bool wide = T > 16 && tiles_of(1, 2) > BLOCKS / SLICES;
+    l->mf = wide ? 2 : 1;
+    l->nf = wide ? 4 : 2;
+    int ks = BLOCKS / tiles_of(l->mf, l->nf);
+    if (ks > SLICES) ks = SLICES;
     if (ks > H / 256) ks = H / 256;
     l->ksplit = ks < 1 ? 1 : ks;
     l->Hp = (H + STEP - 1) / STEP * STEP;
@@ -1080,6 +1103,21 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
     l->part_up = take(4 * static_cast<size_t>(sms) * T * TILE);  // (parts are only made up to one per SM)
     l->part_down = take(4 * static_cast<size_t>(sms) * T * TILE);
     l->total = at;
+}
+
+// Whether a call takes the form of moe_experts that can cut tiles along the
+// contraction: where a contraction of 32 K-steps or more (4096 columns) is
+// expected to meet fewer tiles than CTAs. Which experts are chosen is known on
+// the GPU only; here their number is taken as if all were equally likely, and
+// what is cut, if anything, is decided there (parts_of). H = 7168, I = 2048, 32
+// experts of 256, 1 / 2 / 4 tokens: 24.1 / 31.6 / 46.7 us in this form, 26.5 / 34.0 /
+// 47.8 without cuts; one expert of I = 128, 64 tokens: 59.9 / 79.8. Elsewhere
+// the cuts' code alone costs 1 to 4 us (H = 2048, I = 1408, 64 experts, 128 tokens:
+// 136.6 / 132.7).
+bool cuts(const MoeArgs& a, const Layout& l) {
+    const long long pairs = static_cast<long long>(a.T) * a.top_k * a.local / a.experts;
+    const long long chosen = pairs < 1 ? 1 : pairs < a.local ? pairs : a.local;
+    return (l.up_steps >= 32 && chosen * l.up_tiles <= a.num_sms) || (l.down_steps >= 32 && chosen * l.down_tiles <= a.num_sms);
 }
 
 }  // namespace
@@ -1116,7 +1154,6 @@ int launch_moe(const MoeArgs& a) {
     p.off_epi = (p.off_mask + a.local * 16 + 127) & ~127u;
     p.off_rows = p.off_epi + 2 * 8 * TILE * 4;
     p.off_ring = (p.off_rows + LOADERS * 1024 + 1023) & ~1023u;
-    p.smem = l.mf == 1 ? SMEM_FEW : SMEM_MAX;
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
     p.stall = a.stall;
@@ -1134,7 +1171,8 @@ int launch_moe(const MoeArgs& a) {
     static std::atomic<bool> ready[64];
     cudaError_t e;
     if (!ready[a.dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(moe_experts, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+        e = cudaFuncSetAttribute(moe_experts<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(moe_experts<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s", cudaGetErrorString(e));
         ready[a.dev].store(true, std::memory_order_relaxed);
     }
@@ -1154,8 +1192,8 @@ int launch_moe(const MoeArgs& a) {
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "router kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     cfg.gridDim = dim3(a.num_sms);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = p.smem;
-    e = cudaLaunchKernelEx(&cfg, moe_experts, m13, m2, p);
+    cfg.dynamicSmemBytes = SMEM;
+    e = cuts(a, l) ? cudaLaunchKernelEx(&cfg, moe_experts<true>, m13, m2, p) : cudaLaunchKernelEx(&cfg, moe_experts<false>, m13, m2, p);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "expert layer kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     return MXFP8_OK;
 }
