@@ -741,12 +741,14 @@ void layout(int E, int N, int K, Layout* l) {
     l->n = N < K ? K : N;
     l->ldm = (l->m + 63) & ~63;
     l->ldn = (l->n + 63) & ~63;
-    // Tiles of 128 columns where those of 256 would leave pairs without one: each
-    // then takes half the time to compute and store (5 steps: 1 x 2048 x 1408 256
-    // -> 218 us, 3 x 331 x 1000 165 -> 125 us). With more tiles the wider ones
-    // win: they need three quarters of the operand bytes for the same products.
+    // Tiles of 128 columns up to 1 3/4 tiles of 256 a pair: each then takes half
+    // the time to compute and store, which shortens the chain of products (5 steps,
+    // 256 / 128: 1 x 2048 x 1408, 48 tiles, 244 / 195 us; 4 x 1024 x 1024, 64, 202 / 167;
+    // 20 x 512 x 512, 80, 203 / 160; 1 x 2048 x 4096, 128, 379 / 365). With more, the wider
+    // ones win: they need three quarters of the operand bytes for the same products
+    // (1 x 3000 x 3000, 144, 566 / 635; 4 x 1408 x 2048, 192, 322 / 358).
     l->T = (l->m + TILE - 1) / TILE;
-    l->tn = static_cast<long long>(E) * l->T * ((l->n + TILE - 1) / TILE) <= PAIRS ? TILE / 2 : TILE;
+    l->tn = 4LL * E * l->T * ((l->n + TILE - 1) / TILE) <= 7 * PAIRS ? TILE / 2 : TILE;
     const int Tm = (l->m + l->tn - 1) / l->tn, ksteps = (l->n + KSTEP - 1) / KSTEP;
     l->full = l->T * ((l->n + l->tn - 1) / l->tn);
     l->sym = 0;

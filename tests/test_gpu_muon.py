@@ -168,6 +168,24 @@ def test_long_matrices(E, N, K):
     assert mx.device_status(clear=True) == 0
 
 
+@pytest.mark.parametrize("E,N,K", [
+    (22, 264, 520), (23, 264, 520), (23, 520, 264),   # 132 tiles of 256 x 256: halved; 138: whole, wide and tall
+    (12, 777, 1032), (9, 1100, 600), (35, 257, 257 + 7),
+])
+def test_many_tiles(E, N, K):
+    g = bf16_round(gradient(E, N, K, seed=E + N, kind="strong"))
+    m0 = gradient(E, N, K, seed=E)
+    g[E // 2] = 0
+    m0[E // 2] = 0
+    gd, md = cuda(g, torch.bfloat16), cuda(m0)
+    out = mx.muon_update(gd, md)
+    want, m1 = muon(g, m0)
+    close(out, want)
+    assert np.allclose(md.cpu().numpy(), m1, rtol=2e-6, atol=1e-9)
+    assert torch.equal(out, mx.muon_update(gd, cuda(m0)))
+    assert mx.device_status(clear=True) == 0
+
+
 @pytest.mark.parametrize("N,K", [(40, 96), (96, 40), (300, 200), (200, 304)])
 def test_one_step_against_differences(N, K):
     """One step is odd in u and its derivative at u in direction d is what the formula's differences give."""
