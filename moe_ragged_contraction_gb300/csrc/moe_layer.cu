@@ -32,8 +32,8 @@
 //                 each token's experts.
 //
 // Measured, bytes of the chosen experts' weights over the whole call's time:
-// 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 115 us
-// (5.0 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
+// 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 112 us
+// (5.1 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
 // token 53.5 MB in 29 to 33 us; 32 of 256 experts here, H = 7168, I = 2048,
 // top 8: 128 tokens 1.44 GB in 226 us (6.3 TB/s). A fixed chain of 15 to 16 us
 // stands beside the stream: launches, routing (4 us at one token, 9 at 128),

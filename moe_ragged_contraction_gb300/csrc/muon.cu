@@ -34,7 +34,7 @@
 // rate of the MMA use all of its 64 bytes a clock, and the epilogue's reads of
 // earlier products and planes compete with them (without an epilogue the
 // same list of products takes 330 us). 32 x 7168 x 2048: 13.7 ms for 15.8 TFLOP.
-// Few tiles, 3 x 331 x 1000: 119 us, a chain of 15 products of 7 to 7.6 us each:
+// Few tiles, 3 x 331 x 1000: 117 us, a chain of 15 products of 7 to 7.6 us each:
 // hand-over 1.2, first operands 0.85, products 1.75, epilogue 2.2, stores
 // and their report 1.3 to 2.
 #include <cuda_bf16.h>

@@ -243,6 +243,21 @@ def test_few_long_tiles_are_cut_into_parts():
         assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("T,H,I", [
+    (1, 7168, 64), (40, 4512, 160),        # long rows of x: the up and gate products in parts
+    (3, 96, 4128), (17, 288, 4096),        # long rows of h: the down products in parts
+    (1, 4128, 4224), (128, 4096, 32),      # both; the most tokens
+])
+def test_long_contractions_are_cut_into_parts(T, H, I):
+    """Few tiles with contractions of 4096 columns and more, odd numbers of K-steps among them, two experts of six here."""
+    ops = make(T, H, I, 6, 2, seed=H + I)
+    args = device_args(*ops)
+    out, ids, weights = run(args, 3, first_expert=2)
+    check(*ops, 3, out, ids, weights, first=2)
+    again, _, _ = run(args, 3, first_expert=2)
+    assert torch.equal(out, again)
+
+
 def test_example_runs():
     """The example's path: gradients, update, quantised weights, layer; an expert without tokens stays as it was."""
     import importlib.util
