@@ -64,6 +64,10 @@ constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (r
 constexpr int SMEM = 221184;         // leaves room beside a moe_logits<1, 2> block: moe_experts' CTAs start under it (all of
                                      // it instead: 95.5 -> 99 us for 16 tokens of the 671B rank, equal from 64 tokens on)
 constexpr uint32_t TMEM_ALL = 512;
+// the largest lists, masks and stages still leave a ring of a stage per loader (launch_moe lays them out)
+static_assert((SMEM - 1024 - (512 + MXFP8_MOE_MAX_TOKENS * MXFP8_MOE_MAX_TOPK * 10 + MXFP8_MOE_MAX_EXPERTS * 24 + 256 + 2 * 8 * TILE * 4 +
+                              LOADERS * 1024 + 1024)) / (A_BYTES + PIECES * MXFP8_MOE_MAX_TOKENS * STEP + 512 * 3) >= LOADERS,
+              "pipeline stages");
 // counters: tokens claimed and chosen for, units claimed, down units done
 constexpr int C_CLAIM = 0, C_CHOSEN = 1, C_QUEUE = 2, C_DONE = 3, C_H = 4;
 constexpr int MAX_PARTS = 8;         // pieces of a tile's contraction

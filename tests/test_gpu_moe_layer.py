@@ -258,6 +258,19 @@ def test_long_contractions_are_cut_into_parts(T, H, I):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("H,I", [(1056, 32), (64, 1056)])
+def test_largest_lists_and_fewest_stages(H, I):
+    """The most tokens, experts and choices, every token with the same sixteen experts: 256 columns, three stages."""
+    T, experts, top_k = 128, 1024, 16
+    x, router, w13, s13, w2, s2 = make(T, H, I, experts, experts, seed=77)
+    bias = np.zeros(experts, np.float32)
+    bias[np.arange(top_k) * 63 + 5] = 2.0  # (softmax scores are at most one)
+    args = device_args(x, router, w13, s13, w2, s2)
+    out, ids, weights = run(args, top_k, bias=cuda(bias))
+    check(x, router, w13, s13, w2, s2, top_k, out, ids, weights, bias=bias)
+    assert set(ids.cpu().numpy().ravel().tolist()) == set((np.arange(top_k) * 63 + 5).tolist())
+
+
 def test_example_runs():
     """The example's path: gradients, update, quantised weights, layer; an expert without tokens stays as it was."""
     import importlib.util
