@@ -362,7 +362,8 @@ __device__ __noinline__ void drain_bar(uint32_t bar, uint32_t parity, unsigned l
         }
 }
 
-// Bounded wait until *p >= target (acquire).
+// Bounded wait until *p >= target: an acquire each time, no pause (polled relaxed
+// with one acquire at the end: 16B, 64 tokens 119.7 -> 121.5 us).
 __device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int target, volatile int* abort_flag,
                                            unsigned long long ns, int* status) {
     const uint64_t t0 = global_timer_ns();
@@ -374,7 +375,6 @@ __device__ __noinline__ bool wait_count(const unsigned int* p, unsigned int targ
             atomicOr(status, MXFP8_DEV_WAIT_TIMEOUT);
             return false;
         }
-        __nanosleep(20);
     }
 }
 

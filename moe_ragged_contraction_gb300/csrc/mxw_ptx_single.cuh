@@ -103,12 +103,6 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const unsigned int* p) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t ld_relaxed_gpu(const unsigned int* p) {
-    uint32_t v;
-    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void red_release_gpu_add(unsigned int* p, uint32_t v) {
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
