@@ -78,7 +78,7 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if out is None:
-        out = torch.empty((T, H), dtype=bf16, device=x.device)
+        out = torch.empty_like(x)
     else:
         _check(out, bf16, (T, H), "out", device)
     if topk_ids is not None:
@@ -133,7 +133,7 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
         _check(momentum, torch.float32, shape, "momentum", device)
         momentum_p = momentum.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=grad.device)
+        out = torch.empty_like(grad, dtype=torch.bfloat16)
     else:
         _check(out, torch.bfloat16, shape, "out", device)
     a, b, c = coeffs
