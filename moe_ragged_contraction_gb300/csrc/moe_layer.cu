@@ -38,7 +38,7 @@
 // top 8: 128 tokens 1.44 GB in 226 us (6.3 TB/s). A fixed chain of 15 to 16 us
 // stands beside the stream: launches, routing (4 us at one token, 9 at 128),
 // lists, the hand-over of h, the last sum. Small layers are that chain alone
-// (H = 256: 15 us on the GPU, 17 to 19 with the host's launches).
+// (H = 256: 15 us on the GPU, 17 with the host's launches).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
