@@ -35,7 +35,7 @@
 // 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 112 us
 // (5.1 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
 // token 53.5 MB in 29 to 33 us; 32 of 256 experts here, H = 7168, I = 2048,
-// top 8: 128 tokens 1.44 GB in 226 us (6.3 TB/s). A fixed chain of 15 to 16 us
+// top 8: 128 tokens 1.44 GB in 227 to 241 us, by box. A fixed chain of 15 to 16 us
 // stands beside the stream: launches, routing (4 us at one token, 9 at 128),
 // lists, the hand-over of h, the last sum. Small layers are that chain alone
 // (H = 256: 15 us on the GPU, 17 with the host's launches).
