@@ -106,6 +106,14 @@ size_t mxfp8_moe_layer_workspace_bytes(int T, int experts, int local, int H, int
  *   E        0 <= E <= MXFP8_MAX_EXPERTS (E == 0: no-op); N, K >= 1, at most 32768, K % 8 == 0
  *   steps    1..MXFP8_MUON_MAX_STEPS;  a, b, c finite, |a|, |b|, |c| <= 16;  eps >= 0
  *
+ * Coefficients whose iteration can leave the range of the fp16 operands are
+ * refused (MXFP8_EINVAL). With X0's singular values anywhere in [0, 1], no
+ * singular value of an X that is multiplied may pass sqrt(14), and no
+ * eigenvalue of b A + c A A - beta I may pass 14 in magnitude, where beta is
+ * 0.875 (b + c) in the last step, half of that in the one before and zero in the
+ * others. Maps that keep [0, 1] near [0, 1.3], the default among them, pass for
+ * every step count; a X alone passes for a^(steps - 1) up to 3.7.
+ *
  * The products run on fp16 operands with 11 significant bits (scaled by
  * powers of two) and fp32 accumulation; the a X term keeps 22 bits: the
  * result is within about 1.5e-3 (2-norm, relative) of the exact iteration

@@ -70,6 +70,47 @@ bool muon_sizes(int E, int N, int K) {
     return E >= 0 && E <= MXFP8_MAX_EXPERTS && N >= 1 && N <= 32768 && K >= 1 && K <= 32768;
 }
 
+// Largest |k0 + k1 t + k2 t^2| on [0, T].
+double quadratic_max(double k0, double k1, double k2, double T) {
+    double m = std::fmax(std::fabs(k0), std::fabs(k0 + (k1 + k2 * T) * T));
+    const double t = -k1 / (2 * k2);
+    if (t > 0 && t < T) m = std::fmax(m, std::fabs(k0 + (k1 + k2 * t) * t));
+    return m;
+}
+
+// Largest |a s + b s^3 + c s^5| on [0, S].
+double step_max(double a, double b, double c, double S) {
+    auto f = [&](double s) { const double t = s * s; return std::fabs(s * (a + t * (b + t * c))); };
+    double m = f(S);
+    // the derivative a + 3 b t + 5 c t^2 vanishes; with c = 0 at t = -a / (3 b)
+    const double d = 9 * b * b - 20 * a * c;
+    if (d >= 0) {
+        const double q = -(3 * b + std::copysign(std::sqrt(d), b)) / 2;  // (the root without cancellation, the other from their product)
+        for (const double t : {q / (5 * c), a / q})
+            if (t > 0 && t < S * S) m = std::fmax(m, f(std::sqrt(t)));
+    }
+    return m;
+}
+
+// Whether the iteration stays in the range of the kernels' fp16 operands for
+// every matrix. X0's singular values fill [0, 1]; a step takes s to a s + b s^3
+// + c s^5, so that A's largest eigenvalue and R's largest value (R = b A + c A A
+// - beta I) are known beforehand. Both are stored times 4096 and end at 16; the
+// limit of 14 and the share added to each step's largest value (four roundings
+// to 11 bits of R's terms) leave room for what the roundings add.
+constexpr double MUON_LIMIT = 14.0;
+
+bool muon_in_range(double a, double b, double c, int steps) {
+    double S = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const double T = S * S, beta = (b + c) * (k + 1 == steps ? 0.875 : k + 2 == steps ? 0.4375 : 0.0);
+        const double r = quadratic_max(-beta, b, c, T);
+        if (!(T <= MUON_LIMIT) || !(r <= MUON_LIMIT)) return false;
+        S = step_max(a, b, c, S) + S * (std::fabs(b) * T + 2 * std::fabs(c) * T * T + r) / 1024;
+    }
+    return true;
+}
+
 int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, float mu, int nesterov, int steps,
          float a_, float b_, float c_, float eps, uint16_t* out, void* ws, size_t ws_bytes, bool use_cache,
          void* stream) {
@@ -82,6 +123,11 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
         return host_fail(MXFP8_EINVAL, "steps=%d out of range [1, %d]", steps, MXFP8_MUON_MAX_STEPS);
     if (!(std::fabs(a_) <= 16.f) || !(std::fabs(b_) <= 16.f) || !(std::fabs(c_) <= 16.f))
         return host_fail(MXFP8_EINVAL, "coefficients %g, %g, %g: finite and at most 16 in magnitude", a_, b_, c_);
+    if (!muon_in_range(a_, b_, c_, steps))
+        return host_fail(MXFP8_EINVAL,
+                         "coefficients %g, %g, %g with %d steps leave the range of the products' operands: the eigenvalues of A "
+                         "or R can exceed %g",
+                         a_, b_, c_, steps, MUON_LIMIT);
     if (!std::isfinite(mu) || !std::isfinite(eps) || eps < 0.f)
         return host_fail(MXFP8_EINVAL, "mu=%g must be finite and eps=%g finite and >= 0", mu, eps);
     if ((K % 8) != 0) return host_fail(MXFP8_EALIGN, "K=%d must be a multiple of 8 (16-byte output rows)", K);

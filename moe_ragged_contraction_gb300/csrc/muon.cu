@@ -10,8 +10,9 @@
 //
 // Precision. The products run on fp16 operands (11 significant bits, eight
 // times finer than bf16 at the same rate) scaled by powers of two so that the
-// magnitudes that occur (||X||_2 below 32) neither overflow nor meet fp16's
-// subnormals; the accumulators are fp32. Rounding X itself to 11 bits would cost
+// magnitudes that occur neither overflow nor meet fp16's subnormals (A and R end
+// at 16, so ||X||_2 at 4: the entry point refuses coefficients that can lead
+// there); the accumulators are fp32. Rounding X itself to 11 bits would cost
 // more: its error is spread over all directions while every step multiplies a
 // small singular value by a = 3.4, so that the error of the first steps grows
 // a hundredfold beside what it is to be compared with. The a X term therefore

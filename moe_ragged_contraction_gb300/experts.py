@@ -112,8 +112,9 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
 
     grad: bf16 or fp32 [E, N, K] (or one matrix [N, K]), e.g. what wgrad_grouped
     returns; momentum: fp32 of the same shape, updated in place, or None. coeffs:
-    (a, b, c) of one step X <- a X + (b A + c A A) X, A = X X^T. Returns (or
-    fills) ``out``: bf16, the shape of grad.
+    (a, b, c) of one step X <- a X + (b A + c A A) X, A = X X^T; refused where the
+    iteration can leave the range of the products' operands. Returns (or fills)
+    ``out``: bf16, the shape of grad.
     """
     torch = _torch or _torch_module()
     device, st = _device_and_stream(grad, "grad", stream)
