@@ -124,6 +124,17 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """A new tensor of the stream that will write it (None: the current one). Allocated on another, it could share its
+    memory with work still queued there, and be given away after it is dropped while the kernel still writes."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _expect(t, dtype, name, device=True):
     import torch
 

@@ -1,6 +1,10 @@
 """Operators on the expert weights (argument marshalling only; see
 include/mxfp8_experts.h): the orthogonalised update of a stack of gradients
-and the whole expert layer for a few tokens."""
+and the whole expert layer for a few tokens.
+
+``stream``: the stream that runs the call (default: the current one). The inputs
+have to be ready there, and an output that the call allocates belongs to it:
+order its use on other streams as with any tensor of another stream."""
 from __future__ import annotations
 
 from . import _lib
@@ -78,7 +82,7 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if stream is None else _lib._empty(stream, x.shape, bf16, x.device)
     else:
         _check(out, bf16, (T, H), "out", device)
     if topk_ids is not None:
@@ -134,7 +138,7 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
         _check(momentum, torch.float32, shape, "momentum", device)
         momentum_p = momentum.data_ptr()
     if out is None:
-        out = torch.empty_like(grad, dtype=torch.bfloat16)
+        out = torch.empty_like(grad, dtype=torch.bfloat16) if stream is None else _lib._empty(stream, shape, torch.bfloat16, grad.device)
     else:
         _check(out, torch.bfloat16, shape, "out", device)
     a, b, c = coeffs
