@@ -166,7 +166,7 @@ def wgrad_grouped(A, sA, B, sB, offs, out=None, workspace=None, stream=None):
     if M2 != M or tuple(sA.shape) != (N, M // 32) or tuple(sB.shape) != (K, M // 32):
         raise ValueError("inconsistent operand / scale shapes")
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.bfloat16, device=A.device)
+        out = _empty(stream, (E, N, K), torch.bfloat16, A.device)
     _expect(out, torch.bfloat16, "out")
     if tuple(out.shape) != (E, N, K):
         raise ValueError(f"out must be [{E}, {N}, {K}]")
@@ -200,7 +200,7 @@ def grouped_gemm(X, sX, W, sW, offs, out=None, stream=None):
     if K2 != K or tuple(sX.shape) != (M, K // 32) or tuple(sW.shape) != (E, N, K // 32) or offs.numel() != E:
         raise ValueError("inconsistent operand / scale / offset shapes")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        out = _empty(stream, (M, N), torch.bfloat16, X.device)
     _expect(out, torch.bfloat16, "out")
     if tuple(out.shape) != (M, N):
         raise ValueError(f"out must be [{M}, {N}]")
@@ -257,9 +257,9 @@ def quantize_tokenwise(x, q=None, s=None, stream=None):
     _expect(x, torch.float32, "x")
     R, M = x.shape
     if q is None:
-        q = torch.empty((R, M), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (R, M), torch.uint8, x.device)
     if s is None:
-        s = torch.empty((R, M // 32), dtype=torch.uint8, device=x.device)
+        s = _empty(stream, (R, M // 32), torch.uint8, x.device)
     _expect(q, torch.uint8, "q")
     _expect(s, torch.uint8, "s")
     check(load().mxfp8_quantize_tokenwise(_ptr(x), R, M, _ptr(q), _ptr(s), _stream(stream)))
@@ -274,9 +274,9 @@ def quantize_transpose_bf16(x, q=None, s=None, stream=None):
     _expect(x, torch.bfloat16, "x")
     M, R = x.shape
     if q is None:
-        q = torch.empty((R, M), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (R, M), torch.uint8, x.device)
     if s is None:
-        s = torch.empty((R, M // 32), dtype=torch.uint8, device=x.device)
+        s = _empty(stream, (R, M // 32), torch.uint8, x.device)
     _expect(q, torch.uint8, "q")
     _expect(s, torch.uint8, "s")
     if tuple(q.shape) != (R, M) or tuple(s.shape) != (R, M // 32):
@@ -303,9 +303,9 @@ def quantize_transpose_bf16_sf(x, tile_rows, q=None, sf=None, s=None, stream=Non
     if nbytes == 0:
         raise ValueError(f"invalid sizes R={R}, M={M}, tile_rows={tile_rows}")
     if q is None:
-        q = torch.empty((R, M), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (R, M), torch.uint8, x.device)
     if sf is None:
-        sf = torch.empty((nbytes,), dtype=torch.uint8, device=x.device)
+        sf = _empty(stream, (nbytes,), torch.uint8, x.device)
     _expect(q, torch.uint8, "q")
     _expect(sf, torch.uint8, "sf")
     if s is not None:
@@ -336,7 +336,7 @@ def wgrad_grouped_sf(A, sfA, B, sfB, offs, kn, tn, out=None, stream=None):
     if M2 != M or sfA.numel() < sf_blocks_bytes(N, M, rows_a) or sfB.numel() < sf_blocks_bytes(K, M, rows_b):
         raise ValueError("inconsistent operand / scale-factor block sizes")
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.bfloat16, device=A.device)
+        out = _empty(stream, (E, N, K), torch.bfloat16, A.device)
     _expect(out, torch.bfloat16, "out")
     if tuple(out.shape) != (E, N, K):
         raise ValueError(f"out must be [{E}, {N}, {K}]")

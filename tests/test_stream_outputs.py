@@ -26,9 +26,16 @@ def calls(t):
     x16, x32 = t(bf, M, N), t(f32, N, M)
     x, router, w13, s13, w2, s2 = t(bf, T, K), t(bf, E, K), t(u8, E, 2 * N, K), t(u8, E, 2 * N, K // 32), t(u8, E, K, N), t(u8, E, K, N // 32)
     grad = t(bf, E, N, K)
+    sfA, sfB = t(u8, 4096), t(u8, 4096)  # (blocks of up to 4 tiles of 256 rows by one 128-token step)
     return {
         "moe_layer": lambda stream: [mx.moe_layer(x, router, w13, s13, w2, s2, 2, stream=stream)],
         "muon_update": lambda stream: [mx.muon_update(grad, stream=stream)],
+        "wgrad_grouped": lambda stream: [mx.wgrad_grouped(A, sA, B, sB, offs, stream=stream)],
+        "wgrad_grouped_sf": lambda stream: [mx.wgrad_grouped_sf(A, sfA, B, sfB, offs, 0, 64, stream=stream)],
+        "grouped_gemm": lambda stream: [mx.grouped_gemm(X, sX, W, sW, offs, stream=stream)],
+        "quantize_tokenwise": lambda stream: list(mx.quantize_tokenwise(x32, stream=stream)),
+        "quantize_transpose_bf16": lambda stream: list(mx.quantize_transpose_bf16(x16, stream=stream)),
+        "quantize_transpose_bf16_sf": lambda stream: list(mx.quantize_transpose_bf16_sf(x16, 64, stream=stream)[:2]),
     }
 
 
@@ -63,7 +70,7 @@ def test_outputs_are_allocated_under_the_given_stream(monkeypatch, name):
     def recorded(f):
         def g(*a, **kw):
             seen.append(current[0])
-            return f(*a, **kw)
+            return f(*a, **kw).as_subclass(Host)
         return g
 
     inputs = calls(lambda dtype, *shape: torch.zeros(shape, dtype=dtype).as_subclass(Host))
