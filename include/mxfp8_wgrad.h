@@ -96,7 +96,9 @@ extern "C" {
  * cache does not grow: a call needing more scratch than the stream already
  * holds returns MXFP8_ENOWS (with a message) and records nothing, so make the
  * same call once on that stream before capturing, or use
- * mxfp8_wgrad_grouped_ws.
+ * mxfp8_wgrad_grouped_ws. Scratch that a captured call was given is kept for
+ * good (the graph holds its address) and remains the stream's: replays of such
+ * a graph have to be ordered with the stream's other calls and with one another.
  */
 int mxfp8_wgrad_grouped(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB,
                         const int32_t* offs, int E, int N, int K, int64_t M, uint16_t* out,

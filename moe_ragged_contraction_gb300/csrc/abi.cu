@@ -8,9 +8,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "mxw_internal.h"
+#include "scratch_cache.h"
 #include "../../include/mxfp8_wgrad.h"
 
 // 1: the regular entry points also run each expert's K-steps on the global
@@ -159,60 +159,40 @@ int make_sf_map(CUtensorMap* map, const uint8_t* base, int64_t blocks, int box_b
     return MXFP8_OK;
 }
 
-// Scratch cache keyed by (device, stream). Growth frees the old block in
-// stream order and allocates the new one in stream order, so earlier calls
-// on the same stream finish with the old block first. While the stream is
-// being captured into a CUDA graph the cache neither grows nor frees (a
-// captured allocation would belong to the graph, and the cache would keep a
-// pointer the graph owns): a call that needs more scratch than the stream's
-// cached block fails with MXFP8_ENOWS before anything is recorded.
-struct WsEntry {
-    int dev;
-    cudaStream_t stream;
-    void* ptr;
-    size_t bytes;
+// Scratch from the per-(device, stream) cache, by stream-ordered allocation.
+struct StreamOrdered {
+    const char* what = "";
+    int allocate(void** p, size_t bytes, cudaStream_t s) {
+        what = "cudaMallocAsync (workspace)";
+        return cudaMallocAsync(p, bytes, s);
+    }
+    int release(void* p, cudaStream_t s) {
+        what = "cudaFreeAsync (workspace)";
+        return cudaFreeAsync(p, s);
+    }
 };
-std::vector<WsEntry> g_ws;
+mxw::ScratchCache<cudaStream_t, StreamOrdered> g_ws;
 
 int cached_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t ec = cudaStreamIsCapturing(stream, &cap);
     if (ec != cudaSuccess) return fail_cuda(ec, "cudaStreamIsCapturing");
-    std::lock_guard<std::mutex> lk(g_mu);
-    for (WsEntry& w : g_ws) {
-        if (w.dev == dev && w.stream == stream) {
-            if (w.bytes >= need) {
-                *out = w.ptr;
-                return MXFP8_OK;
-            }
-            break;
-        }
+    StreamOrdered alloc;
+    int e = 0;
+    mxw::Scratch r;
+    try {  // (the list of blocks may have to grow)
+        std::lock_guard<std::mutex> lk(g_mu);
+        r = g_ws.get(alloc, dev, stream, need, cap != cudaStreamCaptureStatusNone, out, &e);
+    } catch (...) {
+        return fail(MXFP8_ECUDA, "no host memory for the list of scratch blocks");
     }
-    if (cap != cudaStreamCaptureStatusNone)
+    if (r == mxw::Scratch::capturing)
         return fail(MXFP8_ENOWS,
                     "the stream is being captured and the scratch cached for it holds less than the %zu bytes this "
                     "call needs: pass a workspace (the _ws entry point) or make the same call once on this stream "
                     "before capturing",
                     need);
-    for (WsEntry& w : g_ws) {
-        if (w.dev == dev && w.stream == stream) {
-            cudaError_t e = cudaFreeAsync(w.ptr, stream);
-            if (e != cudaSuccess) return fail_cuda(e, "cudaFreeAsync (workspace)");
-            w.ptr = nullptr;
-            w.bytes = 0;
-            e = cudaMallocAsync(&w.ptr, need, stream);
-            if (e != cudaSuccess) return fail_cuda(e, "cudaMallocAsync (workspace)");
-            w.bytes = need;
-            *out = w.ptr;
-            return MXFP8_OK;
-        }
-    }
-    WsEntry w{dev, stream, nullptr, 0};
-    cudaError_t e = cudaMallocAsync(&w.ptr, need, stream);
-    if (e != cudaSuccess) return fail_cuda(e, "cudaMallocAsync (workspace)");
-    w.bytes = need;
-    g_ws.push_back(w);
-    *out = w.ptr;
+    if (r == mxw::Scratch::failed) return fail_cuda(static_cast<cudaError_t>(e), alloc.what);
     return MXFP8_OK;
 }
 
