@@ -119,7 +119,10 @@ size_t mxfp8_moe_layer_workspace_bytes(int T, int experts, int local, int H, int
  * result is within about 1.5e-3 (2-norm, relative) of the exact iteration
  * before its rounding to bf16. The output is bit-reproducible.
  *
- * Scratch as for mxfp8_moe_layer (cache, or the _ws form).
+ * Scratch as for mxfp8_moe_layer (cache, or the _ws form). Matrices with a
+ * shorter side up to 128 and a longer one up to 2048 stay on chip: nothing is
+ * taken from the cache (such a call can be captured on any stream), and the _ws
+ * form asks for a nominal 512 bytes that it does not touch.
  */
 int mxfp8_muon_update(const void* grad, int grad_type, float* momentum, int E, int N, int K, float mu, int nesterov,
                       int steps, float a, float b, float c, float eps, uint16_t* out, void* stream);

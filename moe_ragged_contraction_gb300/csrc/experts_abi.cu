@@ -70,6 +70,12 @@ bool muon_sizes(int E, int N, int K) {
     return E >= 0 && E <= MXFP8_MAX_EXPERTS && N >= 1 && N <= 32768 && K >= 1 && K <= 32768;
 }
 
+// Scratch of an update. Matrices that stay on chip need none: a nominal amount is
+// asked for, as 0 stands for invalid sizes.
+constexpr size_t MUON_SMALL_WS = 512;
+
+size_t muon_need(int E, int N, int K) { return mxw::muon_fits_small(N, K) ? MUON_SMALL_WS : mxw::muon_ws_bytes(E, N, K); }
+
 // Largest |k0 + k1 t + k2 t^2| on [0, T].
 double quadratic_max(double k0, double k1, double k2, double T) {
     double m = std::fmax(std::fabs(k0), std::fabs(k0 + (k1 + k2 * T) * T));
@@ -135,7 +141,8 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     if (!grad || !out) return host_fail(MXFP8_EINVAL, "null pointer argument");
     if (misaligned(grad, 16) || misaligned(momentum, 16) || misaligned(out, 16))
         return host_fail(MXFP8_EALIGN, "grad, momentum and out must be 16-byte aligned");
-    const size_t need = mxw::muon_ws_bytes(E, N, K);
+    const bool small = mxw::muon_fits_small(N, K);
+    const size_t need = muon_need(E, N, K);
     if (!use_cache) {
         if (!ws) return host_fail(MXFP8_EINVAL, "null workspace");
         if (misaligned(ws, 256)) return host_fail(MXFP8_EALIGN, "workspace must be 256-byte aligned");
@@ -145,7 +152,7 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     int rc = mxw::host_device(&a.dev, &a.num_sms);
     if (rc) return rc;
     a.stream = static_cast<cudaStream_t>(stream);
-    if (use_cache) {
+    if (use_cache && !small) {
         rc = mxw::host_workspace(a.dev, a.stream, need, &ws);
         if (rc) return rc;
     }
@@ -158,7 +165,7 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     a.stall = mxw::host_take_stall();
     const cudaError_t e = mxw::device_status_address(a.dev, &a.status);
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "device status: %s", cudaGetErrorString(e));
-    return mxw::muon_fits_small(N, K) ? mxw::launch_muon_small(a) : mxw::launch_muon(a);
+    return small ? mxw::launch_muon_small(a) : mxw::launch_muon(a);
 }
 
 }  // namespace
@@ -200,7 +207,7 @@ int mxfp8_muon_update_ws(const void* grad, int grad_type, float* momentum, int E
 
 size_t mxfp8_muon_update_workspace_bytes(int E, int N, int K) {
     if (!muon_sizes(E, N, K) || E < 1 || (K % 8) != 0) return 0;
-    return mxw::muon_ws_bytes(E, N, K);
+    return muon_need(E, N, K);
 }
 
 }  // extern "C"
