@@ -468,8 +468,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tc_commit_pair(bar_drain, 0x3);
         }
         __syncwarp();
-        if (lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
-        __syncwarp();
     } else if (warp == SCOUT) {
         // ------------------------------------------------ scout (both CTAs)
         // Waits, up to AHEAD tiles ahead, until the product before a tile's of the
@@ -721,6 +719,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
     }
+    // All MMAs have completed. Asked once the CTA's own tiles are through, so that
+    // the limit bounds what is left of the last one: in the pair's second CTA, whose
+    // issuer has nothing else to do, it would otherwise bound the whole call.
+    __syncthreads();
+    if (warp == 1 && lane == 0) drain_bar(bar_drain, 0, p.wait_ns, p.status);
+    __syncwarp();
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
