@@ -98,7 +98,8 @@ size_t mxfp8_moe_layer_workspace_bytes(int T, int experts, int local, int H, int
  * which drives the singular values of u towards one and keeps its singular
  * vectors. A zero matrix (an expert without tokens) gives exact zeros; a
  * matrix holding a NaN or an infinity, or whose sum of squares overflows
- * fp32, gives NaN and leaves the other matrices alone.
+ * fp32, gives NaN and leaves the other matrices alone. Small elements lose
+ * nothing: the norm is right down to the smallest subnormals.
  *
  *   grad     [E][N][K] bf16 (the output of mxfp8_wgrad_grouped) or fp32, 16-byte aligned
  *   momentum [E][N][K] fp32, 16-byte aligned, or NULL

@@ -45,6 +45,7 @@
 
 #include "mxw_experts.h"
 #include "mxw_internal.h"
+#include "muon_norm.cuh"
 #include "mxw_ptx_single.cuh"
 #include "../../include/mxfp8_experts.h"
 
@@ -119,29 +120,39 @@ __device__ __forceinline__ float4 load_u(const MuonArgs& a, size_t i) {
     return make_float4(fmaf(a.mu, m.x, g.x), fmaf(a.mu, m.y, g.y), fmaf(a.mu, m.z, g.z), fmaf(a.mu, m.w, g.w));
 }
 
-// One pass: momentum in place, a block's partial sum of u^2. HBM-bound: 10 bytes
+// One pass: momentum in place, a block's partial sums of u^2 and of (2^100 u)^2:
+// where the first has left fp32's normal range below, the second is exact (and
+// finite). HBM-bound: 10 bytes
 // an element with bf16 gradients, 35 us at 8 x 1408 x 2048 (6.6 TB/s). A block's
 // share is contiguous and the partial sums are joined in block order by
 // muon_scale: the same bits on every run.
-__global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* part, unsigned int* done, int n_done) {
+__global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float2* part, unsigned int* done, int n_done) {
     griddep_launch_dependents();
     griddep_wait();  // the gradient may come from the kernel before, and a call before may still use the scratch
     const size_t per = static_cast<size_t>(a.N) * a.K, base = blockIdx.y * per;
-    float s = 0.f;
+    float s = 0.f, t = 0.f;
     const size_t share = (per / 4 + NORM_BLOCKS - 1) / NORM_BLOCKS * 4, end = min(per, (blockIdx.x + 1) * share);
     for (size_t i = blockIdx.x * share + 4 * threadIdx.x; i < end; i += 4 * 256) {
         const float4 u = load_u<true>(a, base + i);
         s += (u.x * u.x + u.y * u.y) + (u.z * u.z + u.w * u.w);
+        const float4 v = make_float4(u.x * NORM_UP, u.y * NORM_UP, u.z * NORM_UP, u.w * NORM_UP);
+        t += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
     }
-    __shared__ float red[8];
+    __shared__ float2 red[8];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    for (int d = 16; d > 0; d >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+        t += __shfl_xor_sync(0xffffffffu, t, d);
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(s, t);
     __syncthreads();
     if (threadIdx.x == 0) {
-        s = 0.f;
-        for (int w = 0; w < 8; ++w) s += red[w];
-        part[blockIdx.y * NORM_BLOCKS + blockIdx.x] = s;
+        s = t = 0.f;
+        for (int w = 0; w < 8; ++w) {
+            s += red[w].x;
+            t += red[w].y;
+        }
+        part[blockIdx.y * NORM_BLOCKS + blockIdx.x] = make_float2(s, t);
     }
     for (int i = (blockIdx.y * NORM_BLOCKS + blockIdx.x) * 256 + threadIdx.x; i < n_done; i += gridDim.y * NORM_BLOCKS * 256)
         done[i] = 0;
@@ -151,23 +162,29 @@ __global__ void __launch_bounds__(256) muon_momentum(const MuonArgs a, float* pa
 // u is formed again from gradient and momentum (a third array of u would cost as
 // much to write as this saves). HBM-bound: 10 bytes an element, 41 us at
 // 8 x 1408 x 2048 (5.6 TB/s).
-__global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params p, const float* part) {
+__global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params p, const float2* part) {
     __shared__ float t[64][65];
-    __shared__ float s_inv;
+    __shared__ float2 s_norm;
     griddep_launch_dependents();
     griddep_wait();
     const int e = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
     if (threadIdx.x < 32) {
-        float s = 0.f;
+        float s = 0.f, up = 0.f;
 #pragma unroll
-        for (int i = 0; i < NORM_BLOCKS / 32; ++i) s += part[e * NORM_BLOCKS + 32 * i + threadIdx.x];
+        for (int i = 0; i < NORM_BLOCKS / 32; ++i) {
+            const float2 v = part[e * NORM_BLOCKS + 32 * i + threadIdx.x];
+            s += v.x;
+            up += v.y;
+        }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        // NaN where the sum is not finite: the whole matrix comes out as NaN
-        if (threadIdx.x == 0) s_inv = s <= 3.4028235e38f ? SX / (sqrtf(s) + a.eps) : __int_as_float(0x7fffffff);
+        for (int d = 16; d > 0; d >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+            up += __shfl_xor_sync(0xffffffffu, up, d);
+        }
+        if (threadIdx.x == 0) s_norm = norm_factors(s, up, a.eps, SX);
     }
     __syncthreads();
-    const float inv = s_inv;
+    const float pre = s_norm.x, inv = s_norm.y;  // X0 = (u pre) inv
     const size_t base = static_cast<size_t>(e) * a.N * a.K;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -175,8 +192,8 @@ __global__ void __launch_bounds__(256) muon_scale(const MuonArgs a, const Params
         float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < a.N && c < a.K) u = load_u<false>(a, base + static_cast<size_t>(r) * a.K + c);
         // eps = 0 and a zero matrix: 0 * inf would be NaN
-        const float v[4] = {u.x == 0.f && inv == inv ? 0.f : u.x * inv, u.y == 0.f && inv == inv ? 0.f : u.y * inv,
-                            u.z == 0.f && inv == inv ? 0.f : u.z * inv, u.w == 0.f && inv == inv ? 0.f : u.w * inv};
+        const float v[4] = {u.x == 0.f && inv == inv ? 0.f : u.x * pre * inv, u.y == 0.f && inv == inv ? 0.f : u.y * pre * inv,
+                            u.z == 0.f && inv == inv ? 0.f : u.z * pre * inv, u.w == 0.f && inv == inv ? 0.f : u.w * pre * inv};
         if (p.tall) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) t[4 * (threadIdx.x & 15) + j][(threadIdx.x >> 4) + 16 * k] = v[j];
@@ -774,7 +791,7 @@ void layout(int E, int N, int K, Layout* l) {
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
     const size_t e = E;
-    l->norm = take(4 * e * NORM_BLOCKS);
+    l->norm = take(sizeof(float2) * e * NORM_BLOCKS);
     l->done = take(4 * e * 3 * MXFP8_MUON_MAX_STEPS);  // (done and arrived: zeroed together)
     l->arrived = take(4 * e * l->sym * 2 * EPI_WARPS);
     l->part = take(l->parts > 1 ? 4 * e * l->sym * l->parts * TILE * l->tn : 0);
@@ -818,7 +835,7 @@ int launch_muon(const MuonArgs& a) {
     p.wait_ns = a.wait_limit_ns;
     p.status = a.status;
     p.stall = a.stall;
-    float* norm = reinterpret_cast<float*>(a.ws + l.norm);
+    float2* norm = reinterpret_cast<float2*>(a.ws + l.norm);
     const int zeroed = static_cast<int>((l.arrived - l.done) / 4 + static_cast<size_t>(a.E) * l.sym * 2 * EPI_WARPS);
     Maps maps;
     int rc = MXFP8_OK;
@@ -869,7 +886,7 @@ int launch_muon(const MuonArgs& a) {
     e = cudaLaunchKernelEx(&pre, muon_momentum, a, norm, p.done, zeroed);
     if (e == cudaSuccess) {
         pre.gridDim = dim3((a.K + 63) / 64, (a.N + 63) / 64, a.E);
-        e = cudaLaunchKernelEx(&pre, muon_scale, a, p, static_cast<const float*>(norm));
+        e = cudaLaunchKernelEx(&pre, muon_scale, a, p, static_cast<const float2*>(norm));
     }
     if (e != cudaSuccess) return host_fail(MXFP8_ECUDA, "update kernel: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     const int items = a.E * (p.full > p.sym * p.parts ? p.full : p.sym * p.parts);

@@ -30,6 +30,7 @@
 
 #include "mxw_experts.h"
 #include "mxw_internal.h"
+#include "muon_norm.cuh"
 #include "mxw_ptx_single.cuh"
 #include "../../include/mxfp8_experts.h"
 
@@ -46,7 +47,7 @@ constexpr float SX = 2048.f, SA = 4096.f;  // as in muon.cu
 // one) or A, R and the partial sums of A
 constexpr int OFF_A = MAXW / 64 * ATOM, OFF_R = OFF_A + 2 * ATOM, OFF_P = OFF_R + 2 * ATOM;
 constexpr int OFF_BAR = OFF_A + M * (MAXW + 1) * 4 > OFF_P + M * M * 4 ? OFF_A + M * (MAXW + 1) * 4 : OFF_P + M * M * 4;
-constexpr int SMEM = OFF_BAR + 256 + 1024;
+constexpr int SMEM = OFF_BAR + 256 + 1024;  // (barrier, TMEM base, 24 pairs of sums; alignment)
 constexpr int CH = 16;               // columns that a thread handles at a time (short code: its first pass misses the instruction cache)
 static_assert(SMEM <= 232448, "shared memory of a CTA");
 constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(M >> 4) << 24);  // kind::f16, fp16 x fp16 -> fp32, M = 128
@@ -103,8 +104,8 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float a, float b) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 struct Small {
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
     const int rank = p.C > 1 ? static_cast<int>(cluster_ctarank()) : 0, e = blockIdx.x / p.C;
     const uint32_t bar = sbase + OFF_BAR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_BAR + 8);
-    float* red = reinterpret_cast<float*>(smem + OFF_BAR + 32);   // [16] warps' sums of squares
-    float* norms = red + 16;                                       // [8] CTAs' sums
+    float2* red = reinterpret_cast<float2*>(smem + OFF_BAR + 32);  // [16] warps' sums of u^2 and (2^100 u)^2
+    float2* norms = red + 16;                                      // [8] CTAs' sums
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(bar, 1);
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
         for (int i = threadIdx.x; i < M * pitch; i += THREADS) u[i] = 0.f;
         __syncthreads();
     }
-    float sq = 0.f;
+    float sq = 0.f, up = 0.f;
     {
         // four neighbours along the gradient's rows: X's columns, or (tall) X's rows;
         // a warp per line, four lines' loads in flight (the momentum's stores
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
                         v[j] = p.a.nesterov ? axpy4(p.a.mu, mo[j], v[j]) : mo[j];
                     }
                     sq += (v[j].x * v[j].x + v[j].y * v[j].y) + (v[j].z * v[j].z + v[j].w * v[j].w);
+                    const float4 t = make_float4(v[j].x * NORM_UP, v[j].y * NORM_UP, v[j].z * NORM_UP, v[j].w * NORM_UP);
+                    up += (t.x * t.x + t.y * t.y) + (t.z * t.z + t.w * t.w);
                     float* d = p.tall ? u + 4 * g * pitch + l : u + l * pitch + 4 * g;
                     const int st = p.tall ? pitch : 1;
                     d[0] = v[j].x; d[st] = v[j].y; d[2 * st] = v[j].z; d[3 * st] = v[j].w;
@@ -191,26 +194,35 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
             }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
-    if (lane == 0) red[warp] = sq;
+    for (int d = 16; d > 0; d >>= 1) {
+        sq += __shfl_xor_sync(0xffffffffu, sq, d);
+        up += __shfl_xor_sync(0xffffffffu, up, d);
+    }
+    if (lane == 0) red[warp] = make_float2(sq, up);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (p.C > 1) cluster_sync_all();  // the other CTAs run: their shared memory may be written
     if (threadIdx.x < p.C) {
-        float s = 0.f;
-        for (int w = 0; w < THREADS / 32; ++w) s += red[w];
-        if (p.C > 1) st_cluster_f32(mapa_shared(smem_u32(norms + rank), threadIdx.x), s);
-        else norms[0] = s;
+        float s = 0.f, t = 0.f;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            s += red[w].x;
+            t += red[w].y;
+        }
+        if (p.C > 1) st_cluster_v2(mapa_shared(smem_u32(norms + rank), threadIdx.x), s, t);
+        else norms[0] = make_float2(s, t);
     }
     __syncwarp();
     if (p.C > 1) cluster_sync_all();
     else __syncthreads();
-    float total = 0.f;
-    for (int c = 0; c < p.C; ++c) total += norms[c];
-    // NaN where the sum is not finite: the whole matrix comes out as NaN
-    const float inv = total <= 3.4028235e38f ? SX / (sqrtf(total) + p.a.eps) : __int_as_float(0x7fffffff);
+    float total = 0.f, total_up = 0.f;
+    for (int c = 0; c < p.C; ++c) {
+        total += norms[c].x;
+        total_up += norms[c].y;
+    }
+    const float2 factors = norm_factors(total, total_up, p.a.eps, SX);
+    const float pre = factors.x, inv = factors.y;  // X0 = (u pre) inv
 
     const uint32_t tacc = tmem + (static_cast<uint32_t>(q4 * 32) << 16), tx = tacc + X_COL;
     const uint32_t row_at = row * 128, sw = row & 7;  // 16-byte piece k of the row in an atom: row_at + ((k ^ sw) << 4)
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const float v = u[row * pitch + c + i];
-            f[i] = v == 0.f && inv == inv ? 0.f : v * inv;  // (eps = 0 and a zero matrix: 0 * inf would be NaN)
+            f[i] = v == 0.f && inv == inv ? 0.f : v * pre * inv;  // (eps = 0 and a zero matrix: 0 * inf would be NaN)
             b[i] = __float_as_uint(f[i]);
         }
         tmem_st_x16(tx + c, b);
