@@ -4,7 +4,9 @@ and the whole expert layer for a few tokens.
 
 ``stream``: the stream that runs the call (default: the current one). The inputs
 have to be ready there, and an output that the call allocates belongs to it:
-order its use on other streams as with any tensor of another stream."""
+order its use on other streams as with any tensor of another stream. Neither
+operator has a backward pass: tensors that require a gradient are refused while
+gradients are being recorded."""
 from __future__ import annotations
 
 from . import _lib
@@ -27,13 +29,15 @@ def _torch_module():
 
 
 def _check(t, dtype, shape, name, device):
-    """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device."""
+    """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device, with no gradient to record."""
     if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
         _lib._expect(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, x or grad on cuda:{device}")
+    if t.requires_grad and _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this operator does not have: detach it or call under torch.no_grad()")
 
 
 def _device_and_stream(t, name, stream):
