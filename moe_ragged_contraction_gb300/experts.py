@@ -9,6 +9,8 @@ operator has a backward pass: tensors that require a gradient are refused while
 gradients are being recorded."""
 from __future__ import annotations
 
+from operator import index
+
 from . import _lib
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -40,6 +42,20 @@ def _check(t, dtype, shape, name, device):
         raise ValueError(f"{name} requires a gradient, which this operator does not have: detach it or call under torch.no_grad()")
 
 
+def _int32(v, name):
+    """v as an int that the library's 32-bit arguments hold (ctypes would take it modulo 2^32)."""
+    v = index(v)
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name}={v} is out of range")
+    return v
+
+
+def _sizes(*v):
+    """Sizes as 32-bit integers; None where one does not fit."""
+    v = [index(i) for i in v]
+    return v if all(-0x80000000 <= i <= 0x7fffffff for i in v) else None
+
+
 def _device_and_stream(t, name, stream):
     torch = _torch
     if not isinstance(t, torch.Tensor):
@@ -66,6 +82,7 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     """
     torch = _torch or _torch_module()
     device, st = _device_and_stream(x, "x", stream)
+    top_k, first_expert = _int32(top_k, "top_k"), _int32(first_expert, "first_expert")
     if x.dim() != 2 or w13.dim() != 3 or router.dim() != 2:
         raise ValueError("x must be [T, H], router [experts, H] and w13 [local, 2 I, H]")
     T, H = x.shape
@@ -111,7 +128,8 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
 
 def moe_layer_workspace_bytes(T: int, experts: int, local: int, H: int, I: int, top_k: int) -> int:
     """Scratch of one moe_layer call (0 if the sizes are invalid)."""
-    return int(_lib.load().mxfp8_moe_layer_workspace_bytes(T, experts, local, H, I, top_k))
+    v = _sizes(T, experts, local, H, I, top_k)
+    return int(_lib.load().mxfp8_moe_layer_workspace_bytes(*v)) if v else 0
 
 
 def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7,
@@ -126,6 +144,7 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
     """
     torch = _torch or _torch_module()
     device, st = _device_and_stream(grad, "grad", stream)
+    steps = _int32(steps, "steps")
     shape = grad.shape
     if len(shape) == 3:
         E, N, K = shape
@@ -161,4 +180,5 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
 
 def muon_update_workspace_bytes(E: int, N: int, K: int) -> int:
     """Scratch of one muon_update call (0 if the sizes are invalid)."""
-    return int(_lib.load().mxfp8_muon_update_workspace_bytes(E, N, K))
+    v = _sizes(E, N, K)
+    return int(_lib.load().mxfp8_muon_update_workspace_bytes(*v)) if v else 0

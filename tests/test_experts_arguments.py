@@ -71,3 +71,35 @@ def test_tensors_that_require_a_gradient(asked, call, name, value):
         call(**{name: v})
     call(**{name: v.detach()})
     assert len(asked) == 2
+
+
+BIG = 2 ** 32
+
+
+@pytest.mark.parametrize("call,kw", [
+    (layer, dict(top_k=BIG + 2)), (layer, dict(first_expert=BIG)), (layer, dict(top_k=2 - BIG)), (layer, dict(first_expert=-BIG)),
+    (update, dict(steps=BIG + 5)), (update, dict(steps=5 - BIG)),
+])
+def test_integers_beyond_32_bits(asked, call, kw):
+    with pytest.raises(ValueError):
+        call(**kw)
+    assert not asked
+
+
+def test_integers_of_other_kinds(asked):
+    layer(top_k=np.int64(2), first_expert=np.int32(0))
+    update(steps=np.int64(3))
+    assert len(asked) == 2
+    with pytest.raises(TypeError):
+        layer(top_k=2.0)
+    with pytest.raises(TypeError):
+        update(steps="5")
+
+
+def test_workspace_queries_beyond_32_bits():
+    mx.build()
+    assert mx.moe_layer_workspace_bytes(4, 8, 8, 64, 32, 2) > 0 and mx.muon_update_workspace_bytes(1, 136, 136) > 0
+    for bad in ((BIG + 4, 8, 8, 64, 32, 2), (4, 8, 8, 64, BIG + 32, 2), (4, 8, 8, 64, 32, BIG + 2)):
+        assert mx.moe_layer_workspace_bytes(*bad) == 0
+    for bad in ((BIG + 1, 136, 136), (1, BIG + 136, 136), (1, 136, 136 - BIG)):
+        assert mx.muon_update_workspace_bytes(*bad) == 0
