@@ -17,9 +17,14 @@
 // small singular value by a = 3.4, so that the error of the first steps grows
 // a hundredfold beside what it is to be compared with. The a X term therefore
 // takes X from two fp16 planes (22 bits); in R X only R's dominant directions
-// see the rounding of X. (Simulated in 64 bits on normal, heavy-tailed,
-// decaying and low-rank spectra: 0.4e-3 .. 1.6e-3 relative error, against
-// 3e-3 .. 27e-3 with one plane and 3e-3 .. 59e-3 in bf16.)
+// see the rounding of X. (Roundings simulated in 64 bits, five steps, on
+// normal, heavy-tailed, decaying and low-rank spectra with shorter sides of 96 and
+// more: 0.4e-3 .. 1.7e-3 relative error, against 3e-3 .. 27e-3 with one plane and
+// 3e-3 .. 59e-3 in bf16. Shorter sides of 8 .. 52: up to 4e-3. Sixteen steps: 5e-3
+// as a rule, 1e-2 .. 6e-2 where the map is steep at some singular values; the error
+// is about a thousand times that of the same iteration in fp32 throughout. The
+// shift in earlier steps too would amplify the noise of directions that u does
+// not have: rank 3, eight steps, 1.5e-3 -> 26e-3.)
 //
 // Kernels of a call: muon_momentum (momentum, partial sums of u^2), muon_scale
 // (X0 = u / norm into its two planes, transposed for tall matrices), muon_main:
