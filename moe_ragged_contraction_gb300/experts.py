@@ -31,15 +31,18 @@ def _torch_module():
 
 
 def _check(t, dtype, shape, name, device):
-    """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device, with no gradient to record."""
+    """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device."""
     if not (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
         _lib._expect(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, x or grad on cuda:{device}")
-    if t.requires_grad and _torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, which this operator does not have: detach it or call under torch.no_grad()")
+
+
+def _refuse_gradients(**tensors):
+    names = [name for name, t in tensors.items() if t is not None and t.requires_grad]
+    raise ValueError(f"{', '.join(names)} requires a gradient, which this operator does not have: detach it or call under torch.no_grad()")
 
 
 def _int32(v, name):
@@ -82,7 +85,8 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     """
     torch = _torch or _torch_module()
     device, st = _device_and_stream(x, "x", stream)
-    top_k, first_expert = _int32(top_k, "top_k"), _int32(first_expert, "first_expert")
+    if not (type(top_k) is int and type(first_expert) is int and 0 <= top_k < 1024 > first_expert >= 0):  # (the checks' cost counts at one token)
+        top_k, first_expert = _int32(top_k, "top_k"), _int32(first_expert, "first_expert")
     if x.dim() != 2 or w13.dim() != 3 or router.dim() != 2:
         raise ValueError("x must be [T, H], router [experts, H] and w13 [local, 2 I, H]")
     T, H = x.shape
@@ -112,6 +116,9 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     if topk_weights is not None:
         _check(topk_weights, f32, (T, top_k), "topk_weights", device)
         weights_p = topk_weights.data_ptr()
+    if (x.requires_grad or router.requires_grad or out.requires_grad or (bias is not None and bias.requires_grad)
+            or (topk_weights is not None and topk_weights.requires_grad)) and torch.is_grad_enabled():
+        _refuse_gradients(x=x, router=router, bias=bias, out=out, topk_weights=topk_weights)
     lib = _lib._lib or _lib.load()
     args = (x.data_ptr(), T, router.data_ptr(), bias_p, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
             experts, first_expert, local, H, I, top_k, _SCORES[score], 1 if renormalize else 0, scale, out.data_ptr(),
@@ -144,7 +151,8 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
     """
     torch = _torch or _torch_module()
     device, st = _device_and_stream(grad, "grad", stream)
-    steps = _int32(steps, "steps")
+    if type(steps) is not int or not 0 <= steps < 1024:
+        steps = _int32(steps, "steps")
     shape = grad.shape
     if len(shape) == 3:
         E, N, K = shape
@@ -164,6 +172,8 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
         out = torch.empty_like(grad, dtype=torch.bfloat16) if stream is None else _lib._empty(stream, shape, torch.bfloat16, grad.device)
     else:
         _check(out, torch.bfloat16, shape, "out", device)
+    if (grad.requires_grad or out.requires_grad or (momentum is not None and momentum.requires_grad)) and torch.is_grad_enabled():
+        _refuse_gradients(grad=grad, momentum=momentum, out=out)
     a, b, c = coeffs
     lib = _lib._lib or _lib.load()
     args = (grad.data_ptr(), 0 if dtype is torch.bfloat16 else 1, momentum_p, E, N, K, mu, 1 if nesterov else 0, steps,
