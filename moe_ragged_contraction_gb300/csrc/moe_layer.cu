@@ -34,8 +34,8 @@
 // Measured, bytes of the chosen experts' weights over the whole call's time:
 // 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 112 us
 // (5.1 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
-// token 53.5 MB in 29 to 33 us; 32 of 256 experts here, H = 7168, I = 2048,
-// top 8: 128 tokens 1.44 GB in 227 to 241 us, by box. A fixed chain of 15 to 16 us
+// token 53.5 MB in 33 us (28 on one box); 32 of 256 experts here, H = 7168, I = 2048,
+// top 8: 128 tokens 1.44 GB in 220 to 243 us. A fixed chain of 15 to 16 us
 // stands beside the stream: launches, routing (4 us at one token, 9 at 128),
 // lists, the hand-over of h, the last sum. Small layers are that chain alone
 // (H = 256: 15 us on the GPU, 17 with the host's launches).
@@ -62,7 +62,7 @@ constexpr int THREADS = 288;         // warps: 0 weight producer, 1 MMA issuer, 
 constexpr int LOADERS = 3;
 constexpr int BLOCK = 2;             // K-steps that a loader takes at a time (rings of 6 stages or more; else 1)
 constexpr int SMEM = 221184;         // leaves room beside a moe_logits<1, 2> block: moe_experts' CTAs start under it (all of
-                                     // it instead: 95.5 -> 99 us for 16 tokens of the 671B rank, equal from 64 tokens on)
+                                     // it instead: 92.4 -> 95.2 us for 16 tokens of the 671B rank, equal from 64 tokens on)
 constexpr uint32_t TMEM_ALL = 512;
 // the largest lists, masks and stages still leave a ring of a stage per loader (launch_moe lays them out)
 static_assert((SMEM - 1024 - (512 + MXFP8_MOE_MAX_TOKENS * MXFP8_MOE_MAX_TOPK * 10 + MXFP8_MOE_MAX_EXPERTS * 24 + 256 + 2 * 8 * TILE * 4 +
@@ -1072,8 +1072,8 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
     // blocks share them, each of their 8 warps at least one 32-column chunk. Tiles
     // of 32 x 32, which read x and the router half as often, where the small ones
     // are so many that they would get fewer slices (whole call, 32 x 32 / 16 x 16: H = 7168,
-    // 256 experts, 128 tokens 229 / 235 us, 32 tokens 151.4 / 147.7; H = 2048, 64
-    // experts, 64 tokens 122.0 / 119.8).
+    // 256 experts, 128 tokens 248 / 254 us, 32 tokens 157.6 / 155.0; H = 2048, 64
+    // experts, 64 tokens 111.6 / 110.2).
     auto tiles_of = [&](int mf, int nf) { return ((experts + 8 * nf - 1) / (8 * nf)) * ((T + 16 * mf - 1) / (16 * mf)); };
     constexpr int BLOCKS = 300, SLICES = 8;
     const bool wide = T > 16 && tiles_of(1, 2) > BLOCKS / SLICES;
@@ -1114,10 +1114,10 @@ void layout(int T, int experts, int local, int H, int I, int top_k, int sms, Lay
 // expected to meet fewer tiles than CTAs. Which experts are chosen is known on
 // the GPU only; here their number is taken as if all were equally likely, and
 // what is cut, if anything, is decided there (parts_of). H = 7168, I = 2048, 32
-// experts of 256, 1 / 2 / 4 tokens: 24.1 / 31.6 / 46.7 us in this form, 26.5 / 34.0 /
-// 47.8 without cuts; one expert of I = 128, 64 tokens: 59.9 / 79.8. Elsewhere
-// the cuts' code alone costs 1 to 4 us (H = 2048, I = 1408, 64 experts, 128 tokens:
-// 136.6 / 132.7).
+// experts of 256, 1 / 2 / 4 tokens: 19.0 / 24.2 / 52.9 us in this form, 18.8 / 27.2 /
+// 51.8 without cuts, by what the routing leaves here; one expert of I = 128, 64
+// tokens: 51.3 / 74.1. Elsewhere the cuts' code alone costs up to 5 us (H = 2048, I =
+// 1408, 64 experts, 128 tokens: 127.7 / 122.5).
 bool cuts(const MoeArgs& a, const Layout& l) {
     const long long pairs = static_cast<long long>(a.T) * a.top_k * a.local / a.experts;
     const long long chosen = pairs < 1 ? 1 : pairs < a.local ? pairs : a.local;

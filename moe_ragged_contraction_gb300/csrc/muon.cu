@@ -40,7 +40,7 @@
 // rate of the MMA use all of its 64 bytes a clock, and the epilogue's reads of
 // earlier products and planes compete with them (without an epilogue the
 // same list of products takes 330 us). 32 x 7168 x 2048: 13.7 ms for 15.8 TFLOP.
-// Few tiles, 3 x 331 x 1000: 114 us, a chain of 15 products of about 7 us each:
+// Few tiles, 3 x 331 x 1000: 113 us, a chain of 15 products of about 7 us each:
 // hand-over 1, first operands 0.85, products 1.75, epilogue 2.2, stores
 // and their report 1.3 to 2.
 #include <cuda_bf16.h>
@@ -771,10 +771,10 @@ void layout(int E, int N, int K, Layout* l) {
     l->ldn = (l->n + 63) & ~63;
     // Tiles of 128 columns up to 1 3/4 tiles of 256 a pair: each then takes half
     // the time to compute and store, which shortens the chain of products (5 steps,
-    // 256 / 128: 1 x 2048 x 1408, 48 tiles, 244 / 195 us; 4 x 1024 x 1024, 64, 202 / 167;
-    // 20 x 512 x 512, 80, 203 / 160; 1 x 2048 x 4096, 128, 379 / 365). With more, the wider
+    // 256 / 128: 1 x 2048 x 1408, 48 tiles, 249 / 198 us; 4 x 1024 x 1024, 64, 202 / 164;
+    // 20 x 512 x 512, 80, 200 / 157; 1 x 2048 x 4096, 128, 383 / 368). With more, the wider
     // ones win: they need three quarters of the operand bytes for the same products
-    // (1 x 3000 x 3000, 144, 566 / 635; 4 x 1408 x 2048, 192, 322 / 358).
+    // (1 x 3000 x 3000, 144, 569 / 640; 4 x 1408 x 2048, 192, 322 / 358).
     l->T = (l->m + TILE - 1) / TILE;
     l->tn = 4LL * E * l->T * ((l->n + TILE - 1) / TILE) <= 7 * PAIRS ? TILE / 2 : TILE;
     const int Tm = (l->m + l->tn - 1) / l->tn, ksteps = (l->n + KSTEP - 1) / KSTEP;
@@ -783,8 +783,8 @@ void layout(int E, int N, int K, Layout* l) {
     for (int i = 0; i < l->T; ++i) l->sym += Tm < (i + 1) * (TILE / l->tn) ? Tm : (i + 1) * (TILE / l->tn);
     // The contraction of X X^T in pieces of sixteen K-steps or more where its tiles
     // occupy less than half of the pairs: the piece that ends last adds them up in
-    // order (1 x 129 x 7032 290 -> 166 us; pieces of eight K-steps cost more to
-    // join than they save, 3 x 331 x 1000 129 -> 146 us).
+    // order (1 x 129 x 7032 188 -> 142 us; pieces of eight K-steps cost more to
+    // join than they save, 3 x 331 x 1000 115 -> 127 us).
     const long long tiles = static_cast<long long>(E) * l->sym;
     l->parts = 1;
     if (2 * tiles <= PAIRS) {

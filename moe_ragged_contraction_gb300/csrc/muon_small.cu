@@ -18,7 +18,7 @@
 // the two transposes of tall matrices happen on the way in and out. The same
 // scaling and shift beta as in the general kernel.
 //
-// Bound by the latency of the chain: 4 x 128 x 256, five steps, 30 us, 6.6 of
+// Bound by the latency of the chain: 4 x 128 x 256, five steps, 31 us, 6.6 of
 // them to load and normalise and 3.6 to 3.8 a step (three products of 0.3 us,
 // the accumulator's way through registers into shared memory after each). 512
 // threads on 16 columns at a time: with 32 columns unrolled in each of 256
@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(THREADS, 1) muon_small(const Small p) {
 
 }  // namespace
 
-// Every matrix that fits goes this way (5 steps, us here / general kernel):
-// 4 x 128 x 256 30 / 104, 64 x 120 x 120 21 / 117, 256 x 128 x 256 58 / 316,
-// 20 x 64 x 1000 59 / 147, and with the largest cluster 1 x 128 x 2048
-// 65 / 126, 32 x 128 x 2048 201 / 260, 128 x 128 x 2048 661 / 706.
+// Every matrix that fits goes this way (5 steps, momentum, us here / general
+// kernel): 4 x 128 x 256 31 / 87, 64 x 120 x 120 24 / 115, 256 x 128 x 256 73 / 337,
+// 20 x 64 x 1000 64 / 130, and with the largest cluster 1 x 128 x 2048
+// 67 / 117, 32 x 128 x 2048 222 / 253; the two meet where many large ones queue for
+// the SMs (128 x 128 x 2048 683 / 665, without momentum 622 / 622).
 bool muon_fits_small(int N, int K) {
     const int m = N < K ? N : K, n = N < K ? K : N;
     return m <= M && n <= MAXC * MAXW;
