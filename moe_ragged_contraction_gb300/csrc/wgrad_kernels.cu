@@ -1048,7 +1048,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MAIN_THREADS, 1)
                 default: mma_issue<4>(p, ctx); break;
             }
         }
-        if (lane == 0) drain_phase(bar_drain, 0, p.wait_ns);
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------ stage watcher (leader only)
@@ -1355,7 +1354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MAIN_THREADS, 1)
     }
 
     // both CTAs stay resident until the pair's MMAs, copies and TMEM reads are
-    // done, then free the pair's TMEM together
+    // done, then free the pair's TMEM together. The wait for the last MMA begins
+    // when the CTA's own tiles are through: in the second CTA, whose warp 1 issues
+    // nothing, its limit would otherwise bound the whole call.
+    __syncthreads();
+    if (warp == 1 && lane == 0) drain_phase(bar_drain, 0, p.wait_ns);
+    __syncwarp();
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
