@@ -34,3 +34,16 @@ from .experts import (  # noqa: F401
     muon_update,
     muon_update_workspace_bytes,
 )
+from .step import (  # noqa: F401
+    TokenPlan,
+    clip_grads,
+    grad_norm,
+    grad_workspace_bytes,
+    token_combine,
+    token_combine_grad,
+    token_dispatch,
+    token_dispatch_grad,
+    token_dispatch_mxfp8,
+    token_plan,
+    token_plan_rows,
+)

@@ -27,6 +27,8 @@ DEV_OFFS_UNSORTED = 1
 DEV_OFFS_RANGE = 2
 DEV_OFFS_ALIGN = 4
 DEV_WAIT_TIMEOUT = 8
+DEV_TOKENS_ROWS = 16
+DEV_TOKENS_RANGE = 32
 
 
 class Mxfp8Error(RuntimeError):
@@ -102,6 +104,32 @@ def load() -> ctypes.CDLL:
         lib.mxfp8_muon_update_ws.restype = I
         lib.mxfp8_muon_update_workspace_bytes.argtypes = [I] * 3
         lib.mxfp8_muon_update_workspace_bytes.restype = Z
+        lib.mxfp8_token_plan.argtypes = [P, I, L, I, I, I, I, L, P, P, P, P]
+        lib.mxfp8_token_plan.restype = I
+        lib.mxfp8_token_plan_rows.argtypes = [L, I, I, I]
+        lib.mxfp8_token_plan_rows.restype = L
+        lib.mxfp8_token_dispatch.argtypes = [P, L, I, I, P, P, L, P, P]
+        lib.mxfp8_token_dispatch.restype = I
+        lib.mxfp8_token_dispatch_mxfp8.argtypes = [P, L, I, I, P, P, L, P, P, P]
+        lib.mxfp8_token_dispatch_mxfp8.restype = I
+        lib.mxfp8_token_dispatch_grad.argtypes = [P, L, L, I, I, P, P, P]
+        lib.mxfp8_token_dispatch_grad.restype = I
+        lib.mxfp8_token_combine.argtypes = [P, L, P, L, I, I, P, P, P]
+        lib.mxfp8_token_combine.restype = I
+        lib.mxfp8_token_combine_grad.argtypes = [P, P, P, L, I, I, P, P, L, P, P, P]
+        lib.mxfp8_token_combine_grad.restype = I
+        norm = [P, P, P, I, P]
+        lib.mxfp8_grad_norm.argtypes = norm + [P]
+        lib.mxfp8_grad_norm.restype = I
+        lib.mxfp8_grad_norm_ws.argtypes = norm + [P, Z, P]
+        lib.mxfp8_grad_norm_ws.restype = I
+        clip = [P, P, P, I, F, F, P, P, P]
+        lib.mxfp8_clip_grads.argtypes = clip + [P]
+        lib.mxfp8_clip_grads.restype = I
+        lib.mxfp8_clip_grads_ws.argtypes = clip + [P, Z, P]
+        lib.mxfp8_clip_grads_ws.restype = I
+        lib.mxfp8_grad_workspace_bytes.argtypes = [I]
+        lib.mxfp8_grad_workspace_bytes.restype = Z
         _lib = lib
         return lib
 
