@@ -12,6 +12,7 @@ struct TokenPlanArgs {
     int id64, top_k, first, local, align;
     int64_t pairs, rows;
     int32_t *offs, *slot, *src;
+    int dev;
     int* status;
     cudaStream_t stream;
 };

@@ -33,6 +33,9 @@ int token_args(mxw::TokenArgs& a, int64_t T, int64_t rows, int H, int top_k, int
     if (!routing(T, top_k)) return bad_routing(T, top_k);
     if (rows < 0 || rows > MAX_ROWS) return host_fail(MXFP8_EINVAL, "rows=%lld out of range", static_cast<long long>(rows));
     if (H < 1 || H > MAX_H) return host_fail(MXFP8_EINVAL, "H=%d out of range [1, %d]", H, MAX_H);
+    if (T > (MAX_ELEMENTS >> 2) / H || rows > (MAX_ELEMENTS >> 2) / H)
+        return host_fail(MXFP8_EINVAL, "T=%lld or rows=%lld of H=%d columns are more than any device holds", static_cast<long long>(T),
+                         static_cast<long long>(rows), H);
     if (H % unit) return host_fail(unit == 32 ? MXFP8_EINVAL : MXFP8_EALIGN, "H=%d must be a multiple of %d", H, unit);
     if ((T && !slot) || (needs_src && rows && !src)) return host_fail(MXFP8_EINVAL, "null plan");
     if (misaligned(slot, 4) || misaligned(src, 4)) return host_fail(MXFP8_EALIGN, "slot and src must be 4-byte aligned");
@@ -48,11 +51,10 @@ int buffer(const void* p, int64_t n, uintptr_t align, const char* name) {
     return MXFP8_OK;
 }
 
-int device(int* sms, int** status) {
-    int dev;
-    const int rc = mxw::host_device(&dev, sms);
+int device(int* dev, int* sms, int** status) {
+    const int rc = mxw::host_device(dev, sms);
     if (rc) return rc;
-    const cudaError_t e = mxw::device_status_address(dev, status);
+    const cudaError_t e = mxw::device_status_address(*dev, status);
     return e == cudaSuccess ? MXFP8_OK : host_fail(MXFP8_ECUDA, "device status: %s", cudaGetErrorString(e));
 }
 
@@ -159,7 +161,7 @@ int mxfp8_token_plan(const void* ids, int id_type, int64_t T, int top_k, int fir
     if (!rc) rc = buffer(src, rows, 4, "src");
     int sms;
     mxw::TokenPlanArgs a{};
-    if (!rc) rc = device(&sms, &a.status);
+    if (!rc) rc = device(&a.dev, &sms, &a.status);
     if (rc) return rc;
     a.ids = ids; a.id64 = id_type == MXFP8_ID_I64; a.top_k = top_k; a.first = first; a.local = local; a.align = align;
     a.pairs = T * top_k; a.rows = rows; a.offs = offs; a.slot = slot; a.src = src;
@@ -170,10 +172,11 @@ int mxfp8_token_plan(const void* ids, int id_type, int64_t T, int top_k, int fir
 int mxfp8_token_dispatch(const uint16_t* x, int64_t T, int H, int top_k, const int32_t* slot, const int32_t* src,
                          int64_t rows, uint16_t* out, void* stream) {
     mxw::TokenArgs a{};
+    int dev;
     int rc = token_args(a, T, rows, H, top_k, 8, slot, src, true, stream);
     if (!rc) rc = buffer(x, T, 16, "x");
     if (!rc) rc = buffer(out, rows, 16, "out");
-    if (!rc) rc = device(&a.num_sms, &a.status);
+    if (!rc) rc = device(&dev, &a.num_sms, &a.status);
     if (rc) return rc;
     a.tok_in = x; a.sorted_out = out;
     return mxw::launch_token_dispatch(a);
@@ -182,11 +185,12 @@ int mxfp8_token_dispatch(const uint16_t* x, int64_t T, int H, int top_k, const i
 int mxfp8_token_dispatch_mxfp8(const uint16_t* x, int64_t T, int H, int top_k, const int32_t* slot, const int32_t* src,
                                int64_t rows, uint8_t* q, uint8_t* s, void* stream) {
     mxw::TokenArgs a{};
+    int dev;
     int rc = token_args(a, T, rows, H, top_k, 32, slot, src, true, stream);
     if (!rc) rc = buffer(x, T, 16, "x");
     if (!rc) rc = buffer(q, rows, 16, "q");
     if (!rc) rc = buffer(s, rows, 1, "s");
-    if (!rc) rc = device(&a.num_sms, &a.status);
+    if (!rc) rc = device(&dev, &a.num_sms, &a.status);
     if (rc || rows == 0) return rc;
     a.tok_in = x; a.q = q; a.s = s;
     return mxw::launch_token_dispatch(a);
@@ -195,10 +199,11 @@ int mxfp8_token_dispatch_mxfp8(const uint16_t* x, int64_t T, int H, int top_k, c
 int mxfp8_token_dispatch_grad(const uint16_t* dxs, int64_t rows, int64_t T, int H, int top_k, const int32_t* slot,
                               uint16_t* dx, void* stream) {
     mxw::TokenArgs a{};
+    int dev;
     int rc = token_args(a, T, rows, H, top_k, 8, slot, nullptr, false, stream);
     if (!rc) rc = buffer(dxs, rows, 16, "dxs");
     if (!rc) rc = buffer(dx, T, 16, "dx");
-    if (!rc) rc = device(&a.num_sms, &a.status);
+    if (!rc) rc = device(&dev, &a.num_sms, &a.status);
     if (rc) return rc;
     a.sorted_in = dxs; a.tok_out = dx;
     return mxw::launch_token_combine(a);
@@ -207,11 +212,12 @@ int mxfp8_token_dispatch_grad(const uint16_t* dxs, int64_t rows, int64_t T, int 
 int mxfp8_token_combine(const uint16_t* y, int64_t rows, const float* weights, int64_t T, int H, int top_k,
                         const int32_t* slot, uint16_t* out, void* stream) {
     mxw::TokenArgs a{};
+    int dev;
     int rc = token_args(a, T, rows, H, top_k, 8, slot, nullptr, false, stream);
     if (!rc) rc = buffer(y, rows, 16, "y");
     if (!rc) rc = buffer(weights, T, 4, "weights");
     if (!rc) rc = buffer(out, T, 16, "out");
-    if (!rc) rc = device(&a.num_sms, &a.status);
+    if (!rc) rc = device(&dev, &a.num_sms, &a.status);
     if (rc || T == 0) return rc;
     a.sorted_in = y; a.weights = weights; a.tok_out = out;
     return mxw::launch_token_combine(a);
@@ -221,13 +227,14 @@ int mxfp8_token_combine_grad(const uint16_t* dout, const uint16_t* y, const floa
                              const int32_t* slot, const int32_t* src, int64_t rows, uint16_t* dy, float* dweights,
                              void* stream) {
     mxw::TokenArgs a{};
+    int dev;
     int rc = token_args(a, T, rows, H, top_k, 8, slot, src, true, stream);
     if (!rc) rc = buffer(dout, T, 16, "dout");
     if (!rc) rc = buffer(y, rows, 16, "y");
     if (!rc) rc = buffer(weights, T, 4, "weights");
     if (!rc) rc = buffer(dy, rows, 16, "dy");
     if (!rc) rc = buffer(dweights, T, 4, "dweights");
-    if (!rc) rc = device(&a.num_sms, &a.status);
+    if (!rc) rc = device(&dev, &a.num_sms, &a.status);
     if (rc) return rc;
     a.tok_in = dout; a.sorted_in = y; a.weights = weights; a.sorted_out = dy; a.dweights = dweights;
     return mxw::launch_token_combine_grad(a);

@@ -3,6 +3,8 @@
 // sum back in token order, and the gradients of both.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "mxw_internal.h"
 #include "mxw_ptx.cuh"
 #include "mxw_quant.cuh"
@@ -14,12 +16,32 @@ namespace {
 
 constexpr uint32_t FULL = 0xffffffffu;
 
-// 16 bytes that are read once. (No ld.global.nc in these kernels: they start
-// before the kernel that writes their inputs has ended, and that path is for
-// data that does not change while a kernel runs.)
-__device__ __forceinline__ uint4 load16(const void* p) {
+// 16 bytes that are read once; zeros and no access unless `there` (no branch:
+// loads of a group leave together). No ld.global.nc in these kernels: they start
+// before the kernel that writes their inputs has ended, and that path is for data
+// that does not change while a kernel runs.
+__device__ __forceinline__ uint4 load16_if(bool there, const void* p) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<uint32_t>(there))
+        : "memory");
+    return v;
+}
+
+// The same through L1, for what neighbouring warps read too.
+__device__ __forceinline__ uint4 load16_l1_if(bool there, const void* p) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<uint32_t>(there))
+        : "memory");
     return v;
 }
 
@@ -31,12 +53,13 @@ __device__ __forceinline__ uint4 load16(const void* p) {
 // the CTAs' counts become starting rows, and every warp walks its run again and
 // hands out rows. match.any gives each lane its place among the lanes with the
 // same expert.
-constexpr int PLAN_MAX_CTAS = 8;
-constexpr int PLAN_SMEM = 200 * 1024;
+constexpr int PLAN_MAX_CTAS = 16;
+constexpr int PLAN_SMEM = 224 * 1024;
+constexpr int PLAN_ONE_CTA = 2048;  // pairs that one CTA sorts
 
 struct PlanPar {
     const void* ids;
-    int pairs, first, local, align, rows;
+    int pairs, first, local, align, rows, groups;
     int32_t *offs, *slot, *src;
     int* status;
 };
@@ -56,12 +79,44 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The local expert of a pair, or -1.
+// A warp works on RUN pairs at a time; their experts and ranks stay in shared memory.
+constexpr int RUN = 512, LOADS = RUN / 32;
+
+// Writes the local experts (or -1) of the pairs at .. hi (RUN at most) to `kept`,
+// with all loads in flight together.
 template <class Id>
-__device__ __forceinline__ int pair_expert(const Id* ids, int p, int hi, int first, int local) {
-    if (p >= hi) return -1;
-    const long long e = static_cast<long long>(ids[p]) - first;
-    return e >= 0 && e < local ? static_cast<int>(e) : -1;
+__device__ __forceinline__ void load_run(const Id* ids, int at, int hi, int first, int local, int lane, int* kept) {
+    Id v[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) v[i] = at + 32 * i + lane < hi ? ids[at + 32 * i + lane] : Id(-1);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const long long d = static_cast<long long>(v[i]) - first;
+        kept[32 * i + lane] = v[i] >= 0 && d >= 0 && d < local ? static_cast<int>(d) : -1;
+    }
+}
+
+// Lanes whose e (below 2^(3 groups), or -1) is this lane's.
+__device__ __forceinline__ uint32_t same_expert(int e, int groups) {
+    uint32_t m = __ballot_sync(FULL, e >= 0);
+    if (__popc(m) <= 8) return __match_any_sync(FULL, e);
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g, e >>= 3) {
+#pragma unroll
+        for (int b = 0; b < 3; ++b) m &= ~(__ballot_sync(FULL, e & (1 << b)) ^ static_cast<uint32_t>((e << (31 - b)) >> 31));
+    }
+    return m;  // (nothing that is used where e is -1)
+}
+
+// The place of each lane's pair among the warp's pairs of its expert so far,
+// counted on in `count`.
+__device__ __forceinline__ int rank_of(int e, int groups, int lane, int* count) {
+    const uint32_t same = same_expert(e, groups);
+    const int before = e >= 0 ? count[e] : 0;
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(same) - 1) count[e] = before + __popc(same);
+    __syncwarp();
+    return before + __popc(same & ((1u << lane) - 1));
 }
 
 template <class Id>
@@ -71,8 +126,12 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
     int* hist = sm;                      // [warps][local]
     int* mine = sm + warps * p.local;    // [local] this CTA's pairs, read by the others
     int* base = mine + p.local;          // [local] first row of the CTA's pairs
-    int* ends = base + p.local;          // [local] rows up to the group's end
-    __shared__ int part[32];
+    int* full = base + p.local;          // [local] end of the group's pairs
+    int* ends = full + p.local;          // [local] end of the group
+    int* own = ends + p.local;           // [local] start of the expert's pairs among the CTA's, by expert
+    int* kept = own + p.local + warp * RUN;
+    uint16_t* sorted = reinterpret_cast<uint16_t*>(own + p.local + warps * RUN);  // [warps * RUN] the CTA's pairs by expert
+    __shared__ int2 part[32];
     const int C = gridDim.x, c = blockIdx.x;  // (the grid is one cluster)
     for (int i = threadIdx.x; i < warps * p.local; i += blockDim.x) hist[i] = 0;
     griddep_launch_dependents();
@@ -81,93 +140,136 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
 
     const Id* ids = static_cast<const Id*>(p.ids);
     const int per = ((p.pairs + C * warps - 1) / (C * warps) + 31) & ~31;
-    const int lo = min(static_cast<long long>(p.pairs), static_cast<long long>(c * warps + warp) * per);
+    const int lo = static_cast<int>(min(static_cast<long long>(p.pairs), static_cast<long long>(c * warps + warp) * per));
     const int hi = min(p.pairs, lo + per);
+    const bool once = per <= RUN;  // the first pass's ranks serve the second
     int* count = hist + warp * p.local;
-    for (int at = lo; at < hi; at += 32) {
-        const int e = pair_expert(ids, at + lane, hi, p.first, p.local);
-        const uint32_t same = __match_any_sync(FULL, e);
-        if (e >= 0 && lane == __ffs(same) - 1) count[e] += __popc(same);
-        __syncwarp();
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.local; e += blockDim.x) {
-        int run = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int n = hist[w * p.local + e];
-            hist[w * p.local + e] = run;
-            run += n;
+    // pass 0 counts, pass 1 gives out rows; rolled, so that the code is short: every
+    // line of it misses the instruction cache once
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int at = lo; at < hi; at += RUN) {
+            const int n = min(RUN, hi - at);
+            if (pass == 1 && once) {
+#pragma unroll 1
+                for (int k = lane; k < n; k += 32) {
+                    const int v = kept[k], e = v & 2047;
+                    int row = -1;
+                    if (v >= 0) {
+                        const int place = count[e] + (v >> 11);
+                        sorted[own[e] + place] = static_cast<uint16_t>(warp * per + k);
+                        row = base[e] + place;
+                        if (row >= p.rows) row = -1;
+                    }
+                    p.slot[at + k] = row;
+                }
+                continue;
+            }
+            load_run(ids, at, hi, p.first, p.local, lane, kept);
+            __syncwarp();
+            if (!once && pass == 0) {
+#pragma unroll 1
+                for (int k = lane; k < n; k += 32)
+                    if (kept[k] >= 0) atomicAdd(count + kept[k], 1);  // (counts only: the order does not matter)
+                continue;
+            }
+#pragma unroll 1
+            for (int k = lane; k - lane < n; k += 32) {
+                const int e = kept[k], rank = rank_of(e, p.groups, lane, count);
+                if (once) {
+                    if (e >= 0) kept[k] = rank << 11 | e;  // (rank < 512, local <= 2048)
+                } else if (k < n) {
+                    int row = e >= 0 ? base[e] + rank : -1;
+                    if (row >= p.rows) row = -1;
+                    if (row >= 0) p.src[row] = at + k;
+                    p.slot[at + k] = row;
+                }
+            }
         }
-        mine[e] = run;
-    }
-    cluster_arrive();
-    cluster_wait();
-    // experts in runs of `each` a thread: totals over the CTAs, then a scan of the padded sizes
-    const int each = (p.local + blockDim.x - 1) / blockDim.x;
-    const int e0 = min(p.local, static_cast<int>(threadIdx.x) * each), e1 = min(p.local, e0 + each);
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) {
-        int total = 0, before = 0;
-        for (int r = 0; r < C; ++r) {
-            const int n = ld_cluster(cluster_map(smem_u32(mine + e), r));
-            if (r < c) before += n;
-            total += n;
-        }
-        base[e] = before;
-        ends[e] = total;
-        sum += (total + p.align - 1) / p.align * p.align;
-    }
-    cluster_arrive();  // (no CTA leaves before the others have read its counts: waited for at the end)
-    int incl = sum;
+        if (pass == 1) break;
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.local; e += blockDim.x) {
+            int run = 0;
+#pragma unroll 1
+            for (int w = 0; w < warps; w += 8) {
+                int n[8];
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int v = __shfl_up_sync(FULL, incl, d);
-        if (lane >= d) incl += v;
-    }
-    if (lane == 31) part[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        const int own = lane < warps ? part[lane] : 0;
-        int v = own;
+                for (int i = 0; i < 8; ++i) n[i] = hist[(w + i) * p.local + e];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    hist[(w + i) * p.local + e] = run;
+                    run += n[i];
+                }
+            }
+            mine[e] = run;
+        }
+        cluster_arrive();
+        cluster_wait();
+        // experts in runs of `each` a thread: totals over the CTAs, then a scan of the padded sizes
+        const int each = (p.local + blockDim.x - 1) / blockDim.x;
+        const int e0 = min(p.local, static_cast<int>(threadIdx.x) * each), e1 = min(p.local, e0 + each);
+        int sum = 0, here = 0;
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            int n[PLAN_MAX_CTAS], total = 0, before = 0;
+#pragma unroll
+            for (int r = 0; r < PLAN_MAX_CTAS; ++r) n[r] = r < C ? ld_cluster(cluster_map(smem_u32(mine + e), r)) : 0;
+#pragma unroll
+            for (int r = 0; r < PLAN_MAX_CTAS; ++r) {
+                if (r < c) before += n[r];
+                total += n[r];
+            }
+            base[e] = before;
+            full[e] = total;
+            sum += (total + p.align - 1) / p.align * p.align;
+            here += mine[e];
+        }
+        cluster_arrive();  // (no CTA leaves before the others have read its counts: waited for at the end)
+        int2 incl = make_int2(sum, here);
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int u = __shfl_up_sync(FULL, v, d);
-            if (lane >= d) v += u;
+            const int x = __shfl_up_sync(FULL, incl.x, d), y = __shfl_up_sync(FULL, incl.y, d);
+            if (lane >= d) {
+                incl.x += x;
+                incl.y += y;
+            }
         }
-        part[lane] = v - own;
-    }
-    __syncthreads();
-    int row = part[warp] + incl - sum;
-    for (int e = e0; e < e1; ++e) {
-        const int total = ends[e], end = row + (total + p.align - 1) / p.align * p.align;
-        if (c == 0) p.offs[e] = min(end, p.rows);
-        base[e] += row;
-        ends[e] = end;
-        // the group's padding, shared among the CTAs by expert
-        if (e % C == c)
-            for (int r = row + total; r < min(end, p.rows); ++r) p.src[r] = -1;
-        row = end;
-    }
-    __syncthreads();
-    bool dropped = false;
-    for (int at = lo; at < hi; at += 32) {
-        const int e = pair_expert(ids, at + lane, hi, p.first, p.local);
-        const uint32_t same = __match_any_sync(FULL, e);
-        int r = -1;
-        if (e >= 0) r = base[e] + count[e] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(same) - 1) count[e] += __popc(same);
-        __syncwarp();
-        if (r >= p.rows) {
-            r = -1;
-            dropped = true;
+        if (lane == 31) part[warp] = incl;
+        __syncthreads();
+        int row = incl.x - sum, at = incl.y - here;
+        for (int w = 0; w < warp && e0 < p.local; ++w) {
+            row += part[w].x;
+            at += part[w].y;
         }
-        if (at + lane < hi) p.slot[at + lane] = r;
-        if (r >= 0) p.src[r] = at + lane;
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            const int total = full[e], end = row + (total + p.align - 1) / p.align * p.align;
+            if (c == 0) p.offs[e] = min(end, p.rows);
+            base[e] += row;
+            full[e] = row + total;
+            ends[e] = end;
+            own[e] = at;
+            row = end;
+            at += mine[e];
+        }
+        __syncthreads();
     }
-    if (__any_sync(FULL, dropped) && lane == 0) atomicOr(p.status, MXFP8_DEV_TOKENS_ROWS);
-    const int last = ends[p.local - 1];
-    for (long long r = last + static_cast<long long>(c) * blockDim.x + threadIdx.x; r < p.rows; r += C * blockDim.x)
+    if (once) {
+        // src by expert: a warp's stores are neighbours
+        __syncthreads();
+        const int first = c * warps * per;
+#pragma unroll 1
+        for (int e = warp; e < p.local; e += warps)
+            for (int i = lane; i < min(mine[e], p.rows - base[e]); i += 32) p.src[base[e] + i] = first + sorted[own[e] + i];
+    }
+    if (c == 0)
+        for (int e = threadIdx.x; e < p.local; e += blockDim.x)
+            if (full[e] > p.rows) atomicOr(p.status, MXFP8_DEV_TOKENS_ROWS);  // (that many pairs were dropped)
+    // padding: a warp an expert, and the rows behind the last group
+    for (int e = c * warps + warp; e < p.local; e += C * warps)
+        for (int r = full[e] + lane; r < min(ends[e], p.rows); r += 32) p.src[r] = -1;
+    for (long long r = ends[p.local - 1] + static_cast<long long>(c) * blockDim.x + threadIdx.x; r < p.rows; r += C * blockDim.x)
         p.src[r] = -1;
     cluster_wait();
 }
@@ -175,11 +277,13 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
 // ------------------------------------------------------------------ rows
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int PAD_ROWS = 8;  // rows of the sorted buffers that a warp looks at for padding
+constexpr int UNITS_ENOUGH = 20000, UNITS_ENOUGH_MXFP8 = 5000, PAD_CTAS = 4096;
 
 struct RowPar {
     int64_t T, rows;
-    int H, k, segs;
+    int H, k, seg, segs;  // seg: columns of a unit
+    int words;            // rows of scales are whole aligned words
+    int pad, pad_ctas;    // zero_padding's rows, and its CTAs
     const int32_t *slot, *src;
     const uint16_t *tok_in, *sorted_in;
     uint16_t *tok_out, *sorted_out;
@@ -216,16 +320,27 @@ __device__ __forceinline__ float2 bf16x2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// Bits of the warp's PAD_ROWS rows from r0 on that are padding.
-__device__ __forceinline__ uint32_t padding_rows(const RowPar& p, int64_t r0, int lane) {
-    bool pad = false;
-    if (lane < PAD_ROWS && r0 + lane < p.rows) pad = checked(p.src[r0 + lane], p.T * p.k, p.status) < 0;
-    return __ballot_sync(FULL, pad);
-}
+// Warps that share a row of padding: each writes some 2 KB of it.
+__host__ __device__ inline int pad_parts(int bytes) { return bytes <= 2048 ? 1 : bytes <= 4096 ? 2 : bytes <= 8192 ? 4 : 8; }
 
-__device__ __forceinline__ void zero_row(void* row, int bytes, int lane) {
-    for (int b = lane * 16; b < bytes; b += 512)
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(row) + b) = make_uint4(0, 0, 0, 0);
+// Zeros on the padding among the `cta`th p.pad * (WARPS / parts) rows (of `bytes`,
+// and of scales): a CTA's work, p.pad rows for each `parts` warps.
+__device__ __forceinline__ void zero_padding(const RowPar& p, uint32_t cta, int lane, uint8_t* out, int bytes, uint8_t* scales, int blocks) {
+    const int parts = pad_parts(bytes), warp = threadIdx.x >> 5, part = (warp & (parts - 1)) * 32 + lane;
+    const int64_t r0 = (static_cast<int64_t>(cta) * (WARPS / parts) + warp / parts) * p.pad;
+    bool pad = false;
+    if (lane < p.pad && r0 + lane < p.rows) pad = checked(p.src[r0 + lane], p.T * p.k, p.status) < 0;
+#pragma unroll 1
+    for (uint32_t rows = __ballot_sync(FULL, pad); rows; rows &= rows - 1) {
+        const int64_t r = r0 + __ffs(rows) - 1;
+        uint8_t* row = out + r * bytes;
+#pragma unroll 4
+        for (int b = part * 16; b < bytes; b += parts * 512) *reinterpret_cast<uint4*>(row + b) = make_uint4(0, 0, 0, 0);
+        if (p.words)
+            for (int b = 4 * part; b < blocks; b += parts * 128) *reinterpret_cast<uint32_t*>(scales + r * blocks + b) = 0;
+        else
+            for (int b = part; b < blocks; b += parts * 32) scales[r * blocks + b] = 0;
+    }
 }
 
 // Each token's columns are read once and written to all of its rows.
@@ -235,224 +350,361 @@ __global__ void __launch_bounds__(THREADS) dispatch_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t tokens = p.T * p.segs, units = tokens + (p.rows + PAD_ROWS - 1) / PAD_ROWS;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * WARPS) {
-        if (u >= tokens) {
-            const int64_t r0 = (u - tokens) * PAD_ROWS;
-            for (uint32_t pad = padding_rows(p, r0, lane); pad; pad &= pad - 1)
-                zero_row(p.sorted_out + (r0 + __ffs(pad) - 1) * p.H, 2 * p.H, lane);
+    const uint32_t tokens = static_cast<uint32_t>(p.T) * p.segs, first_pad = (tokens + WARPS - 1) / WARPS;
+    const uint32_t ctas = first_pad + p.pad_ctas;
+    for (uint32_t cta = blockIdx.x; cta < ctas; cta += gridDim.x) {
+        if (cta >= first_pad) {
+            zero_padding(p, cta - first_pad, lane, reinterpret_cast<uint8_t*>(p.sorted_out), 2 * p.H, nullptr, 0);
             continue;
         }
-        const int64_t t = u / p.segs;
-        const int col = static_cast<int>(u - t * p.segs) * SEG + lane * 8;
+        const uint32_t u = cta * WARPS + (threadIdx.x >> 5);
+        if (u >= tokens) continue;
+        const int64_t t = u / static_cast<uint32_t>(p.segs);
+        const int seg = static_cast<int>(u - static_cast<uint32_t>(t) * p.segs) * p.seg, end = min(p.H, seg + p.seg);
         const Slots s = token_slots(p, t, lane);
         if (!(s.has_lo | s.has_hi)) continue;
-        uint4 v[SEG / 256];
-#pragma unroll
-        for (int i = 0; i < SEG / 256; ++i)
-            if (col + 256 * i < p.H) v[i] = load16(p.tok_in + t * p.H + col + 256 * i);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-            for (uint32_t has = half ? s.has_hi : s.has_lo; has; has &= has - 1) {
-                const int64_t r = __shfl_sync(FULL, half ? s.hi : s.lo, __ffs(has) - 1);
+        for (int c = seg; c < end; c += SEG) {  // (the same for all lanes)
+            const int col = c + lane * 8;
+            uint4 v[SEG / 256];
 #pragma unroll
-                for (int i = 0; i < SEG / 256; ++i)
-                    if (col + 256 * i < p.H) *reinterpret_cast<uint4*>(p.sorted_out + r * p.H + col + 256 * i) = v[i];
-            }
+            for (int i = 0; i < SEG / 256; ++i) v[i] = load16_if(col + 256 * i < end, p.tok_in + t * p.H + col + 256 * i);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+                for (uint32_t has = half ? s.has_hi : s.has_lo; has; has &= has - 1) {
+                    const int64_t r = __shfl_sync(FULL, half ? s.hi : s.lo, __ffs(has) - 1);
+                    uint16_t* out = p.sorted_out + r * p.H + col;
+#pragma unroll
+                    for (int i = 0; i < SEG / 256; ++i)
+                        if (col + 256 * i < end) *reinterpret_cast<uint4*>(out + 256 * i) = v[i];
+                }
+        }
     }
 }
 
-// 16 columns a lane: two neighbouring lanes hold a block of 32.
-constexpr int QSEG = 512;
+// 16 columns a lane in each of QRUNS runs of 512: two neighbouring lanes hold a block of 32.
+constexpr int QRUNS = 4;
+constexpr int QSEG = 512 * QRUNS;
 
-__global__ void __launch_bounds__(THREADS) dispatch_mxfp8_kernel(const RowPar p) {
+__device__ __forceinline__ void quantise16(const uint4& a, const uint4& b, uint4& q, uint32_t& sb) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
+    amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
+    if (amax >= 0x7f800000u) {  // NaN or infinity in the block
+        q = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+        sb = 0xFF;
+        return;
+    }
+    const int e = block_exponent(amax);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = bf16x2(w[2 * i]), y = bf16x2(w[2 * i + 1]);
+        const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x * inv, x.y * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(y.x * inv, y.y * inv), __NV_SATFINITE, __NV_E4M3);
+        o[i] = l | (h << 16);
+    }
+    q = make_uint4(o[0], o[1], o[2], o[3]);
+    sb = e + 127;
+}
+
+__global__ void __launch_bounds__(THREADS, 4) dispatch_mxfp8_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t tokens = p.T * p.segs, units = tokens + (p.rows + PAD_ROWS - 1) / PAD_ROWS;
+    const uint32_t tokens = static_cast<uint32_t>(p.T) * p.segs, first_pad = (tokens + WARPS - 1) / WARPS;
     const int blocks = p.H / 32;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * WARPS) {
-        if (u >= tokens) {
-            const int64_t r0 = (u - tokens) * PAD_ROWS;
-            for (uint32_t pad = padding_rows(p, r0, lane); pad; pad &= pad - 1) {
-                const int64_t r = r0 + __ffs(pad) - 1;
-                zero_row(p.q + r * p.H, p.H, lane);
-                for (int b = lane; b < blocks; b += 32) p.s[r * blocks + b] = 0;
-            }
+    const uint32_t ctas = first_pad + p.pad_ctas;
+    for (uint32_t cta = blockIdx.x; cta < ctas; cta += gridDim.x) {
+        if (cta >= first_pad) {
+            zero_padding(p, cta - first_pad, lane, p.q, p.H, p.s, blocks);
             continue;
         }
-        const int64_t t = u / p.segs;
-        const int col = static_cast<int>(u - t * p.segs) * QSEG + lane * 16;
+        const uint32_t u = cta * WARPS + (threadIdx.x >> 5);
+        if (u >= tokens) continue;
+        const int64_t t = u / static_cast<uint32_t>(p.segs);
+        const int seg = static_cast<int>(u - static_cast<uint32_t>(t) * p.segs) * p.seg, end = min(p.H, seg + p.seg);
         const Slots sl = token_slots(p, t, lane);
         if (!(sl.has_lo | sl.has_hi)) continue;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (col < p.H) {
-            a = load16(p.tok_in + t * p.H + col);
-            b = load16(p.tok_in + t * p.H + col + 8);
-        }
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
-        amax = max(amax, __shfl_xor_sync(FULL, amax, 1));
-        uint4 q;
-        uint8_t sb;
-        if (amax >= 0x7f800000u) {  // NaN or infinity in the block
-            q = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-            sb = 0xFF;
-        } else {
-            const int e = block_exponent(amax);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = bf16x2(w[2 * i]), y = bf16x2(w[2 * i + 1]);
-                const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x.x * inv, x.y * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(y.x * inv, y.y * inv), __NV_SATFINITE, __NV_E4M3);
-                o[i] = l | (h << 16);
-            }
-            q = make_uint4(o[0], o[1], o[2], o[3]);
-            sb = static_cast<uint8_t>(e + 127);
-        }
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half)
-            for (uint32_t has = half ? sl.has_hi : sl.has_lo; has; has &= has - 1) {
-                const int64_t r = __shfl_sync(FULL, half ? sl.hi : sl.lo, __ffs(has) - 1);
-                if (col < p.H) {
-                    *reinterpret_cast<uint4*>(p.q + r * p.H + col) = q;
-                    if (!(lane & 1)) p.s[r * blocks + (col >> 5)] = sb;
+        for (int c = seg; c < end; c += QSEG) {  // (the same for all lanes)
+            const int col = c + lane * 16;
+            uint4 v[QRUNS][2], q[QRUNS];
+#pragma unroll
+            for (int i = 0; i < QRUNS; ++i) {
+                v[i][0] = load16_if(col + 512 * i < end, p.tok_in + t * p.H + col + 512 * i);
+                v[i][1] = load16_if(col + 512 * i < end, p.tok_in + t * p.H + col + 512 * i + 8);
+            }
+            uint32_t mine = 0, word = 0;
+#pragma unroll
+            for (int i = 0; i < QRUNS; ++i) {
+                uint32_t sb;
+                quantise16(v[i][0], v[i][1], q[i], sb);
+                mine |= sb << (8 * i);
+            }
+            // lanes 0 .. 15: the scales of four neighbouring blocks (run lane / 4, lanes 8 (lane % 4) + 0, 2, 4, 6)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) word |= ((__shfl_sync(FULL, mine, 8 * (lane & 3) + 2 * m) >> (8 * (lane >> 2 & 3))) & 0xff) << (8 * m);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half)
+#pragma unroll 1
+                for (uint32_t has = half ? sl.has_hi : sl.has_lo; has; has &= has - 1) {
+                    const int64_t r = __shfl_sync(FULL, half ? sl.hi : sl.lo, __ffs(has) - 1);
+                    uint8_t* out = p.q + r * p.H + col;
+                    uint8_t* scales = p.s + r * blocks + c / 32;
+#pragma unroll
+                    for (int i = 0; i < QRUNS; ++i)
+                        if (col + 512 * i < end) *reinterpret_cast<uint4*>(out + 512 * i) = q[i];
+                    if (p.words) {
+                        if (lane < 4 * QRUNS && c + 128 * lane < end) *reinterpret_cast<uint32_t*>(scales + 4 * lane) = word;
+                    } else if (!(lane & 1)) {
+#pragma unroll
+                        for (int i = 0; i < QRUNS; ++i)
+                            if (col + 512 * i < end) scales[16 * i + lane / 2] = static_cast<uint8_t>(mine >> (8 * i));
+                    }
                 }
+        }
+    }
+}
+
+__device__ __forceinline__ void words(const uint4& v, uint32_t (&w)[4]) {
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+}
+
+// Rows and weights of the next G choices of a token that have a row: the lowest
+// set bits of `has`, which are taken from it.
+template <int G>
+struct Group {
+    int row[G];
+    float w[G];      // 0 where there is none
+    int choice[G];   // -1 where there is none
+};
+
+template <int G, bool WEIGHTED>
+__device__ __forceinline__ Group<G> next_group(uint32_t& has, int slot, float w) {
+    Group<G> g;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        const int from = __ffs(has) - 1;
+        has &= has - 1;
+        g.choice[j] = from;
+        g.row[j] = __shfl_sync(FULL, slot, from & 31);
+        const float v = WEIGHTED ? __shfl_sync(FULL, w, from & 31) : 1.f;
+        g.w[j] = from >= 0 ? v : 0.f;
+    }
+    return g;
+}
+
+// acc += w * row over a group's rows, 8 columns a lane at col + 256 u
+template <int G, int U, bool WEIGHTED>
+__device__ __forceinline__ void add_rows(const RowPar& p, const Group<G>& g, int col, int end, float (&acc)[U][8]) {
+    uint4 v[G][U];
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[j][u] = load16_if(g.choice[j] >= 0 && col + 256 * u < end, p.sorted_in + static_cast<int64_t>(g.row[j]) * p.H + col + 256 * u);
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            uint32_t x[4];
+            words(v[j][u], x);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 f = bf16x2(x[m]);
+                acc[u][2 * m] = WEIGHTED ? fmaf(g.w[j], f.x, acc[u][2 * m]) : acc[u][2 * m] + f.x;
+                acc[u][2 * m + 1] = WEIGHTED ? fmaf(g.w[j], f.y, acc[u][2 * m + 1]) : acc[u][2 * m + 1] + f.y;
+            }
+        }
+}
+
+// The sum of a token's rows over the columns of a unit, G rows of U vectors in flight.
+
+template <int G, int U, bool WEIGHTED>
+__device__ __forceinline__ void combine_token(const RowPar& p, int64_t t, int seg, int lane, const Slots& s, float w_lo, float w_hi) {
+    const int end = min(p.H, seg + p.seg);
+#pragma unroll 1
+    for (int c0 = seg; c0 < end; c0 += 256 * U) {  // (the same for all lanes: they exchange slots)
+        const int c = c0 + lane * 8;
+        float acc[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) acc[u][m] = 0.f;
+        for (uint32_t has = s.has_lo; has;) add_rows<G, U, WEIGHTED>(p, next_group<G, WEIGHTED>(has, s.lo, w_lo), c, end, acc);
+        for (uint32_t has = s.has_hi; has;) add_rows<G, U, WEIGHTED>(p, next_group<G, WEIGHTED>(has, s.hi, w_hi), c, end, acc);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + 256 * u < end) {
+                uint32_t o[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[m] = pack_bf16x2(__float_as_uint(acc[u][2 * m]), __float_as_uint(acc[u][2 * m + 1]));
+                *reinterpret_cast<uint4*>(p.tok_out + t * p.H + c + 256 * u) = make_uint4(o[0], o[1], o[2], o[3]);
             }
     }
 }
 
-// The weighted sum of a token's rows: 8 columns a lane, two runs of 256 columns a
-// warp, the rows in ascending order of the choice.
-constexpr int CSEG = 512;
+// A token with one row or none: 8 vectors in flight, no sums to keep.
+template <bool WEIGHTED>
+__device__ __forceinline__ void combine_one(const RowPar& p, int64_t t, int seg, int lane, const Slots& s, float w_lo, float w_hi) {
+    const int end = min(p.H, seg + p.seg), from = __ffs(s.has_lo | s.has_hi) - 1;
+    const bool some = from >= 0;
+    const int64_t row = __shfl_sync(FULL, s.has_lo ? s.lo : s.hi, from & 31);
+    const float w = WEIGHTED ? __shfl_sync(FULL, s.has_lo ? w_lo : w_hi, from & 31) : 1.f;
+    const uint16_t* in = p.sorted_in + (some ? row * p.H : 0);
+    uint16_t* out = p.tok_out + t * p.H;
+#pragma unroll 1
+    for (int c = seg + lane * 8; c < end; c += 256 * 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = load16_if(some && c + 256 * u < end, in + c + 256 * u);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (c + 256 * u < end) {
+                uint32_t x[4];
+                words(v[u], x);
+                // 0 + w x, as in the sums of more rows (where it turns a product of -0 into 0)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 f = bf16x2(x[m]);
+                    x[m] = pack_bf16x2(__float_as_uint(fmaf(w, f.x, 0.f)), __float_as_uint(fmaf(w, f.y, 0.f)));
+                }
+                *reinterpret_cast<uint4*>(out + c + 256 * u) = some ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0, 0, 0, 0);
+            }
+    }
+}
 
 template <bool WEIGHTED>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const RowPar p) {
+__global__ void __launch_bounds__(THREADS, 4) combine_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t units = p.T * p.segs;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * WARPS) {
-        const int64_t t = u / p.segs;
-        const int col = static_cast<int>(u - t * p.segs) * CSEG + lane * 8;
+    const uint32_t units = static_cast<uint32_t>(p.T) * p.segs;
+    for (uint32_t u = blockIdx.x * WARPS + (threadIdx.x >> 5); u < units; u += gridDim.x * WARPS) {
+        const int64_t t = u / static_cast<uint32_t>(p.segs);
+        const int seg = static_cast<int>(u - static_cast<uint32_t>(t) * p.segs) * p.seg;
         const Slots s = token_slots(p, t, lane);
         float w_lo = 1.f, w_hi = 1.f;
         if (WEIGHTED) {
             if (lane < p.k) w_lo = p.w[t * p.k + lane];
             if (lane + 32 < p.k) w_hi = p.w[t * p.k + lane + 32];
         }
-        float acc[2][8];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i / 8][i % 8] = 0.f;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-            uint32_t has = half ? s.has_hi : s.has_lo;
-            while (has) {
-                // four rows' loads in flight
-                uint4 v[4][2];
-                float w[4];
-                bool there[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    there[j] = has != 0;
-                    const int from = there[j] ? __ffs(has) - 1 : 0;
-                    has &= has - 1;
-                    const int64_t r = __shfl_sync(FULL, half ? s.hi : s.lo, from);
-                    w[j] = __shfl_sync(FULL, half ? w_hi : w_lo, from);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (there[j] && col + 256 * i < p.H)
-                            v[j][i] = load16(p.sorted_in + r * p.H + col + 256 * i);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (there[j]) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t x[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const float2 f = bf16x2(x[m]);
-                                if (WEIGHTED) {
-                                    acc[i][2 * m] = fmaf(w[j], f.x, acc[i][2 * m]);
-                                    acc[i][2 * m + 1] = fmaf(w[j], f.y, acc[i][2 * m + 1]);
-                                } else {
-                                    acc[i][2 * m] += f.x;
-                                    acc[i][2 * m + 1] += f.y;
-                                }
-                            }
-                        }
-                    }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (col + 256 * i < p.H) {
-                uint32_t o[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) o[m] = pack_bf16x2(__float_as_uint(acc[i][2 * m]), __float_as_uint(acc[i][2 * m + 1]));
-                *reinterpret_cast<uint4*>(p.tok_out + t * p.H + col + 256 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+        const int n = __popc(s.has_lo) + __popc(s.has_hi);
+        if (n <= 1) combine_one<WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
+        else if (n <= 3) combine_token<3, 2, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
+        else if (n <= 6) combine_token<6, 1, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
+        else combine_token<8, 1, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
     }
 }
 
-// A warp a pair: its row of y against the token's row of dout, and the weighted
-// row of dout in y's place. The warps of a CTA hold neighbouring pairs, so that a
-// token's row of dout comes from memory once.
-__global__ void __launch_bounds__(THREADS) combine_grad_kernel(const RowPar p) {
-    const int lane = threadIdx.x & 31;
+// A pair's row of y against the token's row of dout, and the weighted row of dout
+// to the pair's row of dy; this thread's part of the product.
+template <int GRAD_VECS>
+__device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t row, int from, int step) {
+    const float w = p.w[pair];
+    const uint16_t* d = p.tok_in + static_cast<int64_t>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.k)) * p.H;
+    const int64_t off = row * p.H;
+    float dot = 0.f;
+#pragma unroll 1
+    for (int c = from; c < p.H; c += step * GRAD_VECS) {
+        uint4 a[GRAD_VECS], b[GRAD_VECS];
+#pragma unroll
+        for (int v = 0; v < GRAD_VECS; ++v) {
+            b[v] = load16_if(c + step * v < p.H, p.sorted_in + off + c + step * v);
+            a[v] = load16_l1_if(c + step * v < p.H, d + c + step * v);
+        }
+#pragma unroll
+        for (int v = 0; v < GRAD_VECS; ++v) {
+            uint32_t x[4], y[4], o[4];
+            words(a[v], x);
+            words(b[v], y);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 f = bf16x2(x[m]), q = bf16x2(y[m]);
+                dot = fmaf(f.x, q.x, dot);
+                dot = fmaf(f.y, q.y, dot);
+                o[m] = pack_bf16x2(__float_as_uint(w * f.x), __float_as_uint(w * f.y));
+            }
+            // (dy may be y: every row has one owner, which has read these columns)
+            if (c + step * v < p.H) *reinterpret_cast<uint4*>(p.sorted_out + off + c + step * v) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+#pragma unroll
+    for (int v = 16; v; v /= 2) dot += __shfl_xor_sync(FULL, dot, v);
+    return dot;
+}
+
+// The gradient of the weighted sum. How a CTA's warps take pairs:
+//   LIST   it lists those of PAIRS neighbouring pairs that have a row, a warp takes
+//          one at a time (one rank of several: most pairs have none)
+//   WARP   a warp a pair
+//   TEAM   all warps one pair, for so few that latency counts
+// Neighbouring pairs share their token's row of dout in L1.
+// (16-byte loads of each of the two rows in flight a thread: 8 in LIST, where two
+// CTAs an SM are enough, else 4.)
+enum Share { LIST, WARP, TEAM };
+constexpr int PAIRS = 64;
+
+template <Share SHARE>
+__global__ void __launch_bounds__(THREADS, SHARE == LIST ? 2 : 4) combine_grad_kernel(const RowPar p) {
+    constexpr int PER = SHARE == LIST ? PAIRS : SHARE == WARP ? WARPS : 1;  // pairs of a CTA at a time
+    __shared__ int list[PAIRS], rows[PAIRS], counts[2];
+    __shared__ float sums[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t pairs = p.T * p.k, units = pairs + (p.rows + PAD_ROWS - 1) / PAD_ROWS;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units;
-         u += static_cast<int64_t>(gridDim.x) * WARPS) {
-        if (u >= pairs) {
-            const int64_t r0 = (u - pairs) * PAD_ROWS;
-            for (uint32_t pad = padding_rows(p, r0, lane); pad; pad &= pad - 1)
-                zero_row(p.sorted_out + (r0 + __ffs(pad) - 1) * p.H, 2 * p.H, lane);
+    const int64_t pairs = p.T * p.k;
+    const uint32_t lists = static_cast<uint32_t>((pairs + PER - 1) / PER),
+                   units = lists + p.pad_ctas;
+    for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+        if (u >= lists) {
+            zero_padding(p, u - lists, lane, reinterpret_cast<uint8_t*>(p.sorted_out), 2 * p.H, nullptr, 0);
             continue;
         }
-        const int64_t r = checked(p.slot[u], p.rows, p.status);
-        float dot = 0.f;
-        if (r >= 0) {
-            const float w = p.w[u];
-            const uint16_t* d = p.tok_in + u / p.k * p.H;
-            const uint16_t* y = p.sorted_in + r * p.H;
-            uint16_t* dy = p.sorted_out + r * p.H;
-            for (int c0 = lane * 8; c0 < p.H; c0 += 1024) {
-                uint4 a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + 256 * i < p.H) {
-                        a[i] = *reinterpret_cast<const uint4*>(d + c0 + 256 * i);
-                        b[i] = *reinterpret_cast<const uint4*>(y + c0 + 256 * i);  // (dy may be y)
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + 256 * i < p.H) {
-                        const uint32_t av[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bv[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float2 f = bf16x2(av[m]), g = bf16x2(bv[m]);
-                            dot = fmaf(f.x, g.x, dot);
-                            dot = fmaf(f.y, g.y, dot);
-                            o[m] = pack_bf16x2(__float_as_uint(w * f.x), __float_as_uint(w * f.y));
-                        }
-                        *reinterpret_cast<uint4*>(dy + c0 + 256 * i) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+        const int64_t first = static_cast<int64_t>(u) * PER;
+        if (SHARE == LIST) {
+            __syncthreads();  // (the list before is done with)
+            int r = -1, at = 0;
+            if (threadIdx.x < PAIRS) {
+                if (first + threadIdx.x < pairs) {
+                    r = checked(p.slot[first + threadIdx.x], p.rows, p.status);
+                    if (r < 0) p.dw[first + threadIdx.x] = 0.f;
+                }
+                const uint32_t has = __ballot_sync(FULL, r >= 0);
+                at = __popc(has & ((1u << lane) - 1));
+                if (lane == 0) counts[warp] = __popc(has);
             }
-        }
+            __syncthreads();
+            if (r >= 0) {
+                if (warp) at += counts[0];
+                list[at] = threadIdx.x;
+                rows[at] = r;
+            }
+            __syncthreads();
+            for (int i = warp; i < counts[0] + counts[1]; i += WARPS) {
+                const float dot = grad_row<8>(p, first + list[i], rows[i], lane * 8, 256);
+                if (lane == 0) p.dw[first + list[i]] = dot;
+            }
+        } else {
+            const int64_t pair = first + (SHARE == WARP ? warp : 0);
+            if (pair >= pairs) continue;
+            const int r = checked(p.slot[pair], p.rows, p.status);
+            float dot = r >= 0 ? grad_row<4>(p, pair, r, (SHARE == WARP ? lane : threadIdx.x) * 8, SHARE == WARP ? 256 : 8 * THREADS) : 0.f;
+            if (SHARE == TEAM) {
+                __syncthreads();  // (the sums of the pair before have been read)
+                if (lane == 0) sums[warp] = dot;
+                __syncthreads();
+                dot = 0.f;
 #pragma unroll
-        for (int d = 16; d; d /= 2) dot += __shfl_xor_sync(FULL, dot, d);
-        if (lane == 0) p.dw[u] = dot;
+                for (int v = 0; v < WARPS; ++v) dot += sums[v];
+            }
+            if (SHARE == WARP ? lane == 0 : threadIdx.x == 0) p.dw[pair] = dot;
+        }
     }
 }
 
@@ -462,12 +714,11 @@ int failed(cudaError_t e, const char* what) {
 
 // Launches `kernel` so that its start overlaps the end of the kernel before it
 // (each kernel waits for that one before its first access).
-template <class Par>
-int launch(void (*kernel)(Par), const Par& p, int64_t units, const TokenArgs& a, const char* what) {
-    const int64_t blocks = (units + WARPS - 1) / WARPS;
-    if (blocks == 0) return MXFP8_OK;
+template <class... Par, class... Arg>
+int launch(void (*kernel)(Par...), int64_t ctas, const TokenArgs& a, const char* what, const Arg&... arg) {
+    if (ctas == 0) return MXFP8_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks < (1 << 22) ? blocks : (1 << 22)));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < (1 << 22) ? ctas : (1 << 22)));
     cfg.blockDim = dim3(THREADS);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];
@@ -475,40 +726,92 @@ int launch(void (*kernel)(Par), const Par& p, int64_t units, const TokenArgs& a,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, arg...);
     return e == cudaSuccess ? MXFP8_OK : failed(e, what);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Columns of a unit (a warp's work): as many as leave `enough` units for the
+// warps to even out.
+int unit_columns(const TokenArgs& a, int least, int enough) {
+    int seg = least;
+    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= enough) seg *= 2;
+    return seg;
 }
 
 RowPar row_par(const TokenArgs& a, int seg) {
     RowPar p{};
-    p.T = a.T; p.rows = a.rows; p.H = a.H; p.k = a.top_k; p.segs = (a.H + seg - 1) / seg;
+    p.T = a.T; p.rows = a.rows; p.H = a.H; p.k = a.top_k; p.seg = seg; p.segs = (a.H + seg - 1) / seg;
     p.slot = a.slot; p.src = a.src; p.tok_in = a.tok_in; p.sorted_in = a.sorted_in;
     p.tok_out = a.tok_out; p.sorted_out = a.sorted_out; p.q = a.q; p.s = a.s; p.w = a.weights; p.dw = a.dweights;
     p.status = a.status;
+    p.words = a.q && a.H % 128 == 0 && (reinterpret_cast<uintptr_t>(a.s) & 3) == 0;
+    // padding: a row for each group of warps while that gives few CTAs, else up to 32
+    const int groups = WARPS / pad_parts(a.q ? a.H : 2 * a.H);
+    p.pad = 1;
+    while (p.pad < 32 && ceil_div(a.rows, groups * p.pad) > PAD_CTAS) p.pad *= 2;
+    p.pad_ctas = static_cast<int>(ceil_div(a.rows, groups * p.pad));
     return p;
 }
 
-int64_t pad_units(const TokenArgs& a) { return (a.rows + PAD_ROWS - 1) / PAD_ROWS; }
-
 }  // namespace
 
+// CTAs of the plan's cluster on a device: 16 where a cluster of 16 full SMs has
+// room, else the portable 8. Asked once per device.
+static cudaError_t plan_cluster(int dev, int* ctas) {
+    static std::atomic<int> known[64];
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(token_plan_kernel<int64_t>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(token_plan_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(PLAN_MAX_CTAS);
+        cfg.blockDim = dim3(1024);
+        cfg.dynamicSmemBytes = PLAN_SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = PLAN_MAX_CTAS;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, token_plan_kernel<int64_t>, &cfg);
+        if (e != cudaSuccess) return e;
+        n = clusters > 0 ? PLAN_MAX_CTAS : 8;
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *ctas = n;
+    return cudaSuccess;
+}
+
 int launch_token_plan(const TokenPlanArgs& a) {
-    PlanPar p{a.ids, static_cast<int>(a.pairs), a.first, a.local, a.align, static_cast<int>(a.rows), a.offs, a.slot, a.src, a.status};
+    PlanPar p{a.ids, static_cast<int>(a.pairs), a.first, a.local, a.align, static_cast<int>(a.rows), 0, a.offs, a.slot, a.src, a.status};
+    while ((1 << (3 * p.groups)) < a.local) ++p.groups;
     auto kernel = a.id64 ? token_plan_kernel<int64_t> : token_plan_kernel<int32_t>;
     int warps = 32;
-    while ((warps + 3) * static_cast<size_t>(a.local) * 4 > PLAN_SMEM) warps /= 2;
-    const size_t smem = (warps + 3) * static_cast<size_t>(a.local) * 4;
-    // (set before every launch: the attribute belongs to the device that is current)
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
-    if (e != cudaSuccess) return failed(e, "token plan: shared memory");
+    const auto bytes = [&] { return (warps + 5) * static_cast<size_t>(a.local) * 4 + warps * RUN * 6; };
+    while (bytes() > PLAN_SMEM) warps /= 2;
+    const size_t smem = bytes();
+    int ctas = 1;
+    cudaError_t e = cudaSuccess;
+    if (a.pairs > PLAN_ONE_CTA) {
+        e = plan_cluster(a.dev, &ctas);
+        if (e != cudaSuccess) return failed(e, "token plan: cluster size");
+    }
+    if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    // (these two before every launch that needs them: they belong to the device that is current)
+    if (e == cudaSuccess && smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
+    if (e != cudaSuccess) return failed(e, "token plan: kernel attributes");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(PLAN_MAX_CTAS);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PLAN_MAX_CTAS;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -519,18 +822,22 @@ int launch_token_plan(const TokenPlanArgs& a) {
 }
 
 int launch_token_dispatch(const TokenArgs& a) {
-    const RowPar p = row_par(a, a.q ? QSEG : SEG);
-    return launch(a.q ? dispatch_mxfp8_kernel : dispatch_kernel, p, a.T * p.segs + pad_units(a), a, "dispatch kernel");
+    const RowPar p = row_par(a, a.q ? unit_columns(a, 512, UNITS_ENOUGH_MXFP8) : unit_columns(a, 256, UNITS_ENOUGH));
+    return launch(a.q ? dispatch_mxfp8_kernel : dispatch_kernel, ceil_div(a.T * p.segs, WARPS) + p.pad_ctas, a, "dispatch kernel", p);
 }
 
 int launch_token_combine(const TokenArgs& a) {
-    const RowPar p = row_par(a, CSEG);
-    return launch(a.weights ? combine_kernel<true> : combine_kernel<false>, p, a.T * p.segs, a, "combine kernel");
+    const RowPar p = row_par(a, unit_columns(a, 256, UNITS_ENOUGH));
+    return launch(a.weights ? combine_kernel<true> : combine_kernel<false>, ceil_div(a.T * p.segs, WARPS), a, "combine kernel", p);
 }
 
 int launch_token_combine_grad(const TokenArgs& a) {
     const RowPar p = row_par(a, a.H);
-    return launch(combine_grad_kernel, p, a.T * a.top_k + pad_units(a), a, "combine gradient kernel");
+    const int64_t pairs = a.T * a.top_k, sms = a.num_sms;
+    const auto go = [&](auto kernel, int per) { return launch(kernel, ceil_div(pairs, per) + p.pad_ctas, a, "combine gradient kernel", p); };
+    if (pairs <= 2 * sms) return go(combine_grad_kernel<TEAM>, 1);
+    if (2 * a.rows >= pairs || pairs <= PAIRS * 4 * sms) return go(combine_grad_kernel<WARP>, WARPS);
+    return go(combine_grad_kernel<LIST>, PAIRS);
 }
 
 }  // namespace mxw
