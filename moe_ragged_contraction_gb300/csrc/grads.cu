@@ -16,7 +16,8 @@ constexpr uint32_t FULL = 0xffffffffu;
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int VECS = 8;                        // 16-byte vectors of a thread in a chunk
 constexpr int CHUNK = THREADS * VECS * 16;     // bytes
-constexpr int MAX_CTAS = 160 * 8;              // partial sums of one launch
+constexpr int SUM_CTAS = 4, SCALE_CTAS = 5;    // resident on an SM
+constexpr int MAX_CTAS = 160 * SUM_CTAS;       // partial sums of one launch
 constexpr int FEW = 64, MANY = 1024;           // tensors of one launch (parameters: 1.9 or 29.7 KB of 32)
 
 template <int N>
@@ -36,6 +37,7 @@ struct Piece {
     const uint8_t *lo, *hi, *at;  // tensor's first and last byte + 1, the thread's first vector
     ptrdiff_t to_out;             // from an input's address to its output's
     bool f32;
+    bool whole;                   // all of the chunk's vectors lie inside the tensor
 };
 
 template <int N>
@@ -52,6 +54,8 @@ __device__ __forceinline__ Piece piece(const Table<N>& t, uint32_t chunk) {
     p.at = base + static_cast<int64_t>(chunk - t.chunk0[a]) * CHUNK + threadIdx.x * 16;
     p.to_out = static_cast<uint8_t*>(t.out[a]) - p.lo;
     p.f32 = t.f32[a] != 0;
+    const uint8_t* begin = p.at - threadIdx.x * 16;
+    p.whole = begin >= p.lo && begin + CHUNK <= p.hi;
     return p;
 }
 
@@ -75,6 +79,16 @@ __device__ __forceinline__ uint4 load_vector(const Piece& p, const uint8_t* at) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ void load_piece(const Piece& p, uint4 (&v)[VECS]) {
+    if (p.whole) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) v[i] = load16(p.at + i * (THREADS * 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) v[i] = load_vector(p, p.at + i * (THREADS * 16));
+    }
+}
+
 __device__ __forceinline__ void store_vector(const Piece& p, const uint8_t* at, const uint4& v) {
     uint8_t* to = const_cast<uint8_t*>(at) + p.to_out;
     if (at >= p.lo && at + 16 <= p.hi && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
@@ -95,38 +109,43 @@ __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w 
 // 2^-24: not near overflow, and so large that what underflow takes from a square
 // (2^-150 at most) is nothing beside it. Elsewhere (and for NaN) the elements
 // are summed again in 64 bits.
-__device__ __forceinline__ double squares(const uint4 (&v)[VECS], bool f32) {
+template <bool F32>
+__device__ __forceinline__ float squares_fp32(const uint4 (&v)[VECS]) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            any |= w[j];
-            if (f32) {
-                const float x = __uint_as_float(w[j]);
-                s[j] = fmaf(x, x, s[j]);
-            } else {
-                const float x = lo_bf16(w[j]), y = hi_bf16(w[j]);
-                s[j] = fmaf(x, x, s[j]);
-                s[j] = fmaf(y, y, s[j]);
-            }
+            const float x = F32 ? __uint_as_float(w[j]) : lo_bf16(w[j]);
+            s[j] = fmaf(x, x, s[j]);
+            if (!F32) s[j] = fmaf(hi_bf16(w[j]), hi_bf16(w[j]), s[j]);
         }
     }
-    const float sum = (s[0] + s[1]) + (s[2] + s[3]);
-    if (sum >= 0x1p-80f && sum <= 0x1p120f) return sum;
-    if ((any & 0x7fff7fffu) == 0 && (!f32 || (any & 0x7fffffffu) == 0)) return 0.0;  // zeros of either sign
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __noinline__ double squares_fp64(uint4 v, bool f32) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     double d = 0.0;
 #pragma unroll 1
-    for (int i = 0; i < VECS; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const double x = f32 ? __uint_as_float(w[j]) : lo_bf16(w[j]), y = f32 ? 0.f : hi_bf16(w[j]);
-            d += x * x + y * y;
-        }
+    for (int j = 0; j < 4; ++j) {
+        const double x = f32 ? __uint_as_float(w[j]) : lo_bf16(w[j]), y = f32 ? 0.f : hi_bf16(w[j]);
+        d += x * x + y * y;
     }
+    return d;
+}
+
+__device__ __forceinline__ double squares(const uint4 (&v)[VECS], bool f32) {
+    const float sum = f32 ? squares_fp32<true>(v) : squares_fp32<false>(v);
+    if (sum >= 0x1p-80f && sum <= 0x1p120f) return sum;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) any |= v[i].x | v[i].y | v[i].z | v[i].w;
+    if ((any & (f32 ? 0x7fffffffu : 0x7fff7fffu)) == 0) return 0.0;  // zeros of either sign
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) d += squares_fp64(v[i], f32);
     return d;
 }
 
@@ -144,7 +163,7 @@ __device__ __forceinline__ double block_sum(double d, double* part) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(THREADS) squares_kernel(const __grid_constant__ Table<N> t, double* partial) {
+__global__ void __launch_bounds__(THREADS, SUM_CTAS) squares_kernel(const __grid_constant__ Table<N> t, double* partial) {
     __shared__ double part[WARPS];
     griddep_launch_dependents();
     griddep_wait();
@@ -152,8 +171,7 @@ __global__ void __launch_bounds__(THREADS) squares_kernel(const __grid_constant_
     for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Piece p = piece(t, c);
         uint4 v[VECS];
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) v[i] = load_vector(p, p.at + i * (THREADS * 16));
+        load_piece(p, v);
         d += squares(v, p.f32);
     }
     d = block_sum(d, part);
@@ -166,17 +184,25 @@ struct Total {
     const float* norm_in;   // or the norm itself
     float* norm;            // receives it (or nullptr)
     float max_norm, eps;
+    float2* factor;         // receives the factor (norm_kernel), or holds it (scale_kernel); nullptr: neither
 };
 
-// sqrt of the sum of the partial sums, the same in every thread and CTA.
+// The factor min(1, max_norm / (norm + eps)) as a product of two: fp32 would hold
+// a very small one with fewer bits.
+__device__ __forceinline__ float2 clip_factor(const Total& t, double norm) {
+    double c = t.max_norm / (norm + t.eps);
+    if (c >= 1.0) c = 1.0;  // (a NaN stays one)
+    const float second = c < 0x1p-100 ? 0x1p-100f : 1.f;
+    return make_float2(static_cast<float>(c / second), second);
+}
+
+// The norm, from the partial sums or the caller, in thread 0.
 __device__ __forceinline__ double global_norm(const Total& t, double* part) {
     if (t.norm_in) return *t.norm_in;
     double d = 0.0;
     for (int i = threadIdx.x; i < t.count; i += THREADS) d += t.partial[i];
     d = block_sum(d, part);
-    if (threadIdx.x == 0) part[0] = d;
-    __syncthreads();
-    return sqrt(part[0]);
+    return threadIdx.x == 0 ? sqrt(d) : 0.0;
 }
 
 __global__ void __launch_bounds__(THREADS) norm_kernel(const Total t) {
@@ -184,37 +210,53 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const Total t) {
     griddep_launch_dependents();
     griddep_wait();
     const double norm = global_norm(t, part);
-    if (threadIdx.x == 0) *t.norm = static_cast<float>(norm);
+    if (threadIdx.x) return;
+    if (t.norm) *t.norm = static_cast<float>(norm);
+    if (t.factor) *t.factor = clip_factor(t, norm);
+}
+
+template <bool F32>
+__device__ __forceinline__ void scale_piece(const Piece& p, const uint4 (&v)[VECS], float first, float second) {
+    const bool straight = p.whole && ((reinterpret_cast<uintptr_t>(p.at) + p.to_out) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = F32 ? __float_as_uint(__uint_as_float(w[j]) * first * second)
+                       : pack_bf16x2(__float_as_uint(lo_bf16(w[j]) * first * second), __float_as_uint(hi_bf16(w[j]) * first * second));
+        const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
+        const uint8_t* at = p.at + i * (THREADS * 16);
+        if (straight) *reinterpret_cast<uint4*>(const_cast<uint8_t*>(at) + p.to_out) = o;
+        else store_vector(p, at, o);
+    }
 }
 
 template <int N>
-__global__ void __launch_bounds__(THREADS) scale_kernel(const __grid_constant__ Table<N> t, const Total total, int in_place) {
+__global__ void __launch_bounds__(THREADS, SCALE_CTAS) scale_kernel(const __grid_constant__ Table<N> t, const Total total, int in_place) {
     __shared__ double part[WARPS];
+    __shared__ float2 factor;
     griddep_launch_dependents();
     griddep_wait();
-    const double norm = global_norm(total, part);
-    if (total.norm && blockIdx.x == 0 && threadIdx.x == 0) *total.norm = static_cast<float>(norm);
-    double c = total.max_norm / (norm + total.eps);
-    if (c >= 1.0) c = 1.0;  // (a NaN stays one)
-    if (c == 1.0 && in_place) return;
-    // two factors where fp32 would hold the one with fewer bits
-    const float second = c < 0x1p-100 ? 0x1p-100f : 1.f;
-    const float first = static_cast<float>(c / second);
-    for (uint32_t chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-        const Piece p = piece(t, chunk);
-        uint4 v[VECS];
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) v[i] = load_vector(p, p.at + i * (THREADS * 16));
-#pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = p.f32 ? __float_as_uint(__uint_as_float(w[j]) * first * second)
-                             : pack_bf16x2(__float_as_uint(lo_bf16(w[j]) * first * second),
-                                           __float_as_uint(hi_bf16(w[j]) * first * second));
-            store_vector(p, p.at + i * (THREADS * 16), make_uint4(w[0], w[1], w[2], w[3]));
+    // (fp64 steps by one thread: a division by all took longer than the scaling)
+    if (total.factor) {
+        if (threadIdx.x == 0) factor = *total.factor;
+    } else {
+        const double norm = global_norm(total, part);
+        if (threadIdx.x == 0) {
+            factor = clip_factor(total, norm);
+            if (total.norm && blockIdx.x == 0) *total.norm = static_cast<float>(norm);
         }
+    }
+    __syncthreads();
+    const float2 f = factor;
+    if (f.x == 1.f && f.y == 1.f && in_place) return;
+    // (the last chunks first: the sum of squares has read them last)
+    for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+        const Piece p = piece(t, t.chunks - 1 - k);
+        uint4 v[VECS];
+        load_piece(p, v);
+        if (p.f32) scale_piece<true>(p, v, f.x, f.y); else scale_piece<false>(p, v, f.x, f.y);
     }
 }
 
@@ -254,13 +296,21 @@ void fill(Table<N>& t, const GradArgs& a, int from) {
 }
 
 int ctas_for(uint32_t chunks, int sms) {
-    const int most = sms * 8 < MAX_CTAS ? sms * 8 : MAX_CTAS;
+    const int most = sms * SUM_CTAS < MAX_CTAS ? sms * SUM_CTAS : MAX_CTAS;
     return chunks < static_cast<uint32_t>(most) ? static_cast<int>(chunks) : most;
 }
+
+// Scaling, from MANY_CHUNKS an SM on: the norm is worked out once beforehand and
+// two chunks are a CTA's; in place, where there is mostly nothing to scale, a
+// grid of IN_PLACE_CTAS an SM ends sooner. With fewer chunks every CTA of a
+// resident grid works the norm out: a launch less.
+constexpr unsigned MANY_CHUNKS = 8, OUT_CHUNKS = 2, IN_PLACE_CTAS = 16;
 
 template <int N>
 int run(const GradArgs& a) {
     Table<N> t;
+    t.n = 0;
+    t.chunks = 0;
     int count = 0;  // partial sums so far
     cudaError_t e = cudaSuccess;
     if (!a.norm_in)
@@ -272,19 +322,32 @@ int run(const GradArgs& a) {
             if (e != cudaSuccess) return failed(e, "sum of squares kernel");
             count += ctas;
         }
-    Total total{a.ws, count, a.norm_in, a.norm_in ? nullptr : a.norm, a.max_norm, a.eps};
+    Total total{a.ws, count, a.norm_in, a.norm_in ? nullptr : a.norm, a.max_norm, a.eps, nullptr};
+    uint64_t chunks = t.chunks;
+    if (a.clip && (a.n > N || a.norm_in)) {
+        chunks = 0;
+        for (int from = 0; from < a.n; from += N) {
+            fill(t, a, from);
+            chunks += t.chunks;
+        }
+    }
+    const bool once = chunks > static_cast<uint64_t>(a.num_sms) * MANY_CHUNKS;
+    if (once || (total.norm && (!a.clip || chunks == 0))) {
+        if (a.clip) total.factor = reinterpret_cast<float2*>(a.ws + count);
+        e = start(norm_kernel, 1, a.stream, total);
+        if (e != cudaSuccess) return failed(e, "norm kernel");
+        total.norm = nullptr;
+    }
     if (a.clip)
         for (int from = 0; from < a.n; from += N) {
-            if (a.n > N || a.norm_in) fill(t, a, from);
+            if (a.n > N) fill(t, a, from);
             if (t.chunks == 0) continue;
-            e = start(scale_kernel<N>, ctas_for(t.chunks, a.num_sms), a.stream, t, total, a.outs ? 0 : 1);
+            unsigned ctas = ctas_for(t.chunks, a.num_sms);
+            if (once) ctas = a.outs ? (t.chunks + OUT_CHUNKS - 1) / OUT_CHUNKS : t.chunks < a.num_sms * IN_PLACE_CTAS ? t.chunks : a.num_sms * IN_PLACE_CTAS;
+            e = start(scale_kernel<N>, ctas, a.stream, t, total, a.outs ? 0 : 1);
             if (e != cudaSuccess) return failed(e, "scaling kernel");
             total.norm = nullptr;  // (written once)
         }
-    if (total.norm) {
-        e = start(norm_kernel, 1, a.stream, total);
-        if (e != cudaSuccess) return failed(e, "norm kernel");
-    }
     return MXFP8_OK;
 }
 
@@ -292,7 +355,7 @@ int run(const GradArgs& a) {
 
 size_t grad_ws_bytes(int n) {
     const size_t launches = n <= FEW ? 1 : (static_cast<size_t>(n) + MANY - 1) / MANY;
-    return launches * MAX_CTAS * sizeof(double);
+    return (launches * MAX_CTAS + 1) * sizeof(double);  // (the partial sums, the norm)
 }
 
 int launch_grads(const GradArgs& a) { return a.n <= FEW ? run<FEW>(a) : run<MANY>(a); }
