@@ -27,8 +27,9 @@ class TokenPlan(NamedTuple):
 
 def _check(t, dtype, shape, name, device):
     """Raises unless t is a contiguous tensor of that dtype and shape on that CUDA device."""
-    if not (isinstance(t, _experts._torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
-        _lib._expect(t, dtype, name)
+    if isinstance(t, _experts._torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
+    _lib._expect(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != device:
@@ -55,19 +56,20 @@ def _begin(t, name, stream):
 def _plan(torch, plan, device):
     """(slot, src, T, top_k, rows) of a plan."""
     _, slot, src = plan
-    if not (isinstance(slot, torch.Tensor) and isinstance(src, torch.Tensor)) or slot.dim() != 2 or src.dim() != 1:
+    if not (isinstance(slot, torch.Tensor) and isinstance(src, torch.Tensor)):
         raise ValueError("plan must be a TokenPlan: offs [local], slot [T, top_k] and src [rows]")
-    i32 = torch.int32
-    _check(slot, i32, slot.shape, "plan.slot", device)
-    _check(src, i32, src.shape, "plan.src", device)
-    T, k = slot.shape
-    return slot, src, T, k, src.shape[0]
+    shape, rows = slot.shape, src.shape
+    if len(shape) != 2 or len(rows) != 1:
+        raise ValueError("plan must be a TokenPlan: offs [local], slot [T, top_k] and src [rows]")
+    _check(slot, torch.int32, shape, "plan.slot", device)
+    _check(src, torch.int32, rows, "plan.src", device)
+    return slot, src, shape[0], shape[1], rows[0]
 
 
 def token_plan_rows(T: int, top_k: int, local: int, align: int = 32) -> int:
     """Rows of the sorted buffers that hold every routing of T tokens (see include/mxfp8_step.h)."""
     T, v = index(T), _sizes(top_k, local, align)
-    rows = int(_lib.load().mxfp8_token_plan_rows(T, *v)) if v and 0 <= T < 2 ** 31 else -1
+    rows = int((_lib._lib or _lib.load()).mxfp8_token_plan_rows(T, *v)) if v and 0 <= T < 2 ** 31 else -1
     if rows < 0:
         raise ValueError(f"unsupported sizes T={T}, top_k={top_k}, local={local}, align={align}")
     return rows
@@ -219,33 +221,41 @@ def token_combine_grad(dout, y, weights, plan, *, dy=None, dweights=None, stream
 
 # ------------------------------------------------------------------ gradients
 
-# (attributes of a list of tensors, by map: the list may be long)
-_contiguous, _device, _address_of, _numel = (methodcaller(m) for m in ("is_contiguous", "get_device", "data_ptr", "numel"))
-_dtype = attrgetter("dtype")
+_PLAIN = None  # the tensor types whose attributes are the base class's
 
 
 def _table(torch, tensors, device, name):
     """(pointers, sizes, types) of a list of tensors, as arrays."""
-    for t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be torch.Tensors, got {type(t).__name__}")
-    if not all(map(_contiguous, tensors)):
+    kinds = set(map(type, tensors))
+    T = torch.Tensor
+    if kinds <= _PLAIN:  # the list may be long: by map over the base class's own attributes
+        contiguous, where, address, numel, dtype = T.is_contiguous, T.get_device, T.data_ptr, T.numel, T.dtype.__get__
+    else:
+        for k in kinds:
+            if not issubclass(k, T):
+                raise TypeError(f"{name} must be torch.Tensors, got {k.__name__}")
+        contiguous, where, address, numel = (methodcaller(m) for m in ("is_contiguous", "get_device", "data_ptr", "numel"))
+        dtype = attrgetter("dtype")
+    if not all(map(contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    if any(map(device.__ne__, map(_device, tensors))):
+    if tensors and set(map(where, tensors)) != {device}:
         raise ValueError(f"{name} must all be on cuda:{device}")
-    types = list(map(_TYPES.get, map(_dtype, tensors)))
+    types = list(map(_TYPES.get, map(dtype, tensors)))
     if None in types:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {tensors[types.index(None)].dtype}")
-    return array("Q", map(_address_of, tensors)), array("q", map(_numel, tensors)), array("i", types)
+    return array("Q", map(address, tensors)), array("q", map(numel, tensors)), array("i", types)
 
 
 _TYPES = {}
+_requires_grad = attrgetter("requires_grad")
 
 
 def _grads(grads, stream, norm=None):
     torch = _experts._torch or _experts._torch_module()
-    if not _TYPES:
+    global _PLAIN
+    if _PLAIN is None:
         _TYPES.update({torch.bfloat16: 0, torch.float32: 1})
+        _PLAIN = {torch.Tensor, torch.nn.Parameter}
     if isinstance(grads, torch.Tensor):
         raise TypeError("grads must be a list of tensors")
     grads = list(grads)
@@ -277,7 +287,7 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
         out = _new(stream, (), torch.float32, grads[0])
     else:
         _check(out, torch.float32, (), "out", device)
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (*grads, out)):
+    if torch.is_grad_enabled() and any(map(_requires_grad, (*grads, out))):
         _experts._refuse_gradients(grads=next((t for t in grads if t.requires_grad), None), out=out)
     end, rest = _workspace(torch, workspace, device, st)
     rc = getattr(lib, "mxfp8_grad_norm" + end)(_address(ptrs), _address(sizes), _address(types), len(grads), out.data_ptr(), *rest)
@@ -302,7 +312,7 @@ def clip_grads(grads, max_norm, *, norm=None, eps=1e-6, out=None, workspace=None
         outs, _, out_types = _table(torch, out, device, "out")
         if out_types != types or any(o.shape != g.shape for o, g in zip(out, grads)):
             raise ValueError("out must have the shapes and dtypes of grads")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (*grads, *(out or ()))):
+    if torch.is_grad_enabled() and any(map(_requires_grad, (*grads, *(out or ())))):
         _experts._refuse_gradients(grads=next((t for t in grads if t.requires_grad), None),
                                    out=next((t for t in out or () if t.requires_grad), None))
     known = None
