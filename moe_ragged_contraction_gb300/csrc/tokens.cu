@@ -47,19 +47,25 @@ __device__ __forceinline__ uint4 load16_l1_if(bool there, const void* p) {
 
 // ------------------------------------------------------------------ plan
 
-// A counting sort by expert that keeps the order of the pairs, in one cluster:
-// every warp counts the experts of its run of pairs (its own row of counters in
-// shared memory: no atomics), the warps' and, through distributed shared memory,
-// the CTAs' counts become starting rows, and every warp walks its run again and
-// hands out rows. match.any gives each lane its place among the lanes with the
-// same expert.
+// A counting sort by expert that keeps the order of the pairs, in clusters that do
+// not talk to one another. Each CTA of a cluster has a part of the pairs, cut into
+// as many segments as there are clusters; the cluster of that number ranks the
+// pairs of the segment and gives them rows, and only counts those of the others:
+// counting takes a tenth of what ranking does, and no scratch or hand-over between
+// clusters is needed. In its segment every warp has a run of pairs and a row of
+// counters in shared memory (no atomics); the warps' counts and, through
+// distributed shared memory, the CTAs' become starting rows.
 constexpr int PLAN_MAX_CTAS = 16;
 constexpr int PLAN_SMEM = 224 * 1024;
-constexpr int PLAN_ONE_CTA = 2048;  // pairs that one CTA sorts
+// Pairs up to which one CTA, one cluster sorts: 2040 pairs take 6.9 us on a cluster
+// and 7.6 on a CTA, 1536 6.9 / 7.0, 384 5.7 either way; 49152 8.4 on a cluster and
+// 8.6 on four, 98304 10.6 / 9.4, 2097152 107 / 45. (More than four clusters of 16 do
+// not fit the GPU at once.)
+constexpr int PLAN_ONE_CTA = 512, PLAN_ONE_CLUSTER = 65536;
 
 struct PlanPar {
     const void* ids;
-    int pairs, first, local, align, rows, groups;
+    int pairs, first, local, align, rows, groups, C, Q;  // C CTAs in each of Q clusters
     int32_t *offs, *slot, *src;
     int* status;
 };
@@ -76,8 +82,9 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// (not the .aligned forms: lanes come out of loops of different lengths)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // A warp works on RUN pairs at a time; their experts and ranks stay in shared memory.
 constexpr int RUN = 512, LOADS = RUN / 32;
@@ -96,7 +103,26 @@ __device__ __forceinline__ void load_run(const Id* ids, int at, int hi, int firs
     }
 }
 
-// Lanes whose e (below 2^(3 groups), or -1) is this lane's.
+// Adds the experts of the pairs lo .. hi to `counts`, by the whole CTA.
+template <class Id>
+__device__ __forceinline__ void count_pairs(const Id* ids, int lo, int hi, const PlanPar& p, int* counts) {
+    constexpr int N = 8;
+#pragma unroll 1
+    for (long long at = lo + static_cast<int>(threadIdx.x); at < hi; at += N * blockDim.x) {
+        Id v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = at + i * static_cast<int>(blockDim.x) < hi ? ids[at + i * static_cast<int>(blockDim.x)] : Id(-1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const long long d = static_cast<long long>(v[i]) - p.first;
+            if (v[i] >= 0 && d >= 0 && d < p.local) atomicAdd(counts + d, 1);
+        }
+    }
+}
+
+// Lanes whose e (below 2^(3 groups), or -1) is this lane's. match.any takes the
+// longer the more values there are: 262144 pairs, one in eight here, 9.8 us with it
+// and 11.2 with ballots; all of 2097152 here, 64 experts, 54 / 45.
 __device__ __forceinline__ uint32_t same_expert(int e, int groups) {
     uint32_t m = __ballot_sync(FULL, e >= 0);
     if (__popc(m) <= 8) return __match_any_sync(FULL, e);
@@ -128,21 +154,27 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
     int* base = mine + p.local;          // [local] first row of the CTA's pairs
     int* full = base + p.local;          // [local] end of the group's pairs
     int* ends = full + p.local;          // [local] end of the group
-    int* own = ends + p.local;           // [local] start of the expert's pairs among the CTA's, by expert
-    int* kept = own + p.local + warp * RUN;
-    uint16_t* sorted = reinterpret_cast<uint16_t*>(own + p.local + warps * RUN);  // [warps * RUN] the CTA's pairs by expert
+    int* own = ends + p.local;           // [local] start of the expert's pairs among the segment's, by expert
+    int* ahead = own + p.local;          // [2][local] the CTA's pairs ahead of the segment and behind it
+    int* kept = ahead + 2 * p.local + warp * RUN;
+    uint16_t* sorted = reinterpret_cast<uint16_t*>(ahead + 2 * p.local + warps * RUN);  // [warps * RUN] the segment's pairs by expert
     __shared__ int2 part[32];
-    const int C = gridDim.x, c = blockIdx.x;  // (the grid is one cluster)
+    const int C = p.C, c = blockIdx.x % C, q = blockIdx.x / C;
     for (int i = threadIdx.x; i < warps * p.local; i += blockDim.x) hist[i] = 0;
+    for (int i = threadIdx.x; i < 2 * p.local; i += blockDim.x) ahead[i] = 0;
     griddep_launch_dependents();
     griddep_wait();
     __syncthreads();
 
     const Id* ids = static_cast<const Id*>(p.ids);
-    const int per = ((p.pairs + C * warps - 1) / (C * warps) + 31) & ~31;
-    const int lo = static_cast<int>(min(static_cast<long long>(p.pairs), static_cast<long long>(c * warps + warp) * per));
-    const int hi = min(p.pairs, lo + per);
+    const int shares = C * p.Q * warps, per = ((p.pairs + shares - 1) / shares + 31) & ~31;
+    const auto at_share = [&](int i) { return static_cast<int>(min(static_cast<long long>(p.pairs), static_cast<long long>(i) * per)); };
+    const int seg = (c * p.Q + q) * warps, lo = at_share(seg + warp), hi = at_share(seg + warp + 1);
     const bool once = per <= RUN;  // the first pass's ranks serve the second
+    if (p.Q > 1) {
+        count_pairs(ids, at_share(c * p.Q * warps), at_share(seg), p, ahead);
+        count_pairs(ids, at_share(seg + warps), at_share((c + 1) * p.Q * warps), p, ahead + p.local);
+    }
     int* count = hist + warp * p.local;
     // pass 0 counts, pass 1 gives out rows; rolled, so that the code is short: every
     // line of it misses the instruction cache once
@@ -202,7 +234,8 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
                     run += n[i];
                 }
             }
-            mine[e] = run;
+            full[e] = run;
+            mine[e] = run + ahead[e] + ahead[p.local + e];
         }
         cluster_arrive();
         cluster_wait();
@@ -220,10 +253,10 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
                 if (r < c) before += n[r];
                 total += n[r];
             }
-            base[e] = before;
-            full[e] = total;
+            base[e] = before + ahead[e];
+            ends[e] = total;
             sum += (total + p.align - 1) / p.align * p.align;
-            here += mine[e];
+            here += full[e];
         }
         cluster_arrive();  // (no CTA leaves before the others have read its counts: waited for at the end)
         int2 incl = make_int2(sum, here);
@@ -244,40 +277,46 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
         }
 #pragma unroll 1
         for (int e = e0; e < e1; ++e) {
-            const int total = full[e], end = row + (total + p.align - 1) / p.align * p.align;
-            if (c == 0) p.offs[e] = min(end, p.rows);
+            const int total = ends[e], n = full[e], end = row + (total + p.align - 1) / p.align * p.align;
+            if (blockIdx.x == 0) p.offs[e] = min(end, p.rows);
             base[e] += row;
             full[e] = row + total;
             ends[e] = end;
             own[e] = at;
+            ahead[e] = n;  // (the segment's pairs from here on)
             row = end;
-            at += mine[e];
+            at += n;
         }
         __syncthreads();
     }
     if (once) {
         // src by expert: a warp's stores are neighbours
         __syncthreads();
-        const int first = c * warps * per;
+        const int first = seg * per;
 #pragma unroll 1
         for (int e = warp; e < p.local; e += warps)
-            for (int i = lane; i < min(mine[e], p.rows - base[e]); i += 32) p.src[base[e] + i] = first + sorted[own[e] + i];
+            for (int i = lane; i < min(ahead[e], p.rows - base[e]); i += 32) p.src[base[e] + i] = first + sorted[own[e] + i];
     }
-    if (c == 0)
+    if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < p.local; e += blockDim.x)
             if (full[e] > p.rows) atomicOr(p.status, MXFP8_DEV_TOKENS_ROWS);  // (that many pairs were dropped)
     // padding: a warp an expert, and the rows behind the last group
-    for (int e = c * warps + warp; e < p.local; e += C * warps)
+    for (int e = blockIdx.x * warps + warp; e < p.local; e += gridDim.x * warps)
         for (int r = full[e] + lane; r < min(ends[e], p.rows); r += 32) p.src[r] = -1;
-    for (long long r = ends[p.local - 1] + static_cast<long long>(c) * blockDim.x + threadIdx.x; r < p.rows; r += C * blockDim.x)
+    for (long long r = ends[p.local - 1] + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; r < p.rows; r += gridDim.x * blockDim.x)
         p.src[r] = -1;
     cluster_wait();
 }
 
 // ------------------------------------------------------------------ rows
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int UNITS_ENOUGH = 20000, UNITS_ENOUGH_MXFP8 = 5000, PAD_CTAS = 4096;
+// What bounds these kernels is DRAM: they have no arithmetic to speak of. A unit of
+// work is a warp's: some columns of a token, or a pair. CTAs of four warps: a CTA
+// lives as long as its longest unit, and tokens have from none to top_k rows here
+// (with eight warps: 16B dispatch 76.9 us against 74.1, combine on the 671B rank
+// 162 / 158, its gradient 225 / 220; with two 75.1, 157, 233).
+constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int PAD_CTAS = 4096;
 
 struct RowPar {
     int64_t T, rows;
@@ -320,8 +359,9 @@ __device__ __forceinline__ float2 bf16x2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// Warps that share a row of padding: each writes some 2 KB of it.
-__host__ __device__ inline int pad_parts(int bytes) { return bytes <= 2048 ? 1 : bytes <= 4096 ? 2 : bytes <= 8192 ? 4 : 8; }
+// Warps that share a row of padding: each writes 2 KB of it or more.
+__host__ __device__ inline int pad_parts(int bytes) { return bytes <= 2048 ? 1 : bytes <= 4096 ? 2 : 4; }
+static_assert(WARPS % 4 == 0, "pad_parts");
 
 // Zeros on the padding among the `cta`th p.pad * (WARPS / parts) rows (of `bytes`,
 // and of scales): a CTA's work, p.pad rows for each `parts` warps.
@@ -343,8 +383,10 @@ __device__ __forceinline__ void zero_padding(const RowPar& p, uint32_t cta, int 
     }
 }
 
-// Each token's columns are read once and written to all of its rows.
-constexpr int SEG = 1024;  // columns that a warp moves
+// Each token's columns are read once and written to all of its rows, SEG at a time.
+// 16384 tokens of 2048 columns to 6 rows each: 74 us, 6.4 TB/s; 32768 of 7168, 32 of
+// 256 experts here: 156 us.
+constexpr int SEG = 1024;
 
 __global__ void __launch_bounds__(THREADS) dispatch_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
@@ -383,7 +425,10 @@ __global__ void __launch_bounds__(THREADS) dispatch_kernel(const RowPar p) {
     }
 }
 
-// 16 columns a lane in each of QRUNS runs of 512: two neighbouring lanes hold a block of 32.
+// As dispatch_kernel, with a token's columns quantised once for all of its rows:
+// 16 columns a lane in each of QRUNS runs of 512, so that two neighbouring lanes
+// hold a block of 32. Scales go out in words of four. 32768 tokens of 7168 columns,
+// 32 of 256 experts here: 106 us, 6.4 TB/s.
 constexpr int QRUNS = 4;
 constexpr int QSEG = 512 * QRUNS;
 
@@ -412,7 +457,7 @@ __device__ __forceinline__ void quantise16(const uint4& a, const uint4& b, uint4
     sb = e + 127;
 }
 
-__global__ void __launch_bounds__(THREADS, 4) dispatch_mxfp8_kernel(const RowPar p) {
+__global__ void __launch_bounds__(THREADS, 8) dispatch_mxfp8_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
@@ -523,8 +568,8 @@ __device__ __forceinline__ void add_rows(const RowPar& p, const Group<G>& g, int
         }
 }
 
-// The sum of a token's rows over the columns of a unit, G rows of U vectors in flight.
-
+// The sum of a token's rows over the columns of a unit, G rows of U vectors in
+// flight: with six 16-byte loads a lane and 32 warps an SM latency is covered.
 template <int G, int U, bool WEIGHTED>
 __device__ __forceinline__ void combine_token(const RowPar& p, int64_t t, int seg, int lane, const Slots& s, float w_lo, float w_hi) {
     const int end = min(p.H, seg + p.seg);
@@ -579,8 +624,12 @@ __device__ __forceinline__ void combine_one(const RowPar& p, int64_t t, int seg,
     }
 }
 
+// The way by the number n of the token's rows, so that six to eight loads are in
+// flight at any n (one way with six rows: k = 8 53.3 us against 51.2; without the
+// way for one row: 671B rank 174 / 162). 16384 tokens, 6 rows of 2048 columns: 74
+// us, 6.3 TB/s.
 template <bool WEIGHTED>
-__global__ void __launch_bounds__(THREADS, 4) combine_kernel(const RowPar p) {
+__global__ void __launch_bounds__(THREADS, 8) combine_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
     griddep_wait();
@@ -641,17 +690,18 @@ __device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t
 
 // The gradient of the weighted sum. How a CTA's warps take pairs:
 //   LIST   it lists those of PAIRS neighbouring pairs that have a row, a warp takes
-//          one at a time (one rank of several: most pairs have none)
-//   WARP   a warp a pair
-//   TEAM   all warps one pair, for so few that latency counts
-// Neighbouring pairs share their token's row of dout in L1.
-// (16-byte loads of each of the two rows in flight a thread: 8 in LIST, where two
-// CTAs an SM are enough, else 4.)
+//          one at a time, 8 loads of each of the two rows in flight: where most
+//          pairs have none (671B rank: 223 us, WARP 239)
+//   WARP   a warp a pair, 4 loads of each row in flight, twice the warps: where most
+//          have one (16B: 137 us, LIST 143; 512 tokens 6.3 / 15)
+//   TEAM   all warps one pair, for so few that latency counts (64 pairs: 3.8 us, WARP 5.7)
+// Neighbouring pairs share their token's row of dout in L1. 32768 tokens of 7168
+// columns, 32 of 256 experts: 220 us, 6.8 TB/s.
 enum Share { LIST, WARP, TEAM };
 constexpr int PAIRS = 64;
 
 template <Share SHARE>
-__global__ void __launch_bounds__(THREADS, SHARE == LIST ? 2 : 4) combine_grad_kernel(const RowPar p) {
+__global__ void __launch_bounds__(THREADS, SHARE == LIST ? 4 : 8) combine_grad_kernel(const RowPar p) {
     constexpr int PER = SHARE == LIST ? PAIRS : SHARE == WARP ? WARPS : 1;  // pairs of a CTA at a time
     __shared__ int list[PAIRS], rows[PAIRS], counts[2];
     __shared__ float sums[WARPS];
@@ -732,11 +782,22 @@ int launch(void (*kernel)(Par...), int64_t ctas, const TokenArgs& a, const char*
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Columns of a unit (a warp's work): as many as leave `enough` units for the
-// warps to even out.
-int unit_columns(const TokenArgs& a, int least, int enough) {
-    int seg = least;
-    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= enough) seg *= 2;
+// Columns of a unit: as many as leave units enough for the warps to even out. A
+// unit's start is a chain of two loads: 256 columns everywhere took 402 us for the
+// sum on the 671B rank, whole tokens everywhere 10.6 us for its 8 tokens; here 149
+// and 2.1.
+int unit_columns(const TokenArgs& a) {
+    int seg = 256;
+    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= (seg == 256 ? 20000 : 40000)) seg *= 2;
+    return seg;
+}
+
+// Quantising wants longer units, 2048 columns (one trip of its loop) where that
+// leaves some 5000 (2048 tokens on the 671B rank: 512 columns 22.6 us, whole tokens
+// 15.1, here 10.4).
+int unit_columns_mxfp8(const TokenArgs& a) {
+    int seg = 512;
+    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= 5000) seg *= 2;
     return seg;
 }
 
@@ -748,6 +809,7 @@ RowPar row_par(const TokenArgs& a, int seg) {
     p.status = a.status;
     p.words = a.q && a.H % 128 == 0 && (reinterpret_cast<uintptr_t>(a.s) & 3) == 0;
     // padding: a row for each group of warps while that gives few CTAs, else up to 32
+    // (always 1: dispatch on the 671B rank 137 us against 108; always 32: 512 tokens 12.8 / 5.2)
     const int groups = WARPS / pad_parts(a.q ? a.H : 2 * a.H);
     p.pad = 1;
     while (p.pad < 32 && ceil_div(a.rows, groups * p.pad) > PAD_CTAS) p.pad *= 2;
@@ -757,15 +819,18 @@ RowPar row_par(const TokenArgs& a, int seg) {
 
 }  // namespace
 
-// CTAs of the plan's cluster on a device: 16 where a cluster of 16 full SMs has
-// room, else the portable 8. Asked once per device.
-static cudaError_t plan_cluster(int dev, int* ctas) {
+// The plan kernels' attributes on the device that is current, set once, and the
+// CTAs of a cluster there: 16 where a cluster of 16 full SMs has room, else the
+// portable 8.
+static cudaError_t plan_device(int dev, int* ctas) {
     static std::atomic<int> known[64];
     int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        cudaError_t e = cudaFuncSetAttribute(token_plan_kernel<int64_t>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(token_plan_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
-        if (e != cudaSuccess) return e;
+        for (const void* f : {reinterpret_cast<const void*>(token_plan_kernel<int32_t>), reinterpret_cast<const void*>(token_plan_kernel<int64_t>)}) {
+            cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
+            if (e != cudaSuccess) return e;
+        }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(PLAN_MAX_CTAS);
         cfg.blockDim = dim3(1024);
@@ -777,7 +842,7 @@ static cudaError_t plan_cluster(int dev, int* ctas) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        e = cudaOccupancyMaxActiveClusters(&clusters, token_plan_kernel<int64_t>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, token_plan_kernel<int64_t>, &cfg);
         if (e != cudaSuccess) return e;
         n = clusters > 0 ? PLAN_MAX_CTAS : 8;
         if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
@@ -787,31 +852,27 @@ static cudaError_t plan_cluster(int dev, int* ctas) {
 }
 
 int launch_token_plan(const TokenPlanArgs& a) {
-    PlanPar p{a.ids, static_cast<int>(a.pairs), a.first, a.local, a.align, static_cast<int>(a.rows), 0, a.offs, a.slot, a.src, a.status};
+    PlanPar p{a.ids, static_cast<int>(a.pairs), a.first, a.local, a.align, static_cast<int>(a.rows), 0, 1, 1, a.offs, a.slot, a.src, a.status};
     while ((1 << (3 * p.groups)) < a.local) ++p.groups;
     auto kernel = a.id64 ? token_plan_kernel<int64_t> : token_plan_kernel<int32_t>;
-    int warps = 32;
-    const auto bytes = [&] { return (warps + 5) * static_cast<size_t>(a.local) * 4 + warps * RUN * 6; };
+    int warps = a.pairs <= 64 && a.local <= 64 ? 8 : 32;
+    const auto bytes = [&] { return (warps + 7) * static_cast<size_t>(a.local) * 4 + warps * RUN * 6; };
     while (bytes() > PLAN_SMEM) warps /= 2;
-    const size_t smem = bytes();
-    int ctas = 1;
     cudaError_t e = cudaSuccess;
-    if (a.pairs > PLAN_ONE_CTA) {
-        e = plan_cluster(a.dev, &ctas);
-        if (e != cudaSuccess) return failed(e, "token plan: cluster size");
+    if (a.pairs > PLAN_ONE_CTA || bytes() > 48 * 1024) {
+        e = plan_device(a.dev, &p.C);
+        if (e != cudaSuccess) return failed(e, "token plan: kernel attributes");
+        if (a.pairs <= PLAN_ONE_CTA) p.C = 1;
+        p.Q = a.pairs > PLAN_ONE_CLUSTER ? 4 : 1;
     }
-    if (ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    // (these two before every launch that needs them: they belong to the device that is current)
-    if (e == cudaSuccess && smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PLAN_SMEM);
-    if (e != cudaSuccess) return failed(e, "token plan: kernel attributes");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(p.C * p.Q);
     cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = bytes();
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.x = p.C;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -822,12 +883,12 @@ int launch_token_plan(const TokenPlanArgs& a) {
 }
 
 int launch_token_dispatch(const TokenArgs& a) {
-    const RowPar p = row_par(a, a.q ? unit_columns(a, 512, UNITS_ENOUGH_MXFP8) : unit_columns(a, 256, UNITS_ENOUGH));
+    const RowPar p = row_par(a, a.q ? unit_columns_mxfp8(a) : unit_columns(a));
     return launch(a.q ? dispatch_mxfp8_kernel : dispatch_kernel, ceil_div(a.T * p.segs, WARPS) + p.pad_ctas, a, "dispatch kernel", p);
 }
 
 int launch_token_combine(const TokenArgs& a) {
-    const RowPar p = row_par(a, unit_columns(a, 256, UNITS_ENOUGH));
+    const RowPar p = row_par(a, unit_columns(a));
     return launch(a.weights ? combine_kernel<true> : combine_kernel<false>, ceil_div(a.T * p.segs, WARPS), a, "combine kernel", p);
 }
 
