@@ -6,7 +6,9 @@
  * mxfp8_grouped_gemm, mxfp8_quantize_transpose_bf16 and mxfp8_wgrad_grouped
  * and back, and from the latter's output to mxfp8_muon_update. Status codes,
  * mxfp8_last_error(), mxfp8_device_status() and the conventions on pointers,
- * streams and errors are those of mxfp8_wgrad.h.
+ * streams and errors are those of mxfp8_wgrad.h. Outputs overlap no input and
+ * no other output unless that is said to be allowed. Under stream capture: a
+ * first call in a context loads kernels, so make one before capturing.
  */
 #ifndef MXFP8_STEP_H
 #define MXFP8_STEP_H

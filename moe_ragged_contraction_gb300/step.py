@@ -42,11 +42,6 @@ def _new(stream, shape, dtype, like):
     return _lib._empty(stream, shape, dtype, like.device)
 
 
-def _no_gradients(torch, **tensors):
-    if any(t.requires_grad for t in tensors.values()) and torch.is_grad_enabled():
-        _experts._refuse_gradients(**tensors)
-
-
 def _begin(t, name, stream):
     torch = _experts._torch or _experts._torch_module()
     device, st = _experts._device_and_stream(t, name, stream)
@@ -125,7 +120,8 @@ def token_dispatch(x, plan, *, out=None, stream=None):
         out = _new(stream, (rows, H), torch.bfloat16, x)
     else:
         _check(out, torch.bfloat16, (rows, H), "out", device)
-    _no_gradients(torch, x=x, out=out)
+    if (x.requires_grad or out.requires_grad) and torch.is_grad_enabled():
+        _experts._refuse_gradients(x=x, out=out)
     rc = lib.mxfp8_token_dispatch(x.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows, out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -148,7 +144,8 @@ def token_dispatch_mxfp8(x, plan, *, q=None, s=None, stream=None):
         s = _new(stream, (rows, H // 32), u8, x)
     else:
         _check(s, u8, (rows, H // 32), "s", device)
-    _no_gradients(torch, x=x)
+    if x.requires_grad and torch.is_grad_enabled():
+        _experts._refuse_gradients(x=x)
     rc = lib.mxfp8_token_dispatch_mxfp8(x.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows, q.data_ptr(), s.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -166,7 +163,8 @@ def token_dispatch_grad(dxs, plan, *, out=None, stream=None):
         out = _new(stream, (T, H), torch.bfloat16, dxs)
     else:
         _check(out, torch.bfloat16, (T, H), "out", device)
-    _no_gradients(torch, dxs=dxs, out=out)
+    if (dxs.requires_grad or out.requires_grad) and torch.is_grad_enabled():
+        _experts._refuse_gradients(dxs=dxs, out=out)
     rc = lib.mxfp8_token_dispatch_grad(dxs.data_ptr(), rows, T, H, k, slot.data_ptr(), out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -185,7 +183,8 @@ def token_combine(y, weights, plan, *, out=None, stream=None):
         out = _new(stream, (T, H), torch.bfloat16, y)
     else:
         _check(out, torch.bfloat16, (T, H), "out", device)
-    _no_gradients(torch, y=y, weights=weights, out=out)
+    if (y.requires_grad or weights.requires_grad or out.requires_grad) and torch.is_grad_enabled():
+        _experts._refuse_gradients(y=y, weights=weights, out=out)
     rc = lib.mxfp8_token_combine(y.data_ptr(), rows, weights.data_ptr(), T, H, k, slot.data_ptr(), out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -204,14 +203,15 @@ def token_combine_grad(dout, y, weights, plan, *, dy=None, dweights=None, stream
     _check(y, bf16, (rows, H), "y", device)
     _check(weights, f32, (T, k), "weights", device)
     if dy is None:
-        dy = _new(stream, (rows, H), bf16, dout)
+        dy = torch.empty_like(y) if stream is None else _new(stream, (rows, H), bf16, dout)
     else:
         _check(dy, bf16, (rows, H), "dy", device)
     if dweights is None:
-        dweights = _new(stream, (T, k), f32, dout)
+        dweights = torch.empty_like(weights) if stream is None else _new(stream, (T, k), f32, dout)
     else:
         _check(dweights, f32, (T, k), "dweights", device)
-    _no_gradients(torch, dout=dout, y=y, weights=weights, dy=dy, dweights=dweights)
+    if (dout.requires_grad or y.requires_grad or weights.requires_grad or dy.requires_grad or dweights.requires_grad) and torch.is_grad_enabled():
+        _experts._refuse_gradients(dout=dout, y=y, weights=weights, dy=dy, dweights=dweights)
     rc = lib.mxfp8_token_combine_grad(dout.data_ptr(), y.data_ptr(), weights.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows,
                                       dy.data_ptr(), dweights.data_ptr(), st)
     if rc:
@@ -322,7 +322,7 @@ def clip_grads(grads, max_norm, *, norm=None, eps=1e-6, out=None, workspace=None
         _check(norm, torch.float32, (), "norm", device)
         known = norm.data_ptr()
     end, rest = _workspace(torch, workspace, device, st)
-    rc = getattr(lib, "mxfp8_clip_grads" + end)(_address(ptrs), _address(sizes), _address(types), len(grads), max_norm, eps, known,
+    rc = getattr(lib, "mxfp8_clip_grads" + end)(_address(ptrs), _address(sizes), _address(types), len(grads), float(max_norm), float(eps), known,
                                                 norm.data_ptr(), _address(outs) if outs is not None else None, *rest)
     if rc:
         _lib.check(rc)
