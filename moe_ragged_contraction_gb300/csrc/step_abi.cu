@@ -125,7 +125,7 @@ int grads(const void* const* g, const int64_t* sizes, const int32_t* types, int 
     int rc = mxw::host_device(&dev, &a.num_sms);
     if (rc) return rc;
     a.stream = static_cast<cudaStream_t>(stream);
-    if (use_cache && !norm_in) {
+    if (use_cache) {
         rc = mxw::host_workspace(dev, a.stream, need, &ws);
         if (rc) return rc;
     }

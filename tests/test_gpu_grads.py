@@ -182,6 +182,25 @@ def test_a_norm_that_is_known():
     assert all(torch.equal(a, b * 0.25) for a, b in zip(many, kept))
 
 
+@pytest.mark.parametrize("n", [5000, 60_000_000])
+@pytest.mark.parametrize("inplace", [True, False])
+def test_a_norm_that_is_known_few_and_many_elements(n, inplace):
+    """The same factor on both sides of the rule for many elements, with the cache's scratch and with a workspace."""
+    g = [torch.randn(n, device="cuda").bfloat16(), torch.randn(n // 3 + 1, device="cuda")]
+    norm = torch.tensor(3.0, device="cuda")
+    c = R.factor(3.0, 1.0)
+    ws = torch.empty(mx.grad_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    for workspace in (None, ws):
+        src = [t.clone() for t in g]
+        out = None if inplace else [torch.full_like(t, 9.0) for t in g]
+        mx.clip_grads(src, 1.0, norm=norm, out=out, workspace=workspace)
+        for a, b in zip(src if inplace else out, g):
+            want = b.double() * c
+            rel = 2 * F32 * 1.001 + (B16 * 1.01 if b.dtype is torch.bfloat16 else 0.0)
+            assert ((a.double() - want).abs() <= rel * want.abs() + 2.0 ** -133).all()
+        assert float(norm) == 3.0
+
+
 def test_a_tensor_twice():
     """Counted twice by the norm; as something to clip refused."""
     a = torch.randn(1000, device="cuda")

@@ -291,6 +291,23 @@ def test_views_of_larger_buffers(shift):
         assert (whole[:8 * shift] == 3.0).all() and (whole[8 * shift + n:] == 3.0).all()
 
 
+@pytest.mark.parametrize("shift", [1, 2, 3, 4])
+@pytest.mark.parametrize("H", [256, 2176])
+def test_scales_at_any_address(shift, H):
+    """Scale planes need no alignment: by words and by bytes, nothing written around them."""
+    rng = np.random.default_rng(H)
+    T, k = 50, 3
+    plan = mx.token_plan(dev(rng.integers(-1, 4, (T, k))).int(), 4)
+    rows = plan.src.numel()
+    x = bf16(rng, T, H)
+    q, s = mx.token_dispatch_mxfp8(x, plan)
+    whole = torch.full((rows * H // 32 + 8,), 77, dtype=torch.uint8, device="cuda")
+    view = whole[shift:shift + rows * H // 32].view(rows, H // 32)
+    q2, _ = mx.token_dispatch_mxfp8(x, plan, s=view)
+    assert torch.equal(q, q2) and torch.equal(s, view)
+    assert (whole[:shift] == 77).all() and (whole[shift + rows * H // 32:] == 77).all()
+
+
 def test_results_are_the_same_bits_every_time():
     rng = np.random.default_rng(11)
     ids = dev(routing("spread", rng, 3000, 8, 64)).int()
