@@ -103,6 +103,32 @@ def test_plan_with_too_few_rows(T, k, local, align, rows):
     assert np.array_equal(np64(mx.token_dispatch(x, plan)), R.dispatch(np64(x), src, k))
 
 
+@pytest.mark.parametrize("T,k,experts,first,local,align", [(300000, 4, 64, 0, 64, 32), (150001, 8, 2100, 40, 2048, 1), (530000, 2, 8, 1, 6, 128), (1100000, 1, 1, 0, 1, 32)])
+def test_plan_of_long_runs(T, k, experts, first, local, align):
+    """More pairs than the kernel keeps ranks of at a time."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    ids = torch.randint(-1 if experts > 1 else 0, experts, (T, k), generator=gen, device="cuda")
+    plan = mx.token_plan(ids, local, first_expert=first, align=align)
+    e = ids.view(-1) - first
+    here = (e >= 0) & (e < local)
+    count = torch.bincount(e[here], minlength=local)
+    padded = (count + align - 1) // align * align
+    offs = torch.cumsum(padded, 0)
+    order = torch.nonzero(here).squeeze(-1)[torch.sort(e[here], stable=True).indices]
+    starts = torch.repeat_interleave(offs - padded, count)
+    row = starts + torch.arange(len(order), device="cuda") - torch.repeat_interleave(torch.cumsum(count, 0) - count, count)
+    slot = torch.full((T * k,), -1, dtype=torch.int32, device="cuda")
+    src = torch.full((plan.src.numel(),), -1, dtype=torch.int32, device="cuda")
+    slot[order], src[row] = row.int(), order.int()
+    assert torch.equal(plan.offs.long(), offs) and torch.equal(plan.slot.view(-1), slot) and torch.equal(plan.src, src)
+    # with too few rows
+    rows = int(offs[-1]) // 2 // align * align
+    short = mx.token_plan(ids, local, first_expert=first, align=align, rows=rows)
+    assert mx.device_status(clear=True) == _lib.DEV_TOKENS_ROWS
+    assert torch.equal(short.slot.view(-1), torch.where(slot < rows, slot, -1)) and torch.equal(short.src, src[:rows])
+
+
 @pytest.mark.parametrize("T", [0, 1, 31, 5000])
 def test_plan_fills_what_it_is_given(T):
     """Every element of the outputs is written, with many rows to spare; no token at all among the sizes."""
