@@ -130,7 +130,7 @@ def test_example_gradients():
     ref = torch.einsum("tk,tki,tkhi->th", p, h, a2[ids])
     grads = torch.autograd.grad(ref, (X64, a13, a2, r64), dout.double())
     for got, want in zip((out, dx, dw13, dw2, drouter), (ref, *grads)):
-        assert float((got.double() - want).norm() / want.norm()) < 0.25
+        assert float((got.double() - want.detach()).norm() / want.detach().norm()) < 0.25
 
 
 def test_a_captured_step():
@@ -173,6 +173,52 @@ def test_a_captured_step():
         torch.cuda.synchronize()
         for a, b in zip(got, want[i]):
             assert torch.equal(a, b)
+
+
+def test_threads_on_streams_of_their_own():
+    """Four host threads at once, each with its stream and its routing."""
+    import threading
+
+    T, k, E, H = 900, 4, 24, 512
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(21)
+
+    def chain(a, stream):
+        ids, x, w, grads = a
+        plan = mx.token_plan(ids, E, stream=stream)
+        xs = mx.token_dispatch(x, plan, stream=stream)
+        out = mx.token_combine(xs, w, plan, stream=stream)
+        dy, dw = mx.token_combine_grad(out, xs, w, plan, stream=stream)
+        clipped = [torch.zeros_like(g) for g in grads]
+        stream.wait_stream(torch.cuda.current_stream())
+        norm = mx.clip_grads(grads, 1.0, out=clipped, stream=stream)
+        return [*plan, xs, out, dy, dw, norm, *clipped]
+
+    sets = [(torch.randint(-1, E, (T, k), generator=gen, device="cuda"), torch.randn((T, H), generator=gen, device="cuda").bfloat16(), torch.rand((T, k), generator=gen, device="cuda"),
+             [torch.randn(n, generator=gen, device="cuda") * (i + 1) for n in (70001, 33)]) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    want = [chain(a, s) for a, s in zip(sets, streams)]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            for _ in range(30):
+                got[i] = chain(sets[i], streams[i])
+            streams[i].synchronize()
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for g, e in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, e))
 
 
 def test_scratch_under_capture():
