@@ -1,9 +1,15 @@
 // Global norm of many gradients and clipping (include/mxfp8_step.h).
 //
 // The tensors' bytes, cut into chunks of CHUNK bytes from the 16-byte boundary
-// at or below each tensor's start, are one list that the CTAs share. A table of
-// the tensors travels as a kernel parameter: nothing is copied to the device and
-// a captured call keeps its own.
+// at or below the start of what is written (of what is read, where nothing is),
+// are one list that the CTAs share. A table of the tensors travels as a kernel
+// parameter: nothing is copied to the device and a captured call keeps its own.
+// Where outputs lie otherwise than their inputs the stores are the whole vectors
+// and the loads the pieces (15.9M fp32 elements in views of one buffer to tensors of
+// their own: 40 us, with the loads whole 95).
+//
+// Bound by DRAM. 416M bf16 elements: sum 119 us (7.0 TB/s), scaled beside them 253
+// more (6.6 TB/s); in place within the limit 5 more.
 #include "mxw_internal.h"
 #include "mxw_ptx.cuh"
 #include "mxw_step.h"
@@ -35,9 +41,9 @@ struct Table {
 // reach over the tensor's ends.
 struct Piece {
     const uint8_t *lo, *hi, *at;  // tensor's first and last byte + 1, the thread's first vector
-    ptrdiff_t to_out;             // from an input's address to its output's
+    ptrdiff_t to_out;             // from an input's address to its output's: there vectors are aligned
     bool f32;
-    bool whole;                   // all of the chunk's vectors lie inside the tensor
+    bool whole;                   // all of the chunk's vectors, and 2 bytes around, lie inside the tensor
 };
 
 template <int N>
@@ -50,12 +56,11 @@ __device__ __forceinline__ Piece piece(const Table<N>& t, uint32_t chunk) {
     Piece p;
     p.lo = static_cast<const uint8_t*>(t.in[a]);
     p.hi = p.lo + t.bytes[a];
-    const uint8_t* base = p.lo - (reinterpret_cast<uintptr_t>(p.lo) & 15);
-    p.at = base + static_cast<int64_t>(chunk - t.chunk0[a]) * CHUNK + threadIdx.x * 16;
+    const uint8_t* begin = p.lo - (reinterpret_cast<uintptr_t>(t.out[a]) & 15) + static_cast<int64_t>(chunk - t.chunk0[a]) * CHUNK;
+    p.at = begin + threadIdx.x * 16;
     p.to_out = static_cast<uint8_t*>(t.out[a]) - p.lo;
     p.f32 = t.f32[a] != 0;
-    const uint8_t* begin = p.at - threadIdx.x * 16;
-    p.whole = begin >= p.lo && begin + CHUNK <= p.hi;
+    p.whole = begin >= p.lo + 2 && begin + CHUNK + 2 <= p.hi;
     return p;
 }
 
@@ -65,11 +70,29 @@ __device__ __forceinline__ uint4 load16(const void* p) {
     return v;
 }
 
-// The vector at `at`, with zeros for what lies outside the tensor.
+// 16 bytes at an address of lower alignment. (What two threads read is in L1.)
+template <class T>
+__device__ __forceinline__ uint4 load16_by(const uint8_t* p) {
+    uint4 v;
+    T* w = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) w[i] = reinterpret_cast<const T*>(p)[i];
+    return v;
+}
+
+// The same at an odd number of halves, from the five words around.
+__device__ __forceinline__ uint4 load16_halves(const uint8_t* p) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p - 2);
+    uint32_t x[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = w[i];
+    return make_uint4(__byte_perm(x[0], x[1], 0x5432), __byte_perm(x[1], x[2], 0x5432), __byte_perm(x[2], x[3], 0x5432), __byte_perm(x[3], x[4], 0x5432));
+}
+
+// The vector at `at`, element by element, with zeros for what lies outside the tensor.
 __device__ __forceinline__ uint4 load_vector(const Piece& p, const uint8_t* at) {
-    if (at >= p.lo && at + 16 <= p.hi) return load16(at);
     uint32_t w[4] = {0, 0, 0, 0};
-    if (at < p.hi) {  // (a vector that starts below lo belongs to the tensor's first chunk and reaches into it)
+    if (at < p.hi && at + 16 > p.lo) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint8_t* e = at + 2 * i;  // (halves: elements are aligned to their size)
@@ -79,19 +102,35 @@ __device__ __forceinline__ uint4 load_vector(const Piece& p, const uint8_t* at) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// ALIGNED: inputs lie like their outputs, vectors are aligned in both.
+template <bool ALIGNED>
 __device__ __forceinline__ void load_piece(const Piece& p, uint4 (&v)[VECS]) {
-    if (p.whole) {
+    constexpr int STEP = THREADS * 16;
+    const int odd = ALIGNED ? 0 : static_cast<int>(p.to_out & 15);
+    if (!p.whole) {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) v[i] = load16(p.at + i * (THREADS * 16));
+        for (int i = 0; i < VECS; ++i) {
+            const uint8_t* at = p.at + i * STEP;
+            v[i] = odd == 0 && at >= p.lo && at + 16 <= p.hi ? load16(at) : load_vector(p, at);
+        }
+    } else if (odd == 0) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) v[i] = load16(p.at + i * STEP);
+    } else if (odd == 8) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) v[i] = load16_by<uint2>(p.at + i * STEP);
+    } else if ((odd & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) v[i] = load16_by<uint32_t>(p.at + i * STEP);
     } else {
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) v[i] = load_vector(p, p.at + i * (THREADS * 16));
+        for (int i = 0; i < VECS; ++i) v[i] = load16_halves(p.at + i * STEP);
     }
 }
 
 __device__ __forceinline__ void store_vector(const Piece& p, const uint8_t* at, const uint4& v) {
     uint8_t* to = const_cast<uint8_t*>(at) + p.to_out;
-    if (at >= p.lo && at + 16 <= p.hi && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+    if (p.whole || (at >= p.lo && at + 16 <= p.hi)) {
         *reinterpret_cast<uint4*>(to) = v;
         return;
     }
@@ -171,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, SUM_CTAS) squares_kernel(const __grid
     for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const Piece p = piece(t, c);
         uint4 v[VECS];
-        load_piece(p, v);
+        load_piece<true>(p, v);
         d += squares(v, p.f32);
     }
     d = block_sum(d, part);
@@ -217,7 +256,6 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const Total t) {
 
 template <bool F32>
 __device__ __forceinline__ void scale_piece(const Piece& p, const uint4 (&v)[VECS], float first, float second) {
-    const bool straight = p.whole && ((reinterpret_cast<uintptr_t>(p.at) + p.to_out) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
         uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -225,10 +263,7 @@ __device__ __forceinline__ void scale_piece(const Piece& p, const uint4 (&v)[VEC
         for (int j = 0; j < 4; ++j)
             w[j] = F32 ? __float_as_uint(__uint_as_float(w[j]) * first * second)
                        : pack_bf16x2(__float_as_uint(lo_bf16(w[j]) * first * second), __float_as_uint(hi_bf16(w[j]) * first * second));
-        const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
-        const uint8_t* at = p.at + i * (THREADS * 16);
-        if (straight) *reinterpret_cast<uint4*>(const_cast<uint8_t*>(at) + p.to_out) = o;
-        else store_vector(p, at, o);
+        store_vector(p, p.at + i * (THREADS * 16), make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
@@ -255,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, SCALE_CTAS) scale_kernel(const __grid
     for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
         const Piece p = piece(t, t.chunks - 1 - k);
         uint4 v[VECS];
-        load_piece(p, v);
+        load_piece<false>(p, v);
         if (p.f32) scale_piece<true>(p, v, f.x, f.y); else scale_piece<false>(p, v, f.x, f.y);
     }
 }
@@ -278,19 +313,19 @@ cudaError_t start(void (*kernel)(Par...), unsigned ctas, cudaStream_t stream, co
     return cudaLaunchKernelEx(&cfg, kernel, arg...);
 }
 
-// The tensors from `from` on that fit one table.
+// The tensors from `from` on that fit one table; outs: with their outputs.
 template <int N>
-void fill(Table<N>& t, const GradArgs& a, int from) {
+void fill(Table<N>& t, const GradArgs& a, int from, bool outs) {
     t.n = a.n - from < N ? a.n - from : N;
     uint32_t chunks = 0;
     for (int i = 0; i < t.n; ++i) {
         const int g = from + i;
         t.in[i] = a.grads[g];
-        t.out[i] = a.outs ? a.outs[g] : const_cast<void*>(a.grads[g]);
+        t.out[i] = outs ? a.outs[g] : const_cast<void*>(a.grads[g]);
         t.f32[i] = a.types[g] == MXFP8_GRAD_F32;
         t.bytes[i] = a.sizes[g] * (t.f32[i] ? 4 : 2);
         t.chunk0[i] = chunks;
-        if (t.bytes[i]) chunks += static_cast<uint32_t>((t.bytes[i] + (reinterpret_cast<uintptr_t>(t.in[i]) & 15) + CHUNK - 1) / CHUNK);
+        if (t.bytes[i]) chunks += static_cast<uint32_t>((t.bytes[i] + (reinterpret_cast<uintptr_t>(t.out[i]) & 15) + CHUNK - 1) / CHUNK);
     }
     t.chunks = chunks;
 }
@@ -315,7 +350,7 @@ int run(const GradArgs& a) {
     cudaError_t e = cudaSuccess;
     if (!a.norm_in)
         for (int from = 0; from < a.n; from += N) {
-            fill(t, a, from);
+            fill(t, a, from, false);
             if (t.chunks == 0) continue;
             const int ctas = ctas_for(t.chunks, a.num_sms);
             e = start(squares_kernel<N>, ctas, a.stream, t, a.ws + count);
@@ -323,14 +358,12 @@ int run(const GradArgs& a) {
             count += ctas;
         }
     Total total{a.ws, count, a.norm_in, a.norm_in ? nullptr : a.norm, a.max_norm, a.eps, nullptr};
-    uint64_t chunks = t.chunks;
-    if (a.clip && (a.n > N || a.norm_in)) {
-        chunks = 0;
+    uint64_t chunks = 0;
+    if (a.clip)
         for (int from = 0; from < a.n; from += N) {
-            fill(t, a, from);
+            fill(t, a, from, a.outs != nullptr);
             chunks += t.chunks;
         }
-    }
     const bool once = chunks > static_cast<uint64_t>(a.num_sms) * MANY_CHUNKS;
     if (once || (total.norm && (!a.clip || chunks == 0))) {
         if (a.clip) total.factor = reinterpret_cast<float2*>(a.ws + count);
@@ -340,7 +373,7 @@ int run(const GradArgs& a) {
     }
     if (a.clip)
         for (int from = 0; from < a.n; from += N) {
-            if (a.n > N) fill(t, a, from);
+            if (a.n > N) fill(t, a, from, a.outs != nullptr);
             if (t.chunks == 0) continue;
             unsigned ctas = ctas_for(t.chunks, a.num_sms);
             if (once) ctas = a.outs ? (t.chunks + OUT_CHUNKS - 1) / OUT_CHUNKS : t.chunks < a.num_sms * IN_PLACE_CTAS ? t.chunks : a.num_sms * IN_PLACE_CTAS;

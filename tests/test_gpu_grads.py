@@ -100,6 +100,30 @@ def test_flat_views_in_place(n, types):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("at", range(8))
+@pytest.mark.parametrize("to", [0, 1, 3, 4])
+def test_inputs_and_outputs_at_any_elements(kind, at, to):
+    """Every distance of an output's address from its input's, modulo 16 bytes; nothing around the outputs is written."""
+    rng = np.random.default_rng(8 * at + to)
+    t = torch.bfloat16 if kind == "bf16" else torch.float32
+    sizes = [50000, 3, 20001]
+    src = torch.from_numpy(rng.standard_normal(80000).astype(np.float32)).cuda().to(t)
+    dst = torch.full((80000,), 7.0, dtype=t, device="cuda")
+    g = [src[at + o:at + o + n] for o, n in zip((0, 50000, 50010), sizes)]
+    out = [dst[to + o:to + o + n] for o, n in zip((0, 50005, 50009), sizes)]
+    norm = mx.clip_grads(g, 1.0, out=out)
+    want = R.norm([np64(v) for v in g])
+    assert abs(float(norm) - want) <= NORM * want
+    rel = FACTOR + (B16 * 1.01 if kind == "bf16" else 0.0)
+    touched = torch.zeros(80000, dtype=torch.bool, device="cuda")
+    for a, b in zip(g, out):
+        e = np64(a) * R.factor(want, 1.0)
+        assert np.all(np.abs(np64(b) - e) <= rel * np.abs(e) + 2.0 ** -133)
+        touched[b.storage_offset():b.storage_offset() + b.numel()] = True
+    assert (dst[~touched] == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("power", [-133, -126, -100, -75, -64, -40, 60, 64, 90, 120])
 def test_values_whose_squares_leave_fp32(kind, power):
     rng = np.random.default_rng(power + 200)
