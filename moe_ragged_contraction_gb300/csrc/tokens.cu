@@ -323,6 +323,7 @@ struct RowPar {
     int H, k, seg, segs;  // seg: columns of a unit
     int words;            // rows of scales are whole aligned words
     int pad, pad_ctas;    // zero_padding's rows, and its CTAs
+    int each;             // pairs of a warp (gradient of the sum)
     const int32_t *slot, *src;
     const uint16_t *tok_in, *sorted_in;
     uint16_t *tok_out, *sorted_out;
@@ -426,12 +427,10 @@ __global__ void __launch_bounds__(THREADS) dispatch_kernel(const RowPar p) {
 }
 
 // As dispatch_kernel, with a token's columns quantised once for all of its rows:
-// 16 columns a lane in each of QRUNS runs of 512, so that two neighbouring lanes
+// 16 columns a lane in each of RUNS runs of 512, so that two neighbouring lanes
 // hold a block of 32. Scales go out in words of four. 32768 tokens of 7168 columns,
-// 32 of 256 experts here: 106 us, 6.4 TB/s.
-constexpr int QRUNS = 4;
-constexpr int QSEG = 512 * QRUNS;
-
+// 32 of 256 experts here: 106 us, 6.4 TB/s. RUNS is 4, or 1 for rows of up to 512
+// columns (49809 tokens of 128: 35 us, 54 with 4, all of it instructions).
 __device__ __forceinline__ void quantise16(const uint4& a, const uint4& b, uint4& q, uint32_t& sb) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t amax = 0;
@@ -457,6 +456,7 @@ __device__ __forceinline__ void quantise16(const uint4& a, const uint4& b, uint4
     sb = e + 127;
 }
 
+template <int RUNS>
 __global__ void __launch_bounds__(THREADS, 8) dispatch_mxfp8_kernel(const RowPar p) {
     const int lane = threadIdx.x & 31;
     griddep_launch_dependents();
@@ -476,17 +476,17 @@ __global__ void __launch_bounds__(THREADS, 8) dispatch_mxfp8_kernel(const RowPar
         const Slots sl = token_slots(p, t, lane);
         if (!(sl.has_lo | sl.has_hi)) continue;
 #pragma unroll 1
-        for (int c = seg; c < end; c += QSEG) {  // (the same for all lanes)
+        for (int c = seg; c < end; c += 512 * RUNS) {  // (the same for all lanes)
             const int col = c + lane * 16;
-            uint4 v[QRUNS][2], q[QRUNS];
+            uint4 v[RUNS][2], q[RUNS];
 #pragma unroll
-            for (int i = 0; i < QRUNS; ++i) {
+            for (int i = 0; i < RUNS; ++i) {
                 v[i][0] = load16_if(col + 512 * i < end, p.tok_in + t * p.H + col + 512 * i);
                 v[i][1] = load16_if(col + 512 * i < end, p.tok_in + t * p.H + col + 512 * i + 8);
             }
             uint32_t mine = 0, word = 0;
 #pragma unroll
-            for (int i = 0; i < QRUNS; ++i) {
+            for (int i = 0; i < RUNS; ++i) {
                 uint32_t sb;
                 quantise16(v[i][0], v[i][1], q[i], sb);
                 mine |= sb << (8 * i);
@@ -502,13 +502,13 @@ __global__ void __launch_bounds__(THREADS, 8) dispatch_mxfp8_kernel(const RowPar
                     uint8_t* out = p.q + r * p.H + col;
                     uint8_t* scales = p.s + r * blocks + c / 32;
 #pragma unroll
-                    for (int i = 0; i < QRUNS; ++i)
+                    for (int i = 0; i < RUNS; ++i)
                         if (col + 512 * i < end) *reinterpret_cast<uint4*>(out + 512 * i) = q[i];
                     if (p.words) {
-                        if (lane < 4 * QRUNS && c + 128 * lane < end) *reinterpret_cast<uint32_t*>(scales + 4 * lane) = word;
+                        if (lane < 4 * RUNS && c + 128 * lane < end) *reinterpret_cast<uint32_t*>(scales + 4 * lane) = word;
                     } else if (!(lane & 1)) {
 #pragma unroll
-                        for (int i = 0; i < QRUNS; ++i)
+                        for (int i = 0; i < RUNS; ++i)
                             if (col + 512 * i < end) scales[16 * i + lane / 2] = static_cast<uint8_t>(mine >> (8 * i));
                     }
                 }
@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(THREADS, 8) combine_kernel(const RowPar p) {
             if (lane + 32 < p.k) w_hi = p.w[t * p.k + lane + 32];
         }
         const int n = __popc(s.has_lo) + __popc(s.has_hi);
-        if (n <= 1) combine_one<WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
+        if (p.seg == 256 && n <= 4) combine_token<4, 1, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
+        else if (n <= 1) combine_one<WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
         else if (n <= 3) combine_token<3, 2, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
         else if (n <= 6) combine_token<6, 1, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
         else combine_token<8, 1, WEIGHTED>(p, t, seg, lane, s, w_lo, w_hi);
@@ -654,8 +655,7 @@ __global__ void __launch_bounds__(THREADS, 8) combine_kernel(const RowPar p) {
 // A pair's row of y against the token's row of dout, and the weighted row of dout
 // to the pair's row of dy; this thread's part of the product.
 template <int GRAD_VECS>
-__device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t row, int from, int step) {
-    const float w = p.w[pair];
+__device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t row, float w, int from, int step) {
     const uint16_t* d = p.tok_in + static_cast<int64_t>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.k)) * p.H;
     const int64_t off = row * p.H;
     float dot = 0.f;
@@ -690,33 +690,36 @@ __device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t
 
 // The gradient of the weighted sum. How a CTA's warps take pairs:
 //   LIST   it lists those of PAIRS neighbouring pairs that have a row, a warp takes
-//          one at a time, 8 loads of each of the two rows in flight: where most
-//          pairs have none (671B rank: 223 us, WARP 239)
-//   WARP   a warp a pair, 4 loads of each row in flight, twice the warps: where most
-//          have one (16B: 137 us, LIST 143; 512 tokens 6.3 / 15)
+//          one at a time, LOADS = 8 loads of each of the two rows in flight: where
+//          most pairs have none (671B rank: 223 us, WARP 239)
+//   WARP   a warp a pair, 4 loads of each row in flight (1 for rows of up to 256
+//          columns), twice the warps: where most have one (16B: 137 us, LIST 143; 512 tokens 6.3 / 15). Several pairs
+//          (`each`) one after the other where rows are short, so that there are not
+//          more CTAs than the GPU can start (321264 pairs of 392 columns, one in four
+//          here: 65 us, 146 with a pair a warp; 16B 134 / 136)
 //   TEAM   all warps one pair, for so few that latency counts (64 pairs: 3.8 us, WARP 5.7)
 // Neighbouring pairs share their token's row of dout in L1. 32768 tokens of 7168
 // columns, 32 of 256 experts: 220 us, 6.8 TB/s.
 enum Share { LIST, WARP, TEAM };
 constexpr int PAIRS = 64;
 
-template <Share SHARE>
+template <Share SHARE, int LOADS>
 __global__ void __launch_bounds__(THREADS, SHARE == LIST ? 4 : 8) combine_grad_kernel(const RowPar p) {
-    constexpr int PER = SHARE == LIST ? PAIRS : SHARE == WARP ? WARPS : 1;  // pairs of a CTA at a time
+    const int per = SHARE == LIST ? PAIRS : SHARE == WARP ? WARPS * p.each : 1;  // pairs of a CTA at a time
     __shared__ int list[PAIRS], rows[PAIRS], counts[2];
     __shared__ float sums[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_launch_dependents();
     griddep_wait();
     const int64_t pairs = p.T * p.k;
-    const uint32_t lists = static_cast<uint32_t>((pairs + PER - 1) / PER),
+    const uint32_t lists = static_cast<uint32_t>((pairs + per - 1) / per),
                    units = lists + p.pad_ctas;
     for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
         if (u >= lists) {
             zero_padding(p, u - lists, lane, reinterpret_cast<uint8_t*>(p.sorted_out), 2 * p.H, nullptr, 0);
             continue;
         }
-        const int64_t first = static_cast<int64_t>(u) * PER;
+        const int64_t first = static_cast<int64_t>(u) * per;
         if (SHARE == LIST) {
             __syncthreads();  // (the list before is done with)
             int r = -1, at = 0;
@@ -737,23 +740,36 @@ __global__ void __launch_bounds__(THREADS, SHARE == LIST ? 4 : 8) combine_grad_k
             }
             __syncthreads();
             for (int i = warp; i < counts[0] + counts[1]; i += WARPS) {
-                const float dot = grad_row<8>(p, first + list[i], rows[i], lane * 8, 256);
+                const float dot = grad_row<LOADS>(p, first + list[i], rows[i], p.w[first + list[i]], lane * 8, 256);
                 if (lane == 0) p.dw[first + list[i]] = dot;
             }
-        } else {
-            const int64_t pair = first + (SHARE == WARP ? warp : 0);
-            if (pair >= pairs) continue;
-            const int r = checked(p.slot[pair], p.rows, p.status);
-            float dot = r >= 0 ? grad_row<4>(p, pair, r, (SHARE == WARP ? lane : threadIdx.x) * 8, SHARE == WARP ? 256 : 8 * THREADS) : 0.f;
-            if (SHARE == TEAM) {
-                __syncthreads();  // (the sums of the pair before have been read)
-                if (lane == 0) sums[warp] = dot;
-                __syncthreads();
-                dot = 0.f;
-#pragma unroll
-                for (int v = 0; v < WARPS; ++v) dot += sums[v];
+        } else if (SHARE == WARP) {
+            // a lane a pair for what there is to know of it, then one after the other
+            const int64_t pair = first + warp * p.each + lane;
+            int r = -1;
+            float w = 0.f, mine = 0.f;
+            const bool real = lane < p.each && pair < pairs;
+            if (real) {
+                r = checked(p.slot[pair], p.rows, p.status);
+                w = p.w[pair];
             }
-            if (SHARE == WARP ? lane == 0 : threadIdx.x == 0) p.dw[pair] = dot;
+#pragma unroll 1
+            for (uint32_t has = __ballot_sync(FULL, r >= 0); has; has &= has - 1) {
+                const int i = __ffs(has) - 1;
+                const float dot = grad_row<LOADS>(p, pair - lane + i, __shfl_sync(FULL, r, i), __shfl_sync(FULL, w, i), lane * 8, 256);
+                if (lane == i) mine = dot;
+            }
+            if (real) p.dw[pair] = mine;
+        } else {
+            const int r = checked(p.slot[first], p.rows, p.status);
+            float dot = r >= 0 ? grad_row<LOADS>(p, first, r, p.w[first], threadIdx.x * 8, 8 * THREADS) : 0.f;
+            __syncthreads();  // (the sums of the pair before have been read)
+            if (lane == 0) sums[warp] = dot;
+            __syncthreads();
+            dot = 0.f;
+#pragma unroll
+            for (int v = 0; v < WARPS; ++v) dot += sums[v];
+            if (threadIdx.x == 0) p.dw[first] = dot;
         }
     }
 }
@@ -785,10 +801,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Columns of a unit: as many as leave units enough for the warps to even out. A
 // unit's start is a chain of two loads: 256 columns everywhere took 402 us for the
 // sum on the 671B rank, whole tokens everywhere 10.6 us for its 8 tokens; here 149
-// and 2.1.
+// and 2.1. Tokens of few choices are alike and need fewer units to even out (10539
+// tokens of 2728 columns, one row each: 33 us with 40000 units, 20.6 with 20000; the
+// sum on the 671B rank 149 / 158).
 int unit_columns(const TokenArgs& a) {
     int seg = 256;
-    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= (seg == 256 ? 20000 : 40000)) seg *= 2;
+    while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= (seg == 256 || a.top_k <= 2 ? 20000 : 40000)) seg *= 2;
     return seg;
 }
 
@@ -884,7 +902,7 @@ int launch_token_plan(const TokenPlanArgs& a) {
 
 int launch_token_dispatch(const TokenArgs& a) {
     const RowPar p = row_par(a, a.q ? unit_columns_mxfp8(a) : unit_columns(a));
-    return launch(a.q ? dispatch_mxfp8_kernel : dispatch_kernel, ceil_div(a.T * p.segs, WARPS) + p.pad_ctas, a, "dispatch kernel", p);
+    return launch(!a.q ? dispatch_kernel : a.H <= 512 ? dispatch_mxfp8_kernel<1> : dispatch_mxfp8_kernel<4>, ceil_div(a.T * p.segs, WARPS) + p.pad_ctas, a, "dispatch kernel", p);
 }
 
 int launch_token_combine(const TokenArgs& a) {
@@ -893,12 +911,16 @@ int launch_token_combine(const TokenArgs& a) {
 }
 
 int launch_token_combine_grad(const TokenArgs& a) {
-    const RowPar p = row_par(a, a.H);
+    RowPar p = row_par(a, a.H);
     const int64_t pairs = a.T * a.top_k, sms = a.num_sms;
     const auto go = [&](auto kernel, int per) { return launch(kernel, ceil_div(pairs, per) + p.pad_ctas, a, "combine gradient kernel", p); };
-    if (pairs <= 2 * sms) return go(combine_grad_kernel<TEAM>, 1);
-    if (2 * a.rows >= pairs || pairs <= PAIRS * 4 * sms) return go(combine_grad_kernel<WARP>, WARPS);
-    return go(combine_grad_kernel<LIST>, PAIRS);
+    if (pairs <= 2 * sms) return go(combine_grad_kernel<TEAM, 4>, 1);
+    if (a.H <= 2048 || 2 * a.rows >= pairs || pairs <= PAIRS * 4 * sms) {
+        p.each = 1;
+        while (p.each < 32 && 2 * p.each * a.H <= 8192 && pairs >= 16384 * static_cast<int64_t>(p.each)) p.each *= 2;
+        return go(a.H <= 256 ? combine_grad_kernel<WARP, 1> : combine_grad_kernel<WARP, 4>, WARPS * p.each);
+    }
+    return go(combine_grad_kernel<LIST, 8>, PAIRS);
 }
 
 }  // namespace mxw
