@@ -31,6 +31,10 @@
 //                 what. Last, when all tiles are done, the weighted sum over
 //                 each token's experts.
 //
+// Both may be resident while the kernel before the call still writes: they wait
+// for its end and then read the caller's tensors with plain loads and TMA, not with
+// ld.global.nc, which is for data that does not change while a kernel runs.
+//
 // Measured, bytes of the chosen experts' weights over the whole call's time:
 // 64 experts of H = 2048, I = 1408, top 6, all here: 64 tokens 571 MB in 112 us
 // (5.1 TB/s; DRAM reads are exactly the weights), 8 tokens 312 MB in 66 us, 1
@@ -154,7 +158,7 @@ __device__ __forceinline__ void split_rows(const Params& p, int first, int strid
     for (int i = first; i < p.T * per; i += stride) {
         const int t = i / per, b = i - t * per, h = b * STEP + 4 * lane;
         uint2 raw = make_uint2(0, 0);
-        if (h < p.H) raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.H + h));
+        if (h < p.H) raw = *reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.H + h);
         float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
                       __uint_as_float(raw.y & 0xFFFF0000u)};
         uint32_t s[PIECES];
@@ -218,13 +222,13 @@ __global__ void __launch_bounds__(256) moe_logits(const Params p) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int t = t0 + 16 * i + 8 * h + g;
-                a[i][h] = t < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + 32 * c + 8 * tg))
+                a[i][h] = t < p.T ? *reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + 32 * c + 8 * tg)
                                   : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
             const int e = e0 + 8 * j + g;
-            b[j] = e < p.experts ? __ldg(reinterpret_cast<const uint4*>(p.router + static_cast<size_t>(e) * p.H + 32 * c + 8 * tg))
+            b[j] = e < p.experts ? *reinterpret_cast<const uint4*>(p.router + static_cast<size_t>(e) * p.H + 32 * c + 8 * tg)
                                  : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                          : (h >> 1) * p.I + min(b.g.rt * (TILE / 2) + 32 * (h & 1) + lane, p.I - 1);
                 const size_t at = (base + wr) * K32 + 4 * k;
                 if (((K32 | static_cast<int>(reinterpret_cast<uintptr_t>(plane))) & 7) == 0) {  // (the planes: 4-byte aligned)
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(plane + at));
+                    const uint2 u = *reinterpret_cast<const uint2*>(plane + at);
                     v[h][0] = u.x; v[h][1] = u.y;
                 } else {
                     // rows of any length: aligned words, shifted together (the plane
@@ -809,7 +813,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t u[BLOCK + 1];
 #pragma unroll
                     for (int i = 0; i <= BLOCK; ++i)
-                        u[i] = i <= nw && w0 + 4 * i < end ? __ldg(reinterpret_cast<const uint32_t*>(plane + w0) + i) : 0u;
+                        u[i] = i <= nw && w0 + 4 * i < end ? reinterpret_cast<const uint32_t*>(plane + w0)[i] : 0u;
 #pragma unroll
                     for (int i = 0; i < BLOCK; ++i) v[h][i] = __funnelshift_r(u[i], u[i + 1], static_cast<uint32_t>(at & 3) * 8);
                 }

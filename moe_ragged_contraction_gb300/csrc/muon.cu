@@ -105,13 +105,16 @@ __device__ __forceinline__ float2 bf16x2_f(uint32_t v) {
 }
 
 // Four values of u at element i (a multiple of 4); FIRST also updates the momentum.
+// Plain loads: this grid may be resident while the kernel before it writes the
+// gradient (a clipping in place, say), and ld.global.nc is for data that does not
+// change while a kernel runs.
 template <bool FIRST>
 __device__ __forceinline__ float4 load_u(const MuonArgs& a, size_t i) {
     float4 g;
     if (a.grad_f32) {
-        g = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i));
+        g = *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i);
     } else {
-        const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i));
+        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i);
         const float2 lo = bf16x2_f(r.x), hi = bf16x2_f(r.y);
         g = make_float4(lo.x, lo.y, hi.x, hi.y);
     }

@@ -113,10 +113,12 @@ struct Small {
     int m, n, w, C, tall;
 };
 
-// Four values of the gradient from element i on (a multiple of 4).
+// Four values of the gradient from element i on (a multiple of 4). Plain loads: the
+// kernel before may write it while this grid is resident, and ld.global.nc is for
+// data that does not change while a kernel runs.
 __device__ __forceinline__ float4 load_grad(const MuonArgs& a, size_t i) {
-    if (a.grad_f32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i));
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i));
+    if (a.grad_f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + i);
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.grad) + i);
     return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
                        __uint_as_float(r.y & 0xFFFF0000u));
 }
