@@ -677,6 +677,8 @@ struct Item {
 // one expert consecutive, N-side tiles fastest; plan entries per expert.
 // Mode 1 (grouped GEMM): item = (row tile, N-side tile), N-side fastest; the
 // plan holds one entry per row tile: (expert, first row, end of the expert's rows).
+// Plain loads: the grid is resident while the prep kernel writes the plan, and
+// ld.global.nc is for data that does not change while a kernel runs.
 __device__ __forceinline__ Item load_item(const MainParams& p, long long i) {
     Item it;
     if (p.mode == 0) {
@@ -685,7 +687,7 @@ __device__ __forceinline__ Item load_item(const MainParams& p, long long i) {
         const int ntpe = p.tiles_m * p.tiles_n;
         const int r = static_cast<int>(i / ntpe);
         const int t = static_cast<int>(i - static_cast<long long>(r) * ntpe);
-        it.g = __ldg(order + r);
+        it.g = order[r];
         if (p.m_fastest) {
             it.tn = t / p.tiles_m;
             it.tm = t - it.tn * p.tiles_m;
@@ -693,16 +695,16 @@ __device__ __forceinline__ Item load_item(const MainParams& p, long long i) {
             it.tm = t / p.tiles_n;
             it.tn = t - it.tm * p.tiles_n;
         }
-        const int start = __ldg(ex + 4 * it.g + 0);
-        const int len = __ldg(ex + 4 * it.g + 1);
+        const int start = ex[4 * it.g + 0];
+        const int len = ex[4 * it.g + 1];
         // grid K-steps start at the run's 128-token grid step; its leading
         // chunks belong to the run before and are skipped
         const int lead = p.grid ? (start & (BK - 1)) : 0;
         it.start = start - lead;
         it.len = len + lead;
         it.kk0 = lead >> 5;
-        it.nsteps = __ldg(ex + 4 * it.g + 2);
-        const int sb = __ldg(ex + 4 * it.g + 3);
+        it.nsteps = ex[4 * it.g + 2];
+        const int sb = ex[4 * it.g + 3];
         it.m0 = it.tm * (2 * BM);
         it.m_end = p.kn ? p.K : p.N;
         it.sfm = (it.tm * p.ts_max + sb) * 2;
@@ -712,7 +714,7 @@ __device__ __forceinline__ Item load_item(const MainParams& p, long long i) {
     } else {
         const int mt = static_cast<int>(i / p.tiles_n);
         it.tn = static_cast<int>(i - static_cast<long long>(mt) * p.tiles_n);
-        const int4 e = __ldg(reinterpret_cast<const int4*>(p.plan + PLAN_HDR) + mt);
+        const int4 e = reinterpret_cast<const int4*>(p.plan + PLAN_HDR)[mt];
         it.g = e.x;
         it.tm = mt;
         it.m0 = e.y;
@@ -974,7 +976,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MAIN_THREADS, 1)
     // mode 1: the number of row tiles depends on the routing; the plan holds the item count
     const int nt_per_expert = p.tiles_m * p.tiles_n;
     const long long total =
-        p.mode == 0 ? static_cast<long long>(p.E) * nt_per_expert : static_cast<long long>(__ldg(p.plan));
+        p.mode == 0 ? static_cast<long long>(p.E) * nt_per_expert : static_cast<long long>(p.plan[0]);
     const int G = gridDim.x / 2, pair = blockIdx.x / 2;
 
     if (warp == 0) {

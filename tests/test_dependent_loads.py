@@ -30,6 +30,15 @@ def test_no_loads_of_constant_data(name):
         assert word not in text, word
 
 
+def test_no_loads_of_constant_data_in_the_main_contraction():
+    """wgrad_main starts beside the prep kernel that writes its plan. (The prep kernels start after all work before them.)"""
+    text = code("wgrad_kernels.cu")
+    main = text[text.index("Item load_item("):text.index("long long item_index(")] + text[text.index("struct ItemStream {"):text.index("cudaError_t launch_main(")]
+    assert main.count("__global__") == 1 and "griddep_wait();" in main
+    for word in ("__ldg", "ld.global.nc", "__restrict__"):
+        assert word not in main, word
+
+
 @pytest.fixture
 def rand():
     if not torch.cuda.is_available():
