@@ -92,7 +92,10 @@ extern "C" {
  * Scratch space (the scale re-layout and the schedule) comes from a cache the
  * library keeps per (device, stream), grown with stream-ordered allocation and
  * reused across calls; calls on one stream are ordered, so they never share
- * scratch concurrently. While `stream` is being captured into a CUDA graph the
+ * scratch concurrently. Several host threads may call on one stream: a call holds
+ * a lock of the (device, stream) until its last launch is enqueued, so that no
+ * other call's launches come between its own. (A workspace of the caller's, in the
+ * _ws forms, has no such lock: one thread at a time.) While `stream` is being captured into a CUDA graph the
  * cache does not grow: a call needing more scratch than the stream already
  * holds returns MXFP8_ENOWS (with a message) and records nothing, so make the
  * same call once on that stream before capturing, or use
@@ -291,7 +294,7 @@ int mxfp8_device_status(int32_t* status, int clear);
  * the last call left in it (each call rewrites all the scratch it reads, so
  * nothing needs clearing): calls whose work overlaps on the GPU (different
  * streams, no ordering between them) race on it and must be avoided by the
- * caller.
+ * caller. Calls of several host threads on one stream are kept apart here.
  */
 int mxfp8_wgrad_grouped_noalloc(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB,
                                 const int32_t* offs, int E, int N, int K, int64_t M, uint16_t* out,

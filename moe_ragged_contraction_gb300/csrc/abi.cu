@@ -172,15 +172,17 @@ struct StreamOrdered {
     }
 };
 mxw::ScratchCache<cudaStream_t, StreamOrdered> g_ws;
+mxw::StreamLocks<cudaStream_t> g_launches;
 
-int cached_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
+int cached_workspace(int dev, cudaStream_t stream, size_t need, void** out, mxw::LaunchLock* launches) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t ec = cudaStreamIsCapturing(stream, &cap);
     if (ec != cudaSuccess) return fail_cuda(ec, "cudaStreamIsCapturing");
     StreamOrdered alloc;
     int e = 0;
     mxw::Scratch r;
-    try {  // (the list of blocks may have to grow)
+    try {  // (the lists of blocks and of mutexes may have to grow)
+        *launches = g_launches.hold(dev, stream);
         std::lock_guard<std::mutex> lk(g_mu);
         r = g_ws.get(alloc, dev, stream, need, cap != cudaStreamCaptureStatusNone, out, &e);
     } catch (...) {
@@ -339,8 +341,9 @@ int run(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB
         }
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    mxw::LaunchLock launches;
     if (use_cache) {
-        rc = cached_workspace(dev, st, lay.total, &ws);
+        rc = cached_workspace(dev, st, lay.total, &ws, &launches);
         if (rc) return rc;
     }
     // M side: 256-row pair tiles, 128 rows per CTA; N side: tn-row tiles, per CTA
@@ -405,8 +408,8 @@ int mxw::host_device(int* dev, int* sms) {
     return rc;
 }
 
-int mxw::host_workspace(int dev, cudaStream_t stream, size_t need, void** out) {
-    return cached_workspace(dev, stream, need, out);
+int mxw::host_workspace(int dev, cudaStream_t stream, size_t need, void** out, LaunchLock* launches) {
+    return cached_workspace(dev, stream, need, out, launches);
 }
 
 uint64_t mxw::host_wait_limit_ns() { return wait_limit_ns(); }
@@ -550,7 +553,8 @@ int mxfp8_grouped_gemm(const uint8_t* X, const uint8_t* sX, const uint8_t* W, co
     g_ev_before = g_ev_after = nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    rc = cached_workspace(dev, st, lay.total, &ws);
+    mxw::LaunchLock launches;
+    rc = cached_workspace(dev, st, lay.total, &ws, &launches);
     if (rc) return rc;
     // X: 256-row tiles, 128 rows per CTA; W as [E][N][K]: per CTA n1/2 rows for the
     // first MMA and n2/2 for the second

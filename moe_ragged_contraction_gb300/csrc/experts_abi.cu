@@ -50,8 +50,9 @@ int moe(const uint16_t* x, int T, const uint16_t* router, const float* bias, con
     if (rc) return rc;
     if (a.num_sms > MAX_SMS) a.num_sms = MAX_SMS;
     a.stream = static_cast<cudaStream_t>(stream);
+    mxw::LaunchLock launches;
     if (use_cache) {
-        rc = mxw::host_workspace(a.dev, a.stream, need, &ws);
+        rc = mxw::host_workspace(a.dev, a.stream, need, &ws, &launches);
         if (rc) return rc;
     }
     a.x = x; a.router = router; a.bias = bias; a.w13 = w13; a.s13 = s13; a.w2 = w2; a.s2 = s2;
@@ -152,8 +153,9 @@ int muon(const void* grad, int grad_type, float* momentum, int E, int N, int K, 
     int rc = mxw::host_device(&a.dev, &a.num_sms);
     if (rc) return rc;
     a.stream = static_cast<cudaStream_t>(stream);
+    mxw::LaunchLock launches;
     if (use_cache && !small) {
-        rc = mxw::host_workspace(a.dev, a.stream, need, &ws);
+        rc = mxw::host_workspace(a.dev, a.stream, need, &ws, &launches);
         if (rc) return rc;
     }
     a.grad = grad; a.grad_f32 = grad_type == MXFP8_GRAD_F32; a.momentum = momentum;

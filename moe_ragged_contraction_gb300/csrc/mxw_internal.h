@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace mxw {
 
 // A CTA pair owns a 256 x TN output tile (TN <= MAX_TN); the token axis is
@@ -151,10 +153,12 @@ cudaError_t device_status_address(int dev, int** addr);
 // Host services of abi.cu shared by the other entry points: sets the message
 // of mxfp8_last_error() and returns `code`; checks the current device (sm_103)
 // and reports its index and SM count; scratch from the per-(device, stream)
-// cache; the limit of the kernels' waits; the tensor-map encoder.
+// cache, with the lock that the caller keeps until it has enqueued its last launch
+// (calls of several threads on a stream otherwise mix their launches); the limit of the kernels' waits; the tensor-map encoder.
 int host_fail(int code, const char* fmt, ...);
 int host_device(int* dev, int* sms);
-int host_workspace(int dev, cudaStream_t stream, size_t need, void** out);
+using LaunchLock = std::unique_lock<std::mutex>;
+int host_workspace(int dev, cudaStream_t stream, size_t need, void** out, LaunchLock* launches);
 uint64_t host_wait_limit_ns();
 int host_take_stall();  // the failure-path test hook, taken by this call
 int host_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,

@@ -35,7 +35,7 @@ struct CtxScratch {
     CUcontext ctx;
     void* ptr;
 };
-std::mutex g_noalloc_mu;
+std::mutex g_noalloc_mu, g_noalloc_launches;
 CtxScratch g_noalloc_cache[64] = {};
 int g_noalloc_used = 0;
 PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
@@ -107,5 +107,7 @@ extern "C" int mxfp8_wgrad_grouped_noalloc(const uint8_t* A, const uint8_t* sA, 
     void* scratch = nullptr;
     const int rc = scratch_in_current_context(&scratch);
     if (rc != MXFP8_OK) return rc;
+    // (the call's two launches hand over through the array: another thread's must not come between)
+    std::lock_guard<std::mutex> launches(g_noalloc_launches);
     return mxfp8_wgrad_grouped_ws(A, sA, B, sB, offs, E, N, K, M, out, scratch, MXFP8_NOALLOC_SCRATCH_BYTES, stream);
 }

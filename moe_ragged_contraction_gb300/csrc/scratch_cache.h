@@ -4,6 +4,8 @@
 
 #include <stddef.h>
 
+#include <deque>
+#include <mutex>
 #include <vector>
 
 namespace mxw {
@@ -63,6 +65,33 @@ class ScratchCache {
         return nullptr;
     }
     std::vector<Block> blocks_;
+};
+
+// One mutex for each (device, stream). A call holds it from the lookup of its scratch
+// until its last launch is enqueued: its launches hand over through that scratch,
+// so those of another thread's call on the stream must not come between them, nor
+// may that call's lookup release the block before they are enqueued.
+template <class Stream>
+class StreamLocks {
+   public:
+    std::unique_lock<std::mutex> hold(int dev, Stream stream) { return std::unique_lock<std::mutex>(of(dev, stream)); }
+
+   private:
+    struct Entry {
+        Entry(int d, Stream s) : dev(d), stream(s) {}
+        int dev;
+        Stream stream;
+        std::mutex mu;
+    };
+    std::mutex& of(int dev, Stream stream) {
+        std::lock_guard<std::mutex> lk(mu_);
+        for (Entry& e : entries_)
+            if (e.dev == dev && e.stream == stream) return e.mu;
+        entries_.emplace_back(dev, stream);
+        return entries_.back().mu;  // (a deque's elements stay where they are)
+    }
+    std::mutex mu_;
+    std::deque<Entry> entries_;
 };
 
 }  // namespace mxw

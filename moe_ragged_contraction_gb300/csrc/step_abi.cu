@@ -125,8 +125,9 @@ int grads(const void* const* g, const int64_t* sizes, const int32_t* types, int 
     int rc = mxw::host_device(&dev, &a.num_sms);
     if (rc) return rc;
     a.stream = static_cast<cudaStream_t>(stream);
+    mxw::LaunchLock launches;
     if (use_cache) {
-        rc = mxw::host_workspace(dev, a.stream, need, &ws);
+        rc = mxw::host_workspace(dev, a.stream, need, &ws, &launches);
         if (rc) return rc;
     }
     a.grads = g; a.sizes = sizes; a.types = types; a.outs = outs; a.n = n;
