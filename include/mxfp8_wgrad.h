@@ -95,7 +95,8 @@ extern "C" {
  * scratch concurrently. Several host threads may call on one stream: a call holds
  * a lock of the (device, stream) until its last launch is enqueued, so that no
  * other call's launches come between its own. (A workspace of the caller's, in the
- * _ws forms, has no such lock: one thread at a time.) While `stream` is being captured into a CUDA graph the
+ * _ws forms, has no such lock: one thread at a time.) cudaStreamPerThread stands for
+ * a stream of each thread's own: each has its own scratch, kept when the thread ends. While `stream` is being captured into a CUDA graph the
  * cache does not grow: a call needing more scratch than the stream already
  * holds returns MXFP8_ENOWS (with a message) and records nothing, so make the
  * same call once on that stream before capturing, or use

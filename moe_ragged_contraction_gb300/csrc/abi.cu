@@ -159,32 +159,46 @@ int make_sf_map(CUtensorMap* map, const uint8_t* base, int64_t blocks, int box_b
     return MXFP8_OK;
 }
 
+// A stream as the cache knows it. cudaStreamPerThread is one handle for as many
+// streams as there are threads, whose work is not ordered: the stream's own number
+// tells them apart. Every other handle is one stream.
+struct StreamKey {
+    cudaStream_t handle;
+    unsigned long long number;
+    bool operator==(const StreamKey& o) const { return handle == o.handle && number == o.number; }
+};
+
 // Scratch from the per-(device, stream) cache, by stream-ordered allocation.
 struct StreamOrdered {
     const char* what = "";
-    int allocate(void** p, size_t bytes, cudaStream_t s) {
+    int allocate(void** p, size_t bytes, const StreamKey& s) {
         what = "cudaMallocAsync (workspace)";
-        return cudaMallocAsync(p, bytes, s);
+        return cudaMallocAsync(p, bytes, s.handle);
     }
-    int release(void* p, cudaStream_t s) {
+    int release(void* p, const StreamKey& s) {
         what = "cudaFreeAsync (workspace)";
-        return cudaFreeAsync(p, s);
+        return cudaFreeAsync(p, s.handle);
     }
 };
-mxw::ScratchCache<cudaStream_t, StreamOrdered> g_ws;
-mxw::StreamLocks<cudaStream_t> g_launches;
+mxw::ScratchCache<StreamKey, StreamOrdered> g_ws;
+mxw::StreamLocks<StreamKey> g_launches;
 
 int cached_workspace(int dev, cudaStream_t stream, size_t need, void** out, mxw::LaunchLock* launches) {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t ec = cudaStreamIsCapturing(stream, &cap);
     if (ec != cudaSuccess) return fail_cuda(ec, "cudaStreamIsCapturing");
+    StreamKey key{stream, 0};
+    if (stream == cudaStreamPerThread) {
+        ec = cudaStreamGetId(stream, &key.number);
+        if (ec != cudaSuccess) return fail_cuda(ec, "cudaStreamGetId");
+    }
     StreamOrdered alloc;
     int e = 0;
     mxw::Scratch r;
     try {  // (the lists of blocks and of mutexes may have to grow)
-        *launches = g_launches.hold(dev, stream);
+        *launches = g_launches.hold(dev, key);
         std::lock_guard<std::mutex> lk(g_mu);
-        r = g_ws.get(alloc, dev, stream, need, cap != cudaStreamCaptureStatusNone, out, &e);
+        r = g_ws.get(alloc, dev, key, need, cap != cudaStreamCaptureStatusNone, out, &e);
     } catch (...) {
         return fail(MXFP8_ECUDA, "no host memory for the list of scratch blocks");
     }

@@ -184,6 +184,46 @@ def test_products_updates_and_layers_of_several_threads_on_one_stream(gen):
     check(calls)
 
 
+def test_per_thread_streams_are_told_apart():
+    """cudaStreamPerThread is one handle for a stream of each thread: the cache asks for the stream's number."""
+    with open(os.path.join(CSRC, "abi.cu")) as f:
+        text = f.read()
+    assert "stream == cudaStreamPerThread" in text and "cudaStreamGetId(stream, &key.number)" in text
+    assert "ScratchCache<cudaStream_t" not in text and "StreamLocks<cudaStream_t" not in text
+
+
+@pytest.mark.gpu
+def test_per_thread_streams(gen):
+    """Updates of different threads on their own default streams, at once: as many scratch blocks."""
+    stream = torch.cuda.ExternalStream(2)  # cudaStreamPerThread
+    grads = [torch.randn((2, 264 + 8 * i, 520), generator=gen, device="cuda") for i in range(4)]
+    want = [mx.muon_update(g) for g in grads]
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in want]
+    norms = [[torch.empty((), device="cuda") for _ in range(20)] for _ in grads]
+    total = [mx.grad_norm([g]) for g in grads]
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(len(grads)), []
+
+    def work(i):
+        try:
+            start.wait()
+            for o, n in zip(outs[i], norms[i]):
+                mx.muon_update(grads[i], out=o, stream=stream)
+                mx.grad_norm([grads[i]], out=n, stream=stream)
+        except Exception as e:  # noqa: BLE001 (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(grads))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for w, mine, n, norm in zip(want, outs, total, norms):
+        assert all(torch.equal(o, w) for o in mine) and all(float(v) == float(n) for v in norm)
+
+
 @pytest.mark.gpu
 def test_entry_without_allocation_of_several_threads(gen):
     import ctypes
