@@ -6,7 +6,7 @@ and the whole expert layer for a few tokens.
 have to be ready there, and an output that the call allocates belongs to it:
 order its use on other streams as with any tensor of another stream. Neither
 operator has a backward pass: tensors that require a gradient are refused while
-gradients are being recorded."""
+gradients are being recorded, and tensors with a forward-mode tangent."""
 from __future__ import annotations
 
 from operator import index
@@ -43,6 +43,14 @@ def _check(t, dtype, shape, name, device):
 def _refuse_gradients(**tensors):
     names = [name for name, t in tensors.items() if t is not None and t.requires_grad]
     raise ValueError(f"{', '.join(names)} requires a gradient, which this operator does not have: detach it or call under torch.no_grad()")
+
+
+def _refuse_tangents(tensors):
+    """tensors: pairs of a name and a tensor or None. (Called inside torch.autograd.forward_ad.dual_level.)"""
+    unpack = _torch.autograd.forward_ad.unpack_dual
+    for name, t in tensors:
+        if t is not None and unpack(t).tangent is not None:
+            raise ValueError(f"{name} has a forward-mode tangent, which this operator would lose: detach it")
 
 
 def _int32(v, name):
@@ -119,6 +127,8 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     if (x.requires_grad or router.requires_grad or out.requires_grad or (bias is not None and bias.requires_grad)
             or (topk_weights is not None and topk_weights.requires_grad)) and torch.is_grad_enabled():
         _refuse_gradients(x=x, router=router, bias=bias, out=out, topk_weights=topk_weights)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _refuse_tangents((("x", x), ("router", router), ("bias", bias), ("out", out), ("topk_weights", topk_weights)))
     lib = _lib._lib or _lib.load()
     args = (x.data_ptr(), T, router.data_ptr(), bias_p, w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
             experts, first_expert, local, H, I, top_k, _SCORES[score], 1 if renormalize else 0, scale, out.data_ptr(),
@@ -174,6 +184,8 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
         _check(out, torch.bfloat16, shape, "out", device)
     if (grad.requires_grad or out.requires_grad or (momentum is not None and momentum.requires_grad)) and torch.is_grad_enabled():
         _refuse_gradients(grad=grad, momentum=momentum, out=out)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _refuse_tangents((("grad", grad), ("momentum", momentum), ("out", out)))
     a, b, c = coeffs
     lib = _lib._lib or _lib.load()
     args = (grad.data_ptr(), 0 if dtype is torch.bfloat16 else 1, momentum_p, E, N, K, mu, 1 if nesterov else 0, steps,

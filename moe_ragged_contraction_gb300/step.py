@@ -5,7 +5,8 @@ norm and clipping of gradients.
 
 ``stream``: as in moe_layer and muon_update. The gradients are operators of
 their own (token_dispatch_grad, token_combine_grad): tensors that require a
-gradient are refused while gradients are being recorded."""
+gradient are refused while gradients are being recorded, and tensors with a
+forward-mode tangent."""
 from __future__ import annotations
 
 from array import array
@@ -122,6 +123,8 @@ def token_dispatch(x, plan, *, out=None, stream=None):
         _check(out, torch.bfloat16, (rows, H), "out", device)
     if (x.requires_grad or out.requires_grad) and torch.is_grad_enabled():
         _experts._refuse_gradients(x=x, out=out)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((("x", x), ("out", out)))
     rc = lib.mxfp8_token_dispatch(x.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows, out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -146,6 +149,8 @@ def token_dispatch_mxfp8(x, plan, *, q=None, s=None, stream=None):
         _check(s, u8, (rows, H // 32), "s", device)
     if x.requires_grad and torch.is_grad_enabled():
         _experts._refuse_gradients(x=x)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((("x", x),))
     rc = lib.mxfp8_token_dispatch_mxfp8(x.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows, q.data_ptr(), s.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -165,6 +170,8 @@ def token_dispatch_grad(dxs, plan, *, out=None, stream=None):
         _check(out, torch.bfloat16, (T, H), "out", device)
     if (dxs.requires_grad or out.requires_grad) and torch.is_grad_enabled():
         _experts._refuse_gradients(dxs=dxs, out=out)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((("dxs", dxs), ("out", out)))
     rc = lib.mxfp8_token_dispatch_grad(dxs.data_ptr(), rows, T, H, k, slot.data_ptr(), out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -185,6 +192,8 @@ def token_combine(y, weights, plan, *, out=None, stream=None):
         _check(out, torch.bfloat16, (T, H), "out", device)
     if (y.requires_grad or weights.requires_grad or out.requires_grad) and torch.is_grad_enabled():
         _experts._refuse_gradients(y=y, weights=weights, out=out)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((("y", y), ("weights", weights), ("out", out)))
     rc = lib.mxfp8_token_combine(y.data_ptr(), rows, weights.data_ptr(), T, H, k, slot.data_ptr(), out.data_ptr(), st)
     if rc:
         _lib.check(rc)
@@ -212,6 +221,8 @@ def token_combine_grad(dout, y, weights, plan, *, dy=None, dweights=None, stream
         _check(dweights, f32, (T, k), "dweights", device)
     if (dout.requires_grad or y.requires_grad or weights.requires_grad or dy.requires_grad or dweights.requires_grad) and torch.is_grad_enabled():
         _experts._refuse_gradients(dout=dout, y=y, weights=weights, dy=dy, dweights=dweights)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((("dout", dout), ("y", y), ("weights", weights), ("dy", dy), ("dweights", dweights)))
     rc = lib.mxfp8_token_combine_grad(dout.data_ptr(), y.data_ptr(), weights.data_ptr(), T, H, k, slot.data_ptr(), src.data_ptr(), rows,
                                       dy.data_ptr(), dweights.data_ptr(), st)
     if rc:
@@ -289,6 +300,8 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
         _check(out, torch.float32, (), "out", device)
     if torch.is_grad_enabled() and any(map(_requires_grad, (*grads, out))):
         _experts._refuse_gradients(grads=next((t for t in grads if t.requires_grad), None), out=out)
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((*(("grads", t) for t in grads), ("out", out)))
     end, rest = _workspace(torch, workspace, device, st)
     rc = getattr(lib, "mxfp8_grad_norm" + end)(_address(ptrs), _address(sizes), _address(types), len(grads), out.data_ptr(), *rest)
     if rc:
@@ -315,6 +328,8 @@ def clip_grads(grads, max_norm, *, norm=None, eps=1e-6, out=None, workspace=None
     if torch.is_grad_enabled() and any(map(_requires_grad, (*grads, *(out or ())))):
         _experts._refuse_gradients(grads=next((t for t in grads if t.requires_grad), None),
                                    out=next((t for t in out or () if t.requires_grad), None))
+    if torch.autograd.forward_ad._current_level >= 0:
+        _experts._refuse_tangents((*(("grads", t) for t in grads), *(("out", t) for t in out or ()), ("norm", norm)))
     known = None
     if norm is None:
         norm = _new(stream, (), torch.float32, grads[0])
