@@ -176,6 +176,13 @@ def _expect(t, dtype, name, device=True):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _in_range(**sizes):
+    """Raises unless the library's 32-bit arguments hold the sizes (ctypes would take them modulo 2^32)."""
+    for name, v in sizes.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name}={v} is out of range")
+
+
 def wgrad_grouped(A, sA, B, sB, offs, out=None, workspace=None, stream=None):
     """dW[g] = dY[g]^T X[g] for every expert (see include/mxfp8_wgrad.h).
 
@@ -191,6 +198,7 @@ def wgrad_grouped(A, sA, B, sB, offs, out=None, workspace=None, stream=None):
     N, M = A.shape
     K, M2 = B.shape
     E = offs.numel()
+    _in_range(N=N, K=K, E=E)
     if M2 != M or tuple(sA.shape) != (N, M // 32) or tuple(sB.shape) != (K, M // 32):
         raise ValueError("inconsistent operand / scale shapes")
     if out is None:
@@ -225,6 +233,7 @@ def grouped_gemm(X, sX, W, sW, offs, out=None, stream=None):
         _expect(t, dt, nm)
     M, K = X.shape
     E, N, K2 = W.shape
+    _in_range(E=E, N=N, K=K)
     if K2 != K or tuple(sX.shape) != (M, K // 32) or tuple(sW.shape) != (E, N, K // 32) or offs.numel() != E:
         raise ValueError("inconsistent operand / scale / offset shapes")
     if out is None:
@@ -238,6 +247,8 @@ def grouped_gemm(X, sX, W, sW, offs, out=None, stream=None):
 
 
 def workspace_bytes(E: int, N: int, K: int, M: int) -> int:
+    if any(not -0x80000000 <= v <= 0x7fffffff for v in (E, N, K)):
+        return 0
     return int(load().mxfp8_wgrad_workspace_bytes(E, N, K, M))
 
 
@@ -246,11 +257,13 @@ ORIENT_AUTO, ORIENT_NK, ORIENT_KN = 0, 1, 2
 
 def set_tile_orientation(mode: int) -> None:
     """Process-wide tile orientation: 0 automatic, 1 (256-row side on A), 2 (on B)."""
+    _in_range(mode=int(mode))
     check(load().mxfp8_wgrad_set_tile_orientation(int(mode)))
 
 
 def set_tile_rows(tn: int) -> None:
     """Process-wide N-side tile width: 0 for the modelled choice, else a multiple of 16 in [16, 448]."""
+    _in_range(tn=int(tn))
     check(load().mxfp8_wgrad_set_tile_rows(int(tn)))
 
 
@@ -259,11 +272,13 @@ STORE_AUTO, STORE_DIRECT = 0, 1
 
 def set_epilogue_store(mode: int) -> None:
     """Process-wide epilogue stores: 0 TMA stores where their staging fits, 1 direct stores only."""
+    _in_range(mode=int(mode))
     check(load().mxfp8_wgrad_set_epilogue_store(int(mode)))
 
 
 def tile_config(E: int, N: int, K: int, M: int) -> dict:
     """Tiling the current settings give for E experts, an [N, K] output and M tokens."""
+    _in_range(E=E, N=N, K=K)
     v = [ctypes.c_int(0) for _ in range(4)]
     check(load().mxfp8_wgrad_tile_config(E, N, K, M, *(ctypes.byref(x) for x in v)))
     kn, tn, tm, tnn = (int(x.value) for x in v)
@@ -272,6 +287,7 @@ def tile_config(E: int, N: int, K: int, M: int) -> dict:
 
 def grouped_gemm_tile_config(E: int, N: int, K: int, M: int) -> dict:
     """Tiling the grouped GEMM would use for X [M, K] and W [E, N, K] under the current settings."""
+    _in_range(E=E, N=N, K=K)
     v = [ctypes.c_int(0) for _ in range(3)]
     check(load().mxfp8_grouped_gemm_tile_config(E, N, K, M, *(ctypes.byref(x) for x in v)))
     tn, tm, tnn = (int(x.value) for x in v)
@@ -284,6 +300,7 @@ def quantize_tokenwise(x, q=None, s=None, stream=None):
 
     _expect(x, torch.float32, "x")
     R, M = x.shape
+    _in_range(R=R)
     if q is None:
         q = _empty(stream, (R, M), torch.uint8, x.device)
     if s is None:
@@ -301,6 +318,7 @@ def quantize_transpose_bf16(x, q=None, s=None, stream=None):
 
     _expect(x, torch.bfloat16, "x")
     M, R = x.shape
+    _in_range(R=R)
     if q is None:
         q = _empty(stream, (R, M), torch.uint8, x.device)
     if s is None:
@@ -315,6 +333,8 @@ def quantize_transpose_bf16(x, q=None, s=None, stream=None):
 
 def sf_blocks_bytes(R: int, M: int, tile_rows: int) -> int:
     """Bytes of the scale-factor blocks of an [R, M] operand cut into tiles of tile_rows rows (0 if invalid)."""
+    if any(not -0x80000000 <= v <= 0x7fffffff for v in (R, tile_rows)):
+        return 0
     return int(load().mxfp8_sf_blocks_bytes(R, M, tile_rows))
 
 
@@ -327,6 +347,7 @@ def quantize_transpose_bf16_sf(x, tile_rows, q=None, sf=None, s=None, stream=Non
 
     _expect(x, torch.bfloat16, "x")
     M, R = x.shape
+    _in_range(R=R, tile_rows=tile_rows)
     nbytes = sf_blocks_bytes(R, M, tile_rows)
     if nbytes == 0:
         raise ValueError(f"invalid sizes R={R}, M={M}, tile_rows={tile_rows}")
@@ -360,6 +381,7 @@ def wgrad_grouped_sf(A, sfA, B, sfB, offs, kn, tn, out=None, stream=None):
     N, M = A.shape
     K, M2 = B.shape
     E = offs.numel()
+    _in_range(N=N, K=K, E=E, kn=int(kn), tn=int(tn))
     rows_a, rows_b = (int(tn), 256) if kn else (256, int(tn))
     if M2 != M or sfA.numel() < sf_blocks_bytes(N, M, rows_a) or sfB.numel() < sf_blocks_bytes(K, M, rows_b):
         raise ValueError("inconsistent operand / scale-factor block sizes")

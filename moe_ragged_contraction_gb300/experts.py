@@ -101,6 +101,8 @@ def moe_layer(x, router, w13, s13, w2, s2, top_k, *, bias=None, first_expert=0, 
     experts = router.shape[0]
     local, I2 = w13.shape[:2]
     I = I2 // 2
+    if (T | H | experts | local | I2) >> 31:
+        raise ValueError(f"sizes out of range: T={T}, H={H}, experts={experts}, local={local}, I={I}")
     u8, bf16, f32 = torch.uint8, torch.bfloat16, torch.float32
     _check(x, bf16, (T, H), "x", device)
     _check(router, bf16, (experts, H), "router", device)
@@ -170,6 +172,8 @@ def muon_update(grad, momentum=None, *, mu=0.95, nesterov=True, steps=5, coeffs=
         E, (N, K) = 1, shape
     else:
         raise ValueError(f"grad must be [E, N, K] or [N, K], got {list(shape)}")
+    if (E | N | K) >> 31:
+        raise ValueError(f"sizes out of range: {list(shape)}")
     dtype = grad.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"grad must be torch.bfloat16 or torch.float32, got {dtype}")

@@ -59,7 +59,12 @@ def _plan(torch, plan, device):
         raise ValueError("plan must be a TokenPlan: offs [local], slot [T, top_k] and src [rows]")
     _check(slot, torch.int32, shape, "plan.slot", device)
     _check(src, torch.int32, rows, "plan.src", device)
-    return slot, src, shape[0], shape[1], rows[0]
+    return slot, src, shape[0], _int32(shape[1], "top_k"), rows[0]
+
+
+def _columns(t):
+    """H of a tensor [.., H]."""
+    return _int32(t.shape[-1], "H") if t.dim() else 0
 
 
 def token_plan_rows(T: int, top_k: int, local: int, align: int = 32) -> int:
@@ -89,7 +94,7 @@ def token_plan(ids, local, *, first_expert=0, align=32, rows=None, out=None, str
         raise ValueError(f"ids must be [T, top_k], got {list(ids.shape)}")
     _check(ids, ids.dtype, ids.shape, "ids", device)
     T, k = ids.shape
-    local, first_expert, align = _int32(local, "local"), _int32(first_expert, "first_expert"), _int32(align, "align")
+    k, local, first_expert, align = _int32(k, "top_k"), _int32(local, "local"), _int32(first_expert, "first_expert"), _int32(align, "align")
     i32 = torch.int32
     if rows is None:
         rows = token_plan_rows(T, k, local, align) if out is None else out[2].shape[0]
@@ -115,7 +120,7 @@ def token_dispatch(x, plan, *, out=None, stream=None):
     """Rows sorted by expert (see include/mxfp8_step.h): x bf16 [T, H] -> out bf16 [rows, H], zeros on padding rows."""
     torch, lib, device, st = _begin(x, "x", stream)
     slot, src, T, k, rows = _plan(torch, plan, device)
-    H = x.shape[-1] if x.dim() else 0
+    H = _columns(x)
     _check(x, torch.bfloat16, (T, H), "x", device)
     if out is None:
         out = _new(stream, (rows, H), torch.bfloat16, x)
@@ -136,7 +141,7 @@ def token_dispatch_mxfp8(x, plan, *, q=None, s=None, stream=None):
     x bf16 [T, H] -> (q uint8 [rows, H] E4M3, s uint8 [rows, H/32] E8M0)."""
     torch, lib, device, st = _begin(x, "x", stream)
     slot, src, T, k, rows = _plan(torch, plan, device)
-    H = x.shape[-1] if x.dim() else 0
+    H = _columns(x)
     _check(x, torch.bfloat16, (T, H), "x", device)
     u8 = torch.uint8
     if q is None:
@@ -162,7 +167,7 @@ def token_dispatch_grad(dxs, plan, *, out=None, stream=None):
     the sum of each token's rows."""
     torch, lib, device, st = _begin(dxs, "dxs", stream)
     slot, src, T, k, rows = _plan(torch, plan, device)
-    H = dxs.shape[-1] if dxs.dim() else 0
+    H = _columns(dxs)
     _check(dxs, torch.bfloat16, (rows, H), "dxs", device)
     if out is None:
         out = _new(stream, (T, H), torch.bfloat16, dxs)
@@ -183,7 +188,7 @@ def token_combine(y, weights, plan, *, out=None, stream=None):
     [T, top_k] -> out bf16 [T, H], the weighted sum of each token's rows."""
     torch, lib, device, st = _begin(y, "y", stream)
     slot, src, T, k, rows = _plan(torch, plan, device)
-    H = y.shape[-1] if y.dim() else 0
+    H = _columns(y)
     _check(y, torch.bfloat16, (rows, H), "y", device)
     _check(weights, torch.float32, (T, k), "weights", device)
     if out is None:
@@ -206,7 +211,7 @@ def token_combine_grad(dout, y, weights, plan, *, dy=None, dweights=None, stream
     dy may be y."""
     torch, lib, device, st = _begin(dout, "dout", stream)
     slot, src, T, k, rows = _plan(torch, plan, device)
-    H = dout.shape[-1] if dout.dim() else 0
+    H = _columns(dout)
     bf16, f32 = torch.bfloat16, torch.float32
     _check(dout, bf16, (T, H), "dout", device)
     _check(y, bf16, (rows, H), "y", device)
