@@ -9,7 +9,7 @@ namespace mxw {
 
 struct TokenPlanArgs {
     const void* ids;
-    int id64, top_k, first, local, align;
+    int id64, first, local, align;
     int64_t pairs, rows;
     int32_t *offs, *slot, *src;
     int dev;

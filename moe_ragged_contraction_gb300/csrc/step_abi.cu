@@ -164,7 +164,7 @@ int mxfp8_token_plan(const void* ids, int id_type, int64_t T, int top_k, int fir
     mxw::TokenPlanArgs a{};
     if (!rc) rc = device(&a.dev, &sms, &a.status);
     if (rc) return rc;
-    a.ids = ids; a.id64 = id_type == MXFP8_ID_I64; a.top_k = top_k; a.first = first; a.local = local; a.align = align;
+    a.ids = ids; a.id64 = id_type == MXFP8_ID_I64; a.first = first; a.local = local; a.align = align;
     a.pairs = T * top_k; a.rows = rows; a.offs = offs; a.slot = slot; a.src = src;
     a.stream = static_cast<cudaStream_t>(stream);
     return mxw::launch_token_plan(a);

@@ -59,12 +59,17 @@ def _plan(torch, plan, device):
         raise ValueError("plan must be a TokenPlan: offs [local], slot [T, top_k] and src [rows]")
     _check(slot, torch.int32, shape, "plan.slot", device)
     _check(src, torch.int32, rows, "plan.src", device)
-    return slot, src, shape[0], _int32(shape[1], "top_k"), rows[0]
+    if shape[1] >> 31:
+        raise ValueError(f"top_k={shape[1]} is out of range")
+    return slot, src, shape[0], shape[1], rows[0]
 
 
 def _columns(t):
     """H of a tensor [.., H]."""
-    return _int32(t.shape[-1], "H") if t.dim() else 0
+    H = t.shape[-1] if t.dim() else 0
+    if H >> 31:
+        raise ValueError(f"H={H} is out of range")
+    return H
 
 
 def token_plan_rows(T: int, top_k: int, local: int, align: int = 32) -> int:
