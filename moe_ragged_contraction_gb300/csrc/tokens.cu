@@ -51,8 +51,8 @@ __device__ __forceinline__ uint4 load16_l1_if(bool there, const void* p) {
 // not talk to one another. Each CTA of a cluster has a part of the pairs, cut into
 // as many segments as there are clusters; the cluster of that number ranks the
 // pairs of the segment and gives them rows, and only counts those of the others:
-// counting takes a tenth of what ranking does, and no scratch or hand-over between
-// clusters is needed. In its segment every warp has a run of pairs and a row of
+// counting takes some 15 instructions for a warp's 32 pairs, ranking 60, and no
+// scratch or hand-over between clusters is needed. In its segment every warp has a run of pairs and a row of
 // counters in shared memory (no atomics); the warps' counts and, through
 // distributed shared memory, the CTAs' become starting rows.
 constexpr int PLAN_MAX_CTAS = 16;
@@ -310,8 +310,12 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanPar p) {
 
 // ------------------------------------------------------------------ rows
 
-// What bounds these kernels is DRAM: they have no arithmetic to speak of. A unit of
-// work is a warp's: some columns of a token, or a pair. CTAs of four warps: a CTA
+// What bounds these kernels is DRAM in calls of many tokens with some 1000 columns
+// or more (92% to 99% of the copy rate); with short rows it is what a unit takes
+// whatever its width: a chain of two loads, and lanes without columns (17613 tokens of
+// 96 columns to MXFP8: 12.8 us for 2.2 of bytes; sum of 54484 tokens of 240 columns:
+// 20.7 for 5.5). They have no arithmetic to speak of. A unit of work is a warp's: some columns of
+// a token, or a pair. CTAs of four warps: a CTA
 // lives as long as its longest unit, and tokens have from none to top_k rows here
 // (with eight warps: 16B dispatch 76.9 us against 74.1, combine on the 671B rank
 // 162 / 158, its gradient 225 / 220; with two 75.1, 157, 233).
@@ -626,7 +630,9 @@ __device__ __forceinline__ void combine_one(const RowPar& p, int64_t t, int seg,
 
 // The way by the number n of the token's rows, so that six to eight loads are in
 // flight at any n (one way with six rows: k = 8 53.3 us against 51.2; without the
-// way for one row: 671B rank 174 / 162). 16384 tokens, 6 rows of 2048 columns: 74
+// way for one row: 671B rank 174 / 162; without that of four rows of one vector in
+// units of 256 columns: 512 tokens, 4 rows of 2048 columns 3.6 / 3.1, 54484 tokens of
+// 240 columns 21.3 / 18.9). 16384 tokens, 6 rows of 2048 columns: 74
 // us, 6.3 TB/s.
 template <bool WEIGHTED>
 __global__ void __launch_bounds__(THREADS, 8) combine_kernel(const RowPar p) {
@@ -691,7 +697,9 @@ __device__ __forceinline__ float grad_row(const RowPar& p, int64_t pair, int64_t
 // The gradient of the weighted sum. How a CTA's warps take pairs:
 //   LIST   it lists those of PAIRS neighbouring pairs that have a row, a warp takes
 //          one at a time, LOADS = 8 loads of each of the two rows in flight: where
-//          most pairs have none (671B rank: 223 us, WARP 239)
+//          most pairs have none and rows more than 2048 columns (671B rank: 223 us, WARP
+//          239; 2560 columns 87 / 100. Shorter rows end sooner than a list pays: 1024
+//          columns 44, WARP 38; 512 38 / 25; at 1536 and 2048 LIST is 5% ahead)
 //   WARP   a warp a pair, 4 loads of each row in flight (1 for rows of up to 256
 //          columns), twice the warps: where most have one (16B: 137 us, LIST 143; 512 tokens 6.3 / 15). Several pairs
 //          (`each`) one after the other where rows are short, so that there are not
@@ -802,8 +810,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // unit's start is a chain of two loads: 256 columns everywhere took 402 us for the
 // sum on the 671B rank, whole tokens everywhere 10.6 us for its 8 tokens; here 149
 // and 2.1. Tokens of few choices are alike and need fewer units to even out (10539
-// tokens of 2728 columns, one row each: 33 us with 40000 units, 20.6 with 20000; the
-// sum on the 671B rank 149 / 158).
+// tokens of 2728 columns, one row each: 33 us with 40000 units, 20.6 with 20000; two
+// rows 37.7 / 34.9; 30000 of 4096 columns, two rows 112 / 114). With more choices it
+// depends: three rows of 2048 columns 49.1 / 45.1, of 4096 149 / 151, the sum on the 671B
+// rank 149 / 158.
 int unit_columns(const TokenArgs& a) {
     int seg = 256;
     while (seg < a.H && a.T * ceil_div(a.H, 2 * seg) >= (seg == 256 || a.top_k <= 2 ? 20000 : 40000)) seg *= 2;
@@ -873,6 +883,8 @@ int launch_token_plan(const TokenPlanArgs& a) {
     PlanPar p{a.ids, static_cast<int>(a.pairs), a.first, a.local, a.align, static_cast<int>(a.rows), 0, 1, 1, a.offs, a.slot, a.src, a.status};
     while ((1 << (3 * p.groups)) < a.local) ++p.groups;
     auto kernel = a.id64 ? token_plan_kernel<int64_t> : token_plan_kernel<int32_t>;
+    // (few of either: 8 warps start sooner. 2 pairs, 4 experts: 3.4 us, 4.3 with 32; 64 pairs, 32 experts 4.3 / 4.7;
+    // with more experts 32 clear and scan faster: 48 pairs, 64 experts 5.5 / 5.2; 64 pairs, 256 experts 8.3 / 6.7)
     int warps = a.pairs <= 64 && a.local <= 64 ? 8 : 32;
     const auto bytes = [&] { return (warps + 7) * static_cast<size_t>(a.local) * 4 + warps * RUN * 6; };
     while (bytes() > PLAN_SMEM) warps /= 2;
